@@ -84,6 +84,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gmm_fp8_int4_fwd.argtypes = [P, I, P, P, P, P, I64, I64, I64, I64, P, I, P, SZ, P]
     for name in EXPORTS[3:]:
         getattr(lib, name).restype = I
+    ffn._declare(lib)
     _lib = lib
     return lib
 
@@ -432,3 +433,8 @@ def gmm_bf16_dx(dy: torch.Tensor, w: torch.Tensor, group_sizes: torch.Tensor,
     _check(lib.gmm_bf16_dx(_ptr(dy), _ptr(w), _ptr(group_sizes), M, K, N, G, _ptr(out),
                            _dt(out), wsp, wsb, _stream(dy)))
     return out
+
+
+from . import ffn  # noqa: E402  (uses the helpers above)
+from .ffn import (FFN_EXPORTS, OP_BF16_SWIGLU, OP_BF16_SWIGLU_BWD, OP_TGMM_MX8,  # noqa: E402,F401
+                  gmm_bf16_swiglu, gmm_bf16_swiglu_bwd, gmm_dequantize_mx8, gmm_quantize_mx8, tgmm_mx8)

@@ -9,13 +9,15 @@
 #include <cstdio>
 #include <initializer_list>
 
-#include "../../include/gmm.h"
+#include "../../include/gmm_ffn.h"
+#include "gmm_check.hpp"
 #include "gmm_config.hpp"
 #include "gmm_launch.hpp"
 
-namespace {
+namespace gmm {
+namespace abi {
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 int fail(int status, const char* fmt, ...) {
     va_list ap;
@@ -25,54 +27,12 @@ int fail(int status, const char* fmt, ...) {
     return status;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace abi
+}  // namespace gmm
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+using namespace gmm::abi;
 
-int check_ptr(const void* p, const char* name) {
-    if (p == nullptr) return fail(GMM_ERR_NULL, "%s is NULL", name);
-    if (!aligned16(p)) return fail(GMM_ERR_ALIGN, "%s is not 16-byte aligned", name);
-    return GMM_OK;
-}
-
-int check_opt_ptr(const void* p, const char* name) {
-    if (p != nullptr && !aligned16(p)) return fail(GMM_ERR_ALIGN, "%s is not 16-byte aligned", name);
-    return GMM_OK;
-}
-
-int check_groups(int64_t M, int64_t G) {
-    if (M < 0 || M > kMaxDim) return fail(GMM_ERR_SHAPE, "M=%lld out of range", (long long)M);
-    if (G < 1 || G > GMM_MAX_GROUPS)
-        return fail(GMM_ERR_SHAPE, "G=%lld outside [1, %d]", (long long)G, GMM_MAX_GROUPS);
-    return GMM_OK;
-}
-
-int check_mult(int64_t v, int64_t mult, const char* name) {
-    if (v < mult || v > kMaxDim || v % mult != 0)
-        return fail(GMM_ERR_SHAPE, "%s=%lld must be a positive multiple of %lld", name,
-                    (long long)v, (long long)mult);
-    return GMM_OK;
-}
-
-int check_out_dtype(int dt, const char* name) {
-    if (dt != GMM_BF16 && dt != GMM_F32)
-        return fail(GMM_ERR_DTYPE, "%s dtype %d is not GMM_BF16 or GMM_F32", name, dt);
-    return GMM_OK;
-}
-
-// Bytes of the status block at the start of every workspace (word 0: the
-// device status of the last call that used it).
-constexpr size_t kWsStatusBytes = 256;
-
-int check_ws(const void* ws, size_t ws_bytes, size_t need) {
-    if (ws == nullptr || ws_bytes < need)
-        return fail(GMM_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed%s", ws == nullptr ? 0 : ws_bytes,
-                    need, ws == nullptr ? " (ws is NULL)" : "");
-    if (!aligned16(ws)) return fail(GMM_ERR_ALIGN, "ws is not 16-byte aligned");
-    return GMM_OK;
-}
-
-int32_t* ws_status(void* ws) { return reinterpret_cast<int32_t*>(ws); }
+namespace {
 
 // The tile configuration a call runs (the library's choice, or the override
 // a tile search set); an override that does not fit the shape is an error.
@@ -102,17 +62,6 @@ gmm_tile_config to_public(const gmm::TileConfig& c) {
     return o;
 }
 
-int hip_status(hipError_t e) {
-    if (e != hipSuccess) return fail(GMM_ERR_HIP, "HIP launch failed: %s", hipGetErrorString(e));
-    return GMM_OK;
-}
-
-#define GMM_TRY(expr)                 \
-    do {                              \
-        int _rc = (expr);             \
-        if (_rc != GMM_OK) return _rc; \
-    } while (0)
-
 }  // namespace
 
 extern "C" {
@@ -133,7 +82,7 @@ const char* gmm_status_string(int status) {
 const char* gmm_last_error(void) { return g_last_error; }
 
 size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G) {
-    (void)M; (void)K; (void)N; (void)G;
+    (void)K; (void)G;
     switch (op) {
         case GMM_OP_METADATA:
         case GMM_OP_FP8_FWD:
@@ -144,6 +93,11 @@ size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G) {
         case GMM_OP_DX:
         case GMM_OP_FP8_INT4_FWD:
             return kWsStatusBytes;
+        case GMM_OP_BF16_SWIGLU:
+        case GMM_OP_TGMM_MX8:
+            return kWsStatusBytes;
+        case GMM_OP_BF16_SWIGLU_BWD:   // and dP, bf16 [M,2N]
+            return kWsStatusBytes + (M > 0 && N > 0 ? (size_t)M * 4 * (size_t)N : 0);
         default:
             return 0;
     }

@@ -103,4 +103,42 @@ hipError_t launch_bf16_dx(const TileConfig& cfg, const void* dy, const void* w, 
 hipError_t launch_tgmm(const TileConfig& cfg, const void* x, const void* dy, const int32_t* group_sizes, int M, int K,
                        int N, int G, void* dw, bool out_bf16, int32_t* status, hipStream_t stream);
 
+constexpr int64_t kMx8BlockSize = 32;   // values that share a checkpoint scale
+
+// 8-bit checkpoints (gmm_mx8.hpp): codes [M,K] and E8M0 scales [M,K/32] of x,
+// and the values back.
+hipError_t launch_quantize_mx8(const void* x, bool x_bf16, int64_t M, int64_t K, uint8_t* q, uint8_t* scale,
+                               hipStream_t stream);
+hipError_t launch_dequantize_mx8(const uint8_t* q, const uint8_t* scale, int64_t M, int64_t K, void* out,
+                                 bool out_bf16, hipStream_t stream);
+
+// dP [M,2N] (bf16) of h = silu(gate) * up from dh [M,N] and P in bf16 (gu) or
+// as a checkpoint (gu_q, gu_s); h, when given, receives the recomputed h.
+hipError_t launch_gated_grad(const void* dh, const void* gu, const uint8_t* gu_q, const uint8_t* gu_s,
+                             const int32_t* group_sizes, int M, int N, int G, void* dgu, void* h,
+                             int32_t* status, hipStream_t stream);
+
+// Operands of the gated block's grouped products.  NN is the column count of
+// the second operand (2N for the fused gate and up weights).
+struct FfnArgs {
+    const uint16_t* a;                    // x [M,K], or dP [M,NN] for dx
+    const uint8_t *aq, *as;               // x as a checkpoint (the weight gradient; else NULL)
+    const uint16_t* b;                    // w [G,K,NN], or dP / dy [M,NN] for the weight gradient
+    const int32_t* group_sizes;
+    int M, K, NN, G;
+    void* out;                            // h [M,NN/2], dx [M,K] or dw [G,K,NN]
+    uint16_t* gu;                         // the forward's P, or NULL
+    uint8_t *gu_q, *gu_s;                 // the forward's P as a checkpoint, or NULL
+    int ntiles_c, ntiles_r, nblocks, placement;   // set by the launcher (placement: of tgmm_tile)
+    int32_t* status;
+};
+hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream);
+hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream);
+hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream);
+
+// Upper bounds of these launches' grids.
+int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G);
+int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G);
+int64_t ffn_dw_blocks(int64_t K, int64_t NN, int64_t G);
+
 }  // namespace gmm
