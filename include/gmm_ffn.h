@@ -12,7 +12,8 @@
  * nearest to v / 2^(c - 127), ties to even.  c is the smallest byte with
  * max|v| <= 448 * 2^(c - 127), 0 for an all-zero block; nothing saturates.
  * Codes are [M,K] bytes, scales [M,K/32] bytes: 8.25 bits a value.  A value
- * read back is exact in bf16.
+ * read back is exact in bf16 (magnitudes of 1.9375 * 2^127 and more round to
+ * 2^128 and read back as infinity).
  */
 #ifndef GMM_FFN_H_
 #define GMM_FFN_H_
