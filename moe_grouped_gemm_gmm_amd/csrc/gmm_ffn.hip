@@ -515,6 +515,238 @@ hipError_t launch(FfnArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------- few rows --
+// The gated forward for few rows per expert (a serving step): the work is
+// reading each busy expert's weights once, so the tile is TR = 16 MB rows by
+// CT gate + CT up columns, small enough that a handful of experts covers the
+// chip, and the workgroup's NW waves split K between them: wave v takes the
+// 32-deep slices v, v + NW, ...  Each wave feeds its own ring of S stages by
+// load-to-LDS and never meets the others before the end, so no barrier stands
+// in the stream of loads.  The partial sums meet in LDS, added in wave order.
+//
+// Stage layout: x as direct rows of 32; the weights as rows of CT gate and CT
+// up columns in 32-byte chunks, chunk k at k ^ key: the 8 rows that one pass
+// of a transposed read covers (0-3 and 8-11 of 16) fall on each bank once.
+//
+// What bounds it: a pass over one token's 8 experts (33 MB) takes 17.7 us, of
+// which 3.4 us are launch and prologue; a bare read of as many cold bytes
+// takes 10.4 us.  Deeper rings and more waves change nothing; weights that lie
+// contiguously for each workgroup would (14 us), but the layout is the
+// caller's.
+template <int CT>
+__device__ __forceinline__ int few_key(int r) {
+    return CT == 32 ? ((r >> 1) & 1) | ((r >> 2) & 2) : (r >> 3) & 1;
+}
+
+// The reads of a slice in one asm block (one wait): MB direct fragments of x
+// and the NF transposed ones of the weights, second half 4 rows on.
+template <int MB, int NF, int HALF>
+__device__ __forceinline__ void few_slice(v8bf (&fa)[MB], v8bf (&fb)[NF], const unsigned (&da)[MB],
+                                          const unsigned (&ba)[NF]) {
+    static_assert((MB == 1 || MB == 2 || MB == 4) && (NF == 2 || NF == 4), "1, 2 or 4 row blocks, 2 or 4 column blocks");
+    if constexpr (MB == 4 && NF == 4) {
+        direct_tr_slice<HALF>(fa, fb, da, ba);
+        return;
+    }
+    // rows past MB read the last block again
+    v4i d[4];
+    u64 o[8];
+    if constexpr (NF == 4)
+        asm volatile(
+            "ds_read_b128 %0, %10\n\t"
+            "ds_read_b128 %1, %11\n\t"
+            "ds_read_b64_tr_b16 %2, %12\n\t"
+            "ds_read_b64_tr_b16 %3, %12 offset:%16\n\t"
+            "ds_read_b64_tr_b16 %4, %13\n\t"
+            "ds_read_b64_tr_b16 %5, %13 offset:%16\n\t"
+            "ds_read_b64_tr_b16 %6, %14\n\t"
+            "ds_read_b64_tr_b16 %7, %14 offset:%16\n\t"
+            "ds_read_b64_tr_b16 %8, %15\n\t"
+            "ds_read_b64_tr_b16 %9, %15 offset:%16\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3]), "=&v"(o[4]), "=&v"(o[5]),
+              "=&v"(o[6]), "=&v"(o[7])
+            : "v"(da[0]), "v"(da[MB - 1]), "v"(ba[0]), "v"(ba[1]), "v"(ba[NF - 2]), "v"(ba[NF - 1]), "i"(HALF)
+            : "memory");
+    else if constexpr (MB <= 2)
+        asm volatile(
+            "ds_read_b128 %0, %6\n\t"
+            "ds_read_b128 %1, %7\n\t"
+            "ds_read_b64_tr_b16 %2, %8\n\t"
+            "ds_read_b64_tr_b16 %3, %8 offset:%10\n\t"
+            "ds_read_b64_tr_b16 %4, %9\n\t"
+            "ds_read_b64_tr_b16 %5, %9 offset:%10\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3])
+            : "v"(da[0]), "v"(da[MB - 1]), "v"(ba[0]), "v"(ba[1]), "i"(HALF)
+            : "memory");
+    else
+        asm volatile(
+            "ds_read_b128 %0, %8\n\t"
+            "ds_read_b128 %1, %9\n\t"
+            "ds_read_b128 %2, %10\n\t"
+            "ds_read_b128 %3, %11\n\t"
+            "ds_read_b64_tr_b16 %4, %12\n\t"
+            "ds_read_b64_tr_b16 %5, %12 offset:%14\n\t"
+            "ds_read_b64_tr_b16 %6, %13\n\t"
+            "ds_read_b64_tr_b16 %7, %13 offset:%14\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3])
+            : "v"(da[0]), "v"(da[1 % MB]), "v"(da[2 % MB]), "v"(da[3 % MB]), "v"(ba[0]), "v"(ba[1]), "i"(HALF)
+            : "memory");
+#pragma unroll
+    for (int i = 0; i < MB; ++i) fa[i] = __builtin_bit_cast(v8bf, d[i]);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) fb[i] = __builtin_bit_cast(v8bf, u64x2{o[2 * i], o[2 * i + 1]});
+}
+
+template <bool OUT_BF16, int SAVE, int MB, int CT, int NW, int S>
+__global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) {
+    constexpr int TR = 16 * MB, NTHR = 64 * NW, NF = CT / 8, NI = CT / 8;
+    constexpr int kA = TR * 32, kB = 64 * CT, kSt = kA + kB;   // elements
+    constexpr int kRow = 2 * CT + 4;                           // fp32 staging row
+    constexpr int kRing = NW * S * kSt;
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[kRing];
+    __shared__ int s_info[5];
+    static_assert(NW * TR * kRow * 2 <= kRing, "the partial sums fit the rings");
+    static_assert(kRing * 2 <= 163840 - 1024, "the rings fit the LDS");
+
+    const int tid = threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    FfnItem it;
+    if (!ffn_item<kGated, TR, 2 * CT, NTHR>(a, s_info, it)) return;
+    if (it.g == a.G) {
+        zero_tail<kGated, OUT_BF16, SAVE, 2 * CT, NTHR>(a, it);
+        return;
+    }
+    const int K = a.K, NN = a.NN, N = NN / 2;
+    uint16_t* mine = ring + wave * S * kSt;
+    int64_t a_off[MB], b_off[NI];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const DmaLane d = dma_direct<32, 4, 16>(i, lane);
+        a_off[i] = (int64_t)min(it.row0 + d.row, it.hi - 1) * K + d.col;
+    }
+    constexpr int LPR = CT / 4;   // lanes per row of 2 CT columns
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int r = (64 / LPR) * i + lane / LPR, p = lane % LPR;
+        const int col = 16 * ((p >> 1) ^ few_key<CT>(r)) + 8 * (p & 1);
+        b_off[i] = (int64_t)r * NN + it.c0 + (col < CT ? col : N + col - CT);
+    }
+    const uint16_t* wg = a.b + (int64_t)it.g * K * NN;
+    auto issue = [&](int i, int stage) {
+        const int r0 = 32 * (wave + NW * i);
+        uint16_t* sa = mine + stage * kSt;
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+            const uint16_t* pa = a.a + a_off[j] + r0;
+            __builtin_amdgcn_global_load_lds(pa, (GMM_LDS void*)(sa + j * 512), 16, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const uint16_t* pb = wg + (int64_t)r0 * NN + b_off[j];
+            __builtin_amdgcn_global_load_lds(pb, (GMM_LDS void*)(sa + kA + j * 512), 16, 0, 0);
+        }
+    };
+    const int lr = lane & 15, lg = lane >> 4;
+    const unsigned base = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)mine;
+    unsigned a_dir[MB], b_tr[NF];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+        const int row = 16 * i + lr;
+        a_dir[i] = base + (unsigned)(2 * (row * 32 + 8 * (lg ^ direct_key<32>(row))));
+    }
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+        const int r = 8 * lg + (lr >> 2);
+        b_tr[i] = base + (unsigned)(2 * (kA + r * 2 * CT + 16 * (i ^ few_key<CT>(r)) + (lr & 3) * 4));
+    }
+    v4f acc[MB][NF];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    const int ns = (K / 32 - wave + NW - 1) / NW;   // this wave's slices
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+        if (i < ns) issue(i, i);
+    int stage = 0;
+    for (int i = 0; i < ns; ++i) {
+        if (i + S - 2 < ns) wait_vmem<(NI + MB) * (S - 2)>(); else wait_vmem<0>();
+        if (i + S - 1 < ns) issue(i + S - 1, stage == 0 ? S - 1 : stage - 1);
+        const unsigned so = (unsigned)(stage * kSt * 2);
+        unsigned da[MB], ba[NF];
+#pragma unroll
+        for (int j = 0; j < MB; ++j) da[j] = a_dir[j] + so;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) ba[j] = b_tr[j] + so;
+        v8bf af[MB], bf[NF];
+        few_slice<MB, NF, 4 * 4 * CT>(af, bf, da, ba);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[m], acc[m][j], 0, 0, 0);
+        stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    __syncthreads();   // every wave is done with its ring
+    float* part = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            *reinterpret_cast<v4f*>(part + (wave * TR + 16 * m + lr) * kRow + 16 * j + 4 * lg) = acc[m][j];
+    __syncthreads();
+    // CT / 4 threads a row, 4 gate and 4 up columns each
+    constexpr int TPR = CT / 4;
+    for (int e = tid; e < TR * TPR; e += NTHR) {
+        const int r = e / TPR, c = (e % TPR) * 4, row = it.row0 + r;
+        if (row >= it.hi) continue;   // the lanes of a row together
+        v4f g = v4f{0.f, 0.f, 0.f, 0.f}, u = g;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            g += *reinterpret_cast<const v4f*>(part + (w * TR + r) * kRow + c);
+            u += *reinterpret_cast<const v4f*>(part + (w * TR + r) * kRow + CT + c);
+        }
+        const float h0 = silu_mul(g[0], u[0]), h1 = silu_mul(g[1], u[1]), h2 = silu_mul(g[2], u[2]),
+                    h3 = silu_mul(g[3], u[3]);
+        const int64_t o = (int64_t)row * N + it.c0 + c, pg = (int64_t)row * NN + it.c0 + c;
+        if constexpr (OUT_BF16)
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + o) =
+                make_uint2(pack_rne(h0, h1), pack_rne(h2, h3));
+        else
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + o) = make_float4(h0, h1, h2, h3);
+        if constexpr (SAVE == kSaveBf16) {
+            *reinterpret_cast<uint2*>(a.gu + pg) = make_uint2(pack_rne(g[0], g[1]), pack_rne(g[2], g[3]));
+            *reinterpret_cast<uint2*>(a.gu + pg + N) = make_uint2(pack_rne(u[0], u[1]), pack_rne(u[2], u[3]));
+        }
+        if constexpr (SAVE == kSaveMx8) {
+            static_assert(SAVE != kSaveMx8 || CT == 32, "a row's columns are one block");
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const v4f v = p == 0 ? g : u;
+                const uint32_t m = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+                const uint32_t sc = mx8_scale_code(__float_as_uint(max_over_8(__uint_as_float(m))));
+                const float inv = mx8_inverse(sc);
+                *reinterpret_cast<uint32_t*>(a.gu_q + pg + p * N) =
+                    e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                if ((e & 7) == 0) a.gu_s[(pg + p * N) >> 5] = (uint8_t)sc;
+            }
+        }
+    }
+}
+
+template <bool OUT_BF16, int SAVE, int MB, int CT, int NW, int S>
+hipError_t launch_few(FfnArgs a, hipStream_t stream) {
+    a.ntiles_c = a.NN / 2 / CT;
+    a.nblocks = (int)(max_work_items(a.M, a.G < a.M ? a.G : a.M, 16 * MB) * a.ntiles_c);
+    hipLaunchKernelGGL((gated_few_kernel<OUT_BF16, SAVE, MB, CT, NW, S>), dim3((unsigned)a.nblocks), dim3(64 * NW), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
 template <int MODE, int SAVE = kSaveNone>
 hipError_t launch_any(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
     return out_bf16 ? launch<MODE, true, SAVE, 3, 3, 2, 2>(a, stream) : launch<MODE, false, SAVE, 3, 3, 2, 2>(a, stream);
@@ -523,6 +755,7 @@ hipError_t launch_any(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
 }  // namespace
 
 int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G) {
+    // of the 128-row tiles; the few-row form only takes grids near the chip's size
     return max_work_items(M, G < M ? G : M, 128) * ((N + 63) / 64);
 }
 
@@ -532,10 +765,39 @@ int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G) {
 
 int64_t ffn_dw_blocks(int64_t K, int64_t NN, int64_t G) { return G * ((K + 127) / 128) * ((NN + 127) / 128); }
 
+// The few-row form is for grids that the 128-row tiles leave unfilled.  With
+// B busy experts (at most min(G, M)) of few rows each, those tiles make B N/64
+// workgroups, each streaming its columns of the weights alone; below one per
+// CU the chip idles.  Measured at K = 2048, N = 512, cold weights (us, 128-row
+// tiles / few rows): 1 expert 25.7 / 10.4, 8 experts (33 MB) 28.7 / 17.7, 32
+// experts 37.5 / 39.4.  16 + 16 columns (8 waves) fill the chip from half as
+// many experts as 32 + 32 (4 waves): 8 experts 17.7 against 18.8 us, 16
+// experts (more workgroups than CUs) 29.4 against 20.7 us.
+constexpr int kFewMaxRows = 64;   // mean rows an expert: up to 4 blocks of 16
+
+template <bool OUT_BF16, int SAVE, int MB>
+hipError_t launch_few_mb(const FfnArgs& a, int busy, hipStream_t stream) {
+    if constexpr (SAVE != kSaveMx8)
+        if ((int64_t)busy * (a.NN / 32) <= device_cus())
+            return launch_few<OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
+    return launch_few<OUT_BF16, SAVE, MB, 32, 4, 3>(a, stream);
+}
+
+template <int SAVE, bool OUT_BF16>
+hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
+    const int busy = a.G < a.M ? a.G : a.M, rows = (a.M + busy - 1) / busy;
+    if (rows <= kFewMaxRows && (int64_t)busy * (a.NN / 128) < device_cus()) {
+        if (rows <= 16) return launch_few_mb<OUT_BF16, SAVE, 1>(a, busy, stream);
+        if (rows <= 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, busy, stream);
+        return launch_few_mb<OUT_BF16, SAVE, 4>(a, busy, stream);
+    }
+    return launch<kGated, OUT_BF16, SAVE, 3, 3, 2, 2>(a, stream);
+}
+
 hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    if (a.gu_q != nullptr) return launch_any<kGated, kSaveMx8>(a, out_bf16, stream);
-    if (a.gu != nullptr) return launch_any<kGated, kSaveBf16>(a, out_bf16, stream);
-    return launch_any<kGated, kSaveNone>(a, out_bf16, stream);
+    if (a.gu_q != nullptr) return out_bf16 ? launch_gated<kSaveMx8, true>(a, stream) : launch_gated<kSaveMx8, false>(a, stream);
+    if (a.gu != nullptr) return out_bf16 ? launch_gated<kSaveBf16, true>(a, stream) : launch_gated<kSaveBf16, false>(a, stream);
+    return out_bf16 ? launch_gated<kSaveNone, true>(a, stream) : launch_gated<kSaveNone, false>(a, stream);
 }
 
 hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream) {

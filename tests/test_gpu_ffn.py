@@ -535,3 +535,18 @@ def test_offsets_past_32_bits():
     _, c, want = mx8_64(f64(big[-1:]))
     assert np.array_equal(f64(back[-1:]), want) and np.array_equal(raw(s[-1:]), c)
     assert (back[:-1] == 0).all()
+
+
+# Few rows an expert: 16, 32 and 64-row tiles, 16 + 16 and 32 + 32 columns, K slices fewer than waves.
+FEW = [
+    ([1], 1, 64, 64), ([16], 16, 2048, 128), ([17, 0, 15], 40, 128, 64), ([40, 0], 40, 192, 320),
+    ([64], 64, 448, 64), ([70, 3, 0, 100], 200, 320, 192), ([0, 9, 31, 0, 33], 100, 576, 256),
+    ([5, 0, 1, 2] * 3, 30, 64, 1024),
+]
+
+
+@pytest.mark.parametrize("shape", FEW, ids=["M%d_K%d_N%d_G%d" % (M, K, N, len(s)) for s, M, K, N in FEW])
+@pytest.mark.parametrize("save", ["none", "bf16", "mx8"])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_forward_few_rows(shape, save, dt):
+    test_forward(shape, save, dt)
