@@ -17,6 +17,8 @@
 #include "gmm_mx8.hpp"
 #include "gmm_tile.hpp"
 
+#include <type_traits>
+
 namespace gmm {
 
 namespace {
@@ -40,9 +42,93 @@ __device__ __forceinline__ void zero_block(void* base, int64_t pitch, int lo, in
         *reinterpret_cast<uint32_t*>(static_cast<char*>(base) + (int64_t)(lo + e / w) * pitch + col + 4 * (e % w)) = 0u;
 }
 
+// Work item of block b when every group's rows are cut into ceil(s / cap)
+// items of equal height (to 16 rows; cap a multiple of 16): a group of just
+// over cap rows gives two halves instead of a full item and a sliver.  Items
+// are dealt to the XCDs as in balanced_work_item.
+__device__ __forceinline__ WorkItem even_item(int g, int glo, int ghi, int idx, int cap) {
+    const int n = (ghi - glo + cap - 1) / cap;
+    const int h = ((ghi - glo + n - 1) / n + 15) & ~15;
+    WorkItem it;
+    it.g = g;
+    it.tile = -1;
+    it.lo = glo + idx * h;
+    it.hi = min(ghi, it.lo + h);
+    return it;
+}
+
+template <int CAP>
+__device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ group_sizes, int G, int M, int ntiles,
+                                                   int b, int& col) {
+    col = 0;
+    const int lane = lane_id();
+    // Up to 256 groups the clamped ranges and item offsets stay in registers,
+    // every load issued before the first scan; beyond, a second pass.
+    const bool inreg = G <= 256;
+    int lo[4], hi[4], cn[4], W[4], raw[4];
+    int carry = 0, items = 0;
+    if (inreg) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[k] = group_size_at(group_sizes, G, 64 * k + lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            lo[k] = hi[k] = cn[k] = W[k] = 0;
+            if (64 * k < G) {
+                const GroupChunk ch = group_chunk_of(raw[k], M, carry);
+                lo[k] = ch.lo;
+                hi[k] = ch.hi;
+                carry = ch.next_carry;
+                cn[k] = group_items<true>(ch.lo, ch.hi, CAP);
+                const int incl = wave_incl_scan(cn[k]);
+                W[k] = items + incl - cn[k];
+                items += lane_value(incl, 63);
+            }
+        }
+    } else {
+        for (int base = 0; base < G; base += 64) {
+            const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
+            carry = ch.next_carry;
+            items += lane_value(wave_incl_scan(group_items<true>(ch.lo, ch.hi, CAP)), 63);
+        }
+    }
+    const int total = min(carry, M);
+    const int L = xcd_balance(b, (items + tail_items<true>(total, M, CAP)) * ntiles);
+    if (L < 0) return WorkItem{-1, 0, 0, 0};
+    const int w = L / ntiles;
+    col = L % ntiles;
+    if (w >= items) return tail_item<true>(G, M, total, items, CAP, w);
+    if (inreg) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned long long m = __ballot(cn[k] > 0 && w >= W[k] && w < W[k] + cn[k]);
+            if (m) {
+                const int src = __ffsll((long long)m) - 1;
+                return even_item(64 * k + src, lane_value(lo[k], src), lane_value(hi[k], src),
+                                 w - lane_value(W[k], src), CAP);
+            }
+        }
+    } else {
+        int first = 0;
+        carry = 0;
+        for (int base = 0; base < G; base += 64) {
+            const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
+            carry = ch.next_carry;
+            const int c = group_items<true>(ch.lo, ch.hi, CAP), incl = wave_incl_scan(c), Wb = first + incl - c;
+            const unsigned long long m = __ballot(c > 0 && w >= Wb && w < Wb + c);
+            if (m) {
+                const int src = __ffsll((long long)m) - 1;
+                return even_item(base + src, lane_value(ch.lo, src), lane_value(ch.hi, src), w - lane_value(Wb, src),
+                                 CAP);
+            }
+            first += lane_value(incl, 63);
+        }
+    }
+    return WorkItem{-1, 0, 0, 0};   // not reached: w < items has an owner
+}
+
 // Work item of a workgroup; every mode's block 0 also writes the call's
 // device status word.  TR x TC: tile rows and columns of the product.
-template <int MODE, int TR, int TC, int NTHR>
+template <int MODE, int TR, int TC>
 __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int* s_info, FfnItem& it) {
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     if (wave == 1 && blockIdx.x == 0) {
@@ -68,7 +154,7 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int* s_info, FfnItem&
     } else {
         if (wave == 0) {
             int col;
-            const WorkItem wi = balanced_work_item<true>(a.group_sizes, a.G, a.M, TR, a.ntiles_c, blockIdx.x, col);
+            const WorkItem wi = even_work_item<TR>(a.group_sizes, a.G, a.M, a.ntiles_c, blockIdx.x, col);
             if (lane == 0) { s_info[0] = wi.g; s_info[1] = wi.lo; s_info[2] = wi.hi; s_info[3] = col; }
         }
         __syncthreads();
@@ -106,111 +192,98 @@ __device__ __forceinline__ void zero_tail(const FfnArgs& a, const FfnItem& it) {
     }
 }
 
-// Epilogue of the gated forward for a TR x TC tile (gate columns, then up
-// columns) held as 64 x 64 wave blocks: acc[i][0..1] gate, acc[i][2..3] up;
-// lane (lr, lg) holds row 16i + lr and columns 16j + 4lg .. +3 of its wave's
-// 32.  Everything leaves through LDS (`sm`, idle by now) so that global
-// stores cover whole row segments.
-template <bool OUT_BF16, int SAVE, int TR, int TC, int WN, int NTHR>
-__device__ __forceinline__ void gated_epilogue(const FfnArgs& a, const FfnItem& it, v4f (&acc)[4][4],
-                                               uint16_t* sm) {
-    constexpr int H = TC / 2;
+// Epilogue of the gated forward.  Fragments j < NJ / 2 of a lane's row are
+// gate columns, j + NJ / 2 the same up columns; lane (lr, lg) holds columns
+// 4lg .. +3 of each 16 and row lr of every other 16-row block.  Everything
+// leaves through LDS (`sm`, idle by now) so that global stores cover whole row
+// segments.
+template <bool OUT_BF16, int SAVE, int NJ>
+__device__ __forceinline__ void gated_epilogue(const FfnArgs& a, const FfnItem& it, v4f (&acc)[4][NJ], uint16_t* sm) {
+    constexpr int TC = 32 * NJ, H = TC / 2, HJ = NJ / 2, NTHR = 256;
     const int tid = threadIdx.x, lane = lane_id();
-    const int wm = (tid >> 6) / WN, wn = (tid >> 6) % WN, lr = lane & 15, lg = lane >> 4;
-    const int N = a.NN / 2, rows = it.hi - it.lo;
+    const int wm = tid >> 7, wn = (tid >> 6) & 1, lr = lane & 15, lg = lane >> 4;
+    const int N = a.NN / 2, rows = it.hi - it.row0;
+    const int r0 = 16 * wm + lr, hc = 16 * HJ * wn + 4 * lg;   // tile row of block 0, column of fragment 0
     if constexpr (SAVE == kSaveBf16) {
         constexpr int P = TC + 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint2*>(sm + (wm * 64 + 16 * i + lr) * P + (j < 2 ? 0 : H) + wn * 32 + 16 * (j & 1) + 4 * lg) =
+            for (int j = 0; j < NJ; ++j)
+                *reinterpret_cast<uint2*>(sm + (r0 + 32 * i) * P + (j < HJ ? 0 : H) + hc + 16 * (j % HJ)) =
                     make_uint2(pack_rne(acc[i][j][0], acc[i][j][1]), pack_rne(acc[i][j][2], acc[i][j][3]));
         __syncthreads();
         for (int e = tid; e < rows * (TC / 8); e += NTHR) {
             const int r = e / (TC / 8), c = (e % (TC / 8)) * 8;
             const int col = it.c0 + (c < H ? c : c - H);
             if (col < N)
-                store_out(a.gu + (int64_t)(it.lo + r) * a.NN + (c < H ? 0 : N) + col,
+                store_out(a.gu + (int64_t)(it.row0 + r) * a.NN + (c < H ? 0 : N) + col,
                           *reinterpret_cast<const uint4*>(sm + r * P + c));
         }
         __syncthreads();
     }
     if constexpr (SAVE == kSaveMx8) {
-        // a wave's 32 gate (and up) columns of a row are one block, spread
+        // 32 gate (or up) columns of a row are one block: two fragments, spread
         // over the lanes lr, lr + 16, lr + 32, lr + 48
         constexpr int P = TC + 16, NS = TC / 32;
         uint8_t* cm = reinterpret_cast<uint8_t*>(sm);
-        uint8_t* ss = cm + TR * P;
+        uint8_t* ss = cm + 128 * P;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const v4f v0 = acc[i][2 * p], v1 = acc[i][2 * p + 1];
+            for (int b = 0; b < HJ; ++b) {   // HJ / 2 gate blocks, then as many up blocks
+                const v4f v0 = acc[i][2 * b], v1 = acc[i][2 * b + 1];
                 uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) m = max(m, max(abs_bits(v0[k]), abs_bits(v1[k])));
                 const uint32_t c = mx8_scale_code(max_over_rows16(m));
                 const float inv = mx8_inverse(c);
-                const int r = wm * 64 + 16 * i + lr;
-                uint8_t* d = cm + r * P + p * H + wn * 32 + 4 * lg;
-                *reinterpret_cast<uint32_t*>(d) = e4m3x4(v0[0] * inv, v0[1] * inv, v0[2] * inv, v0[3] * inv);
-                *reinterpret_cast<uint32_t*>(d + 16) = e4m3x4(v1[0] * inv, v1[1] * inv, v1[2] * inv, v1[3] * inv);
-                if (lg == 0) ss[r * NS + p * WN + wn] = (uint8_t)c;
+                const int r = r0 + 32 * i, col = (b < HJ / 2 ? 0 : H) + 32 * (b % (HJ / 2)) + hc;
+                *reinterpret_cast<uint32_t*>(cm + r * P + col) =
+                    e4m3x4(v0[0] * inv, v0[1] * inv, v0[2] * inv, v0[3] * inv);
+                *reinterpret_cast<uint32_t*>(cm + r * P + col + 16) =
+                    e4m3x4(v1[0] * inv, v1[1] * inv, v1[2] * inv, v1[3] * inv);
+                if (lg == 0) ss[r * NS + (col >> 5)] = (uint8_t)c;
             }
         __syncthreads();
         for (int e = tid; e < rows * (TC / 16); e += NTHR) {
             const int r = e / (TC / 16), c = (e % (TC / 16)) * 16;
             const int col = it.c0 + (c < H ? c : c - H);
             if (col < N)
-                store_out(a.gu_q + (int64_t)(it.lo + r) * a.NN + (c < H ? 0 : N) + col,
+                store_out(a.gu_q + (int64_t)(it.row0 + r) * a.NN + (c < H ? 0 : N) + col,
                           *reinterpret_cast<const uint4*>(cm + r * P + c));
         }
         for (int e = tid; e < rows * (NS / 2); e += NTHR) {   // pairs of scale bytes: 64 columns
-            const int r = e / (NS / 2), k = (e % (NS / 2)) * 2;
-            const int p = k / WN, b = k % WN;
+            const int r = e / (NS / 2), k = (e % (NS / 2)) * 2, up = k >= NS / 2;
+            const int b = k - (up ? NS / 2 : 0);
             if (it.c0 + b * 32 < N)
-                *reinterpret_cast<uint16_t*>(a.gu_s + (int64_t)(it.lo + r) * (a.NN / 32) + (p * N + it.c0) / 32 + b) =
+                *reinterpret_cast<uint16_t*>(a.gu_s + (int64_t)(it.row0 + r) * (a.NN / 32) + ((up ? N : 0) + it.c0) / 32 + b) =
                     *reinterpret_cast<const uint16_t*>(ss + r * NS + k);
         }
         __syncthreads();
     }
-    if constexpr (OUT_BF16) {
-        constexpr int P = H + 8;
+    using V = typename std::conditional<OUT_BF16, uint2, float4>::type;   // four columns
+    using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
+    constexpr int P = H + 16 / (int)sizeof(E), C = 16 / (int)sizeof(E);
+    E* om = reinterpret_cast<E*>(sm);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const v4f g = acc[i][j], u = acc[i][j + 2];
-                *reinterpret_cast<uint2*>(sm + (wm * 64 + 16 * i + lr) * P + wn * 32 + 16 * j + 4 * lg) =
-                    make_uint2(pack_rne(silu_mul(g[0], u[0]), silu_mul(g[1], u[1])),
-                               pack_rne(silu_mul(g[2], u[2]), silu_mul(g[3], u[3])));
-            }
-        __syncthreads();
-        for (int e = tid; e < rows * (H / 8); e += NTHR) {
-            const int r = e / (H / 8), c = (e % (H / 8)) * 8;
-            if (it.c0 + c < N)
-                store_out(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(it.lo + r) * N + it.c0 + c,
-                          *reinterpret_cast<const uint4*>(sm + r * P + c));
+        for (int j = 0; j < HJ; ++j) {
+            const v4f g = acc[i][j], u = acc[i][j + HJ];
+            const float h0 = silu_mul(g[0], u[0]), h1 = silu_mul(g[1], u[1]), h2 = silu_mul(g[2], u[2]),
+                        h3 = silu_mul(g[3], u[3]);
+            V v;
+            if constexpr (OUT_BF16) v = make_uint2(pack_rne(h0, h1), pack_rne(h2, h3));
+            else v = make_float4(h0, h1, h2, h3);
+            *reinterpret_cast<V*>(om + (r0 + 32 * i) * P + hc + 16 * j) = v;
         }
-    } else {
-        constexpr int P = H + 4;
-        float* fm = reinterpret_cast<float*>(sm);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const v4f g = acc[i][j], u = acc[i][j + 2];
-                *reinterpret_cast<float4*>(fm + (wm * 64 + 16 * i + lr) * P + wn * 32 + 16 * j + 4 * lg) =
-                    make_float4(silu_mul(g[0], u[0]), silu_mul(g[1], u[1]), silu_mul(g[2], u[2]), silu_mul(g[3], u[3]));
-            }
-        __syncthreads();
-        for (int e = tid; e < rows * (H / 4); e += NTHR) {
-            const int r = e / (H / 4), c = (e % (H / 4)) * 4;
-            if (it.c0 + c < N)
-                store_out(reinterpret_cast<float*>(a.out) + (int64_t)(it.lo + r) * N + it.c0 + c,
-                          *reinterpret_cast<const float4*>(fm + r * P + c));
-        }
+    __syncthreads();
+    for (int e = tid; e < rows * (H / C); e += NTHR) {
+        const int r = e / (H / C), c = (e % (H / C)) * C;
+        if (it.c0 + c < N)
+            store_out(reinterpret_cast<E*>(a.out) + (int64_t)(it.row0 + r) * N + it.c0 + c,
+                      *reinterpret_cast<const uint4*>(om + r * P + c));
     }
 }
 
@@ -232,61 +305,204 @@ __device__ __forceinline__ void mx8_expand16(const u32x4& codes, uint32_t scale_
     }
 }
 
-// WM x WN waves of 64 x 64, S stages, RES workgroups per CU.
-template <int MODE, bool OUT_BF16, int SAVE, int S, int RES, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, RES * WM * WN / 4) void ffn_kernel(const FfnArgs a) {
-    using D = DmaShape<S, RES, WM, WN>;
-    constexpr int RD = D::kRD, TR = D::kTR, TC = D::kTC, NW = D::kWaves, NB = RD / 32, NTHR = 64 * NW;
-    constexpr int NIA = MODE == kBwdWQ ? 0 : D::kInstrA, NIB = D::kInstrB, kSt = D::kStage;
-    static_assert((WM == 2 && WN == 2) || (WM == 4 && WN == 2) || (WM == 2 && WN == 4), "2 x 2, 4 x 2 or 2 x 4 waves");
-    static_assert(RES * S * kSt * 2 <= 163840 - 1024, "the rings of RES workgroups fit the LDS");
-    static_assert(MODE != kBwdWQ || (NB == 1 && S >= 3 && TR * RD == NTHR * 16), "one 16-code chunk per thread");
+// ---- fragment reads of one 32-deep slice, one asm block and one wait each.
+// A wave's four direct fragments of A sit 2048 bytes apart (every other 16 rows
+// of 64 bytes, the same swizzle key), direct fragments of B 1024 bytes; a wave's transposed fragments j and j + 4 of B 256 bytes
+// apart (columns 128 apart: the key only permutes the low 3 bits of the
+// 32-byte chunk); the second half of a transposed fragment HA / HB bytes on.
+
+template <int HB>
+__device__ __forceinline__ void read_direct_tr8(v8bf (&fa)[4], v8bf (&fb)[8], unsigned a, const unsigned (&b)[4]) {
+    v4i d[4];
+    u64 o[16];
+    asm volatile(
+        "ds_read_b128 %0, %20\n\t"
+        "ds_read_b64_tr_b16 %4, %21\n\t"
+        "ds_read_b64_tr_b16 %5, %21 offset:%25\n\t"
+        "ds_read_b64_tr_b16 %6, %22\n\t"
+        "ds_read_b64_tr_b16 %7, %22 offset:%25\n\t"
+        "ds_read_b64_tr_b16 %8, %23\n\t"
+        "ds_read_b64_tr_b16 %9, %23 offset:%25\n\t"
+        "ds_read_b64_tr_b16 %10, %24\n\t"
+        "ds_read_b64_tr_b16 %11, %24 offset:%25\n\t"
+        "ds_read_b64_tr_b16 %12, %21 offset:256\n\t"
+        "ds_read_b64_tr_b16 %13, %21 offset:%26\n\t"
+        "ds_read_b64_tr_b16 %14, %22 offset:256\n\t"
+        "ds_read_b64_tr_b16 %15, %22 offset:%26\n\t"
+        "ds_read_b64_tr_b16 %16, %23 offset:256\n\t"
+        "ds_read_b64_tr_b16 %17, %23 offset:%26\n\t"
+        "ds_read_b64_tr_b16 %18, %24 offset:256\n\t"
+        "ds_read_b64_tr_b16 %19, %24 offset:%26\n\t"
+        "ds_read_b128 %1, %20 offset:2048\n\t"
+        "ds_read_b128 %2, %20 offset:4096\n\t"
+        "ds_read_b128 %3, %20 offset:6144\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3]),
+          "=&v"(o[4]), "=&v"(o[5]), "=&v"(o[6]), "=&v"(o[7]), "=&v"(o[8]), "=&v"(o[9]), "=&v"(o[10]), "=&v"(o[11]),
+          "=&v"(o[12]), "=&v"(o[13]), "=&v"(o[14]), "=&v"(o[15])
+        : "v"(a), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "i"(HB), "i"(HB + 256)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fa[i] = __builtin_bit_cast(v8bf, d[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fb[i] = __builtin_bit_cast(v8bf, u64x2{o[2 * i], o[2 * i + 1]});
+}
+
+template <int NJ>
+__device__ __forceinline__ void read_direct_direct(v8bf (&fa)[4], v8bf (&fb)[NJ], unsigned a, unsigned b) {
+    v4i d[4], e[8];
+    if constexpr (NJ == 8)
+        asm volatile(
+            "ds_read_b128 %0, %12\n\t"
+            "ds_read_b128 %4, %13\n\t"
+            "ds_read_b128 %5, %13 offset:1024\n\t"
+            "ds_read_b128 %6, %13 offset:2048\n\t"
+            "ds_read_b128 %7, %13 offset:3072\n\t"
+            "ds_read_b128 %8, %13 offset:4096\n\t"
+            "ds_read_b128 %9, %13 offset:5120\n\t"
+            "ds_read_b128 %10, %13 offset:6144\n\t"
+            "ds_read_b128 %11, %13 offset:7168\n\t"
+            "ds_read_b128 %1, %12 offset:2048\n\t"
+            "ds_read_b128 %2, %12 offset:4096\n\t"
+            "ds_read_b128 %3, %12 offset:6144\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(e[0]), "=&v"(e[1]), "=&v"(e[2]), "=&v"(e[3]),
+              "=&v"(e[4]), "=&v"(e[5]), "=&v"(e[6]), "=&v"(e[7])
+            : "v"(a), "v"(b)
+            : "memory");
+    else
+        asm volatile(
+            "ds_read_b128 %0, %8\n\t"
+            "ds_read_b128 %4, %9\n\t"
+            "ds_read_b128 %5, %9 offset:1024\n\t"
+            "ds_read_b128 %6, %9 offset:2048\n\t"
+            "ds_read_b128 %7, %9 offset:3072\n\t"
+            "ds_read_b128 %1, %8 offset:2048\n\t"
+            "ds_read_b128 %2, %8 offset:4096\n\t"
+            "ds_read_b128 %3, %8 offset:6144\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(d[3]), "=&v"(e[0]), "=&v"(e[1]), "=&v"(e[2]), "=&v"(e[3])
+            : "v"(a), "v"(b)
+            : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fa[i] = __builtin_bit_cast(v8bf, d[i]);
+#pragma unroll
+    for (int i = 0; i < NJ; ++i) fb[i] = __builtin_bit_cast(v8bf, e[i]);
+}
+
+template <int HA, int HB>
+__device__ __forceinline__ void read_tr_tr8(v8bf (&fa)[4], v8bf (&fb)[8], const unsigned (&a)[4],
+                                            const unsigned (&b)[4]) {
+    u64 p[8], o[16];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %24\n\t"
+        "ds_read_b64_tr_b16 %1, %24 offset:%32\n\t"
+        "ds_read_b64_tr_b16 %8, %28\n\t"
+        "ds_read_b64_tr_b16 %9, %28 offset:%33\n\t"
+        "ds_read_b64_tr_b16 %10, %29\n\t"
+        "ds_read_b64_tr_b16 %11, %29 offset:%33\n\t"
+        "ds_read_b64_tr_b16 %12, %30\n\t"
+        "ds_read_b64_tr_b16 %13, %30 offset:%33\n\t"
+        "ds_read_b64_tr_b16 %14, %31\n\t"
+        "ds_read_b64_tr_b16 %15, %31 offset:%33\n\t"
+        "ds_read_b64_tr_b16 %16, %28 offset:256\n\t"
+        "ds_read_b64_tr_b16 %17, %28 offset:%34\n\t"
+        "ds_read_b64_tr_b16 %18, %29 offset:256\n\t"
+        "ds_read_b64_tr_b16 %19, %29 offset:%34\n\t"
+        "ds_read_b64_tr_b16 %20, %30 offset:256\n\t"
+        "ds_read_b64_tr_b16 %21, %30 offset:%34\n\t"
+        "ds_read_b64_tr_b16 %22, %31 offset:256\n\t"
+        "ds_read_b64_tr_b16 %23, %31 offset:%34\n\t"
+        "ds_read_b64_tr_b16 %2, %25\n\t"
+        "ds_read_b64_tr_b16 %3, %25 offset:%32\n\t"
+        "ds_read_b64_tr_b16 %4, %26\n\t"
+        "ds_read_b64_tr_b16 %5, %26 offset:%32\n\t"
+        "ds_read_b64_tr_b16 %6, %27\n\t"
+        "ds_read_b64_tr_b16 %7, %27 offset:%32\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(p[0]), "=&v"(p[1]), "=&v"(p[2]), "=&v"(p[3]), "=&v"(p[4]), "=&v"(p[5]), "=&v"(p[6]), "=&v"(p[7]),
+          "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3]), "=&v"(o[4]), "=&v"(o[5]), "=&v"(o[6]), "=&v"(o[7]),
+          "=&v"(o[8]), "=&v"(o[9]), "=&v"(o[10]), "=&v"(o[11]), "=&v"(o[12]), "=&v"(o[13]), "=&v"(o[14]), "=&v"(o[15])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "i"(HA), "i"(HB),
+          "i"(HB + 256)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fa[i] = __builtin_bit_cast(v8bf, u64x2{p[2 * i], p[2 * i + 1]});
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fb[i] = __builtin_bit_cast(v8bf, u64x2{o[2 * i], o[2 * i + 1]});
+}
+
+// Sizes of a tile of 128 x (32 NJ): 4 waves, 2 x 2, of 64 x (16 NJ).
+template <int NJ>
+struct FfnTile {
+    static constexpr int kTR = 128, kTC = 32 * NJ, kS = 3, kRes = NJ == 8 ? 2 : 3;
+    static constexpr int kSliceA = kTR * 32, kSliceB = kTC * 32, kStage = kSliceA + kSliceB;   // elements
+    static constexpr int kNIB = NJ / 2;            // load-to-LDS instructions of B per wave and slice
+    static_assert(kRes * kS * kStage * 2 <= 163840 - 1024, "the rings of kRes workgroups fit the LDS");
+};
+
+// Column of fragment j of wave column wn within the tile.  Direct B (dX):
+// 16 NJ contiguous columns.  Transposed B: the tile's left and right half
+// give NJ / 2 fragments each (gate and up, in the gated forward).
+template <int MODE, int NJ>
+__device__ __forceinline__ int frag_col(int wn, int j) {
+    if constexpr (MODE == kBwdX) return 16 * (NJ * wn + j);
+    return (j >= NJ / 2 ? 16 * NJ : 0) + 16 * ((NJ / 2) * wn + j % (NJ / 2));
+}
+
+template <int MODE, bool OUT_BF16, int SAVE, int NJ>
+__global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnArgs a) {
+    using T = FfnTile<NJ>;
+    constexpr int S = T::kS, TR = T::kTR, TC = T::kTC, NTHR = 256, kSt = T::kStage, NIB = T::kNIB;
     constexpr bool kW = MODE == kBwdW || MODE == kBwdWQ;   // both operands transposed
-    constexpr bool A_TR = kW, B_TR = MODE != kBwdX, kSpread = kW;
+    constexpr bool kSpread = kW;
     __shared__ __attribute__((aligned(1024))) uint16_t ring[S * kSt];
     __shared__ int s_info[5];
-    static_assert(MODE != kGated || TR * (TC + 16) * 2 <= S * kSt * 2, "epilogue staging fits the ring");
 
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     FfnItem it;
-    if (!ffn_item<MODE, TR, TC, NTHR>(a, s_info, it)) return;
+    if (!ffn_item<MODE, TR, TC>(a, s_info, it)) return;
     if (!kW && it.g == a.G) {
         zero_tail<MODE, OUT_BF16, SAVE, TC, NTHR>(a, it);
         return;
     }
     const int K = a.K, NN = a.NN, N = NN / 2;
     const int g = it.g, row0 = it.row0, hi = it.hi, c0 = it.c0, red_lo = it.red_lo, red_hi = it.red_hi;
+    // 16-row blocks of the tile that hold rows, and those of this wave (the
+    // wave rows take alternate blocks, so both have work in a short tile)
+    const int blocks = (hi - row0 + 15) >> 4;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int nb = kW ? min(4, max(0, blocks - 4 * wm)) : (blocks + 1 - wm) >> 1;
 
-    // ---- global element offsets of this lane's load-to-LDS instructions at
-    //      reduction index 0; rows and columns past the operand are clamped
-    //      to its last ones (they only reach outputs that are not stored)
+    // ---- global addresses of this lane's load-to-LDS instructions: two of A
+    //      and NIB of B per wave and slice.  Rows and columns past the operand
+    //      are clamped to its last ones (they only reach outputs that are not
+    //      stored); a 16-row block of A without rows is not loaded.
     const int lda = MODE == kGated ? K : NN;
     const uint16_t* wg = a.b + (kW ? 0 : (int64_t)g * K * NN);
-    int64_t a_off[NIA > 0 ? NIA : 1], b_off[NIB];
-    int a_row[NIA > 0 ? NIA : 1], b_row[NIB];
+    const int na = MODE == kBwdWQ ? 0 : (kW ? 2 : (wave < blocks) + (wave + 4 < blocks));
+    int64_t a_off[2], b_off[NIB];
+    int a_row[2] = {0, 0}, b_row[NIB];
 #pragma unroll
-    for (int i = 0; i < NIA; ++i) {
-        const int j = NIA * wave + i;
+    for (int i = 0; i < 2; ++i) {
         if constexpr (kW) {
-            const DmaLane d = dma_trans<kSpread, TR>(j, lane);
+            const DmaLane d = dma_trans<kSpread, TR>(wave + 4 * i, lane);
             a_row[i] = d.row;
             a_off[i] = min(row0 + d.col, K - 8);
         } else {
-            const DmaLane d = dma_direct<RD, D::kChunks, D::kRows>(j, lane);
-            a_row[i] = 0;
+            const DmaLane d = dma_direct<32, 4, 16>(wave + 4 * i, lane);
             a_off[i] = (int64_t)min(row0 + d.row, hi - 1) * lda + d.col;
         }
     }
 #pragma unroll
     for (int i = 0; i < NIB; ++i) {
-        const int j = NIB * wave + i;
         if constexpr (MODE == kBwdX) {
-            const DmaLane d = dma_direct<RD, D::kChunks, D::kRows>(j, lane);
+            const DmaLane d = dma_direct<32, 4, 16>(wave + 4 * i, lane);
             b_row[i] = 0;
             b_off[i] = (int64_t)min(c0 + d.row, K - 1) * NN + d.col;
         } else {
-            const DmaLane d = dma_trans<kSpread, TC>(j, lane);
+            const DmaLane d = dma_trans<kSpread, TC>(wave + 4 * i, lane);
             b_row[i] = d.row;
             if constexpr (MODE == kGated)
                 b_off[i] = d.col < TC / 2 ? min(c0 + d.col, N - 8) : N + min(c0 + d.col - TC / 2, N - 8);
@@ -295,18 +511,9 @@ __global__ __launch_bounds__(64 * WM * WN, RES * WM * WN / 4) void ffn_kernel(co
         }
     }
     auto issue = [&](int t, int stage) {
-        const int r0 = red_lo + t * RD;
-        uint16_t* sa = ring + stage * kSt;
-        uint16_t* sb = sa + D::kSliceA;
-#pragma unroll
-        for (int i = 0; i < NIA; ++i) {
-            const uint16_t* pa;
-            if constexpr (kW)
-                pa = a.a + (int64_t)min(r0 + a_row[i], red_hi - 1) * K + a_off[i];
-            else
-                pa = a.a + a_off[i] + r0;
-            __builtin_amdgcn_global_load_lds(pa, (GMM_LDS void*)(sa + (NIA * wave + i) * 512), 16, 0, 0);
-        }
+        const int r0 = red_lo + t * 32;
+        uint16_t* sa = ring + stage * kSt + 512 * wave;
+        uint16_t* sb = sa + T::kSliceA;
 #pragma unroll
         for (int i = 0; i < NIB; ++i) {
             const uint16_t* pb;
@@ -316,202 +523,216 @@ __global__ __launch_bounds__(64 * WM * WN, RES * WM * WN / 4) void ffn_kernel(co
                 pb = wg + (int64_t)(r0 + b_row[i]) * NN + b_off[i];
             else
                 pb = wg + b_off[i] + r0;
-            __builtin_amdgcn_global_load_lds(pb, (GMM_LDS void*)(sb + (NIB * wave + i) * 512), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(pb, (GMM_LDS void*)(sb + 2048 * i), 16, 0, 0);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= na) break;
+            const uint16_t* pa;
+            if constexpr (kW)
+                pa = a.a + (int64_t)min(r0 + a_row[i], red_hi - 1) * K + a_off[i];
+            else
+                pa = a.a + a_off[i] + r0;
+            __builtin_amdgcn_global_load_lds(pa, (GMM_LDS void*)(sa + 2048 * i), 16, 0, 0);
+        }
+    };
+    const int nsl = (red_hi - red_lo + 31) >> 5;
+    // this wave's share of slice t has landed when only the younger slices'
+    // loads are outstanding
+    static_assert(S == 3, "one younger slice");
+    auto wait_slice = [&](int t) {
+        if (t + 1 >= nsl) wait_vmem<0>();
+        else if (MODE == kBwdWQ && t + 2 < nsl) wait_vmem<NIB + 2>();   // and the codes fetched with it
+        else if (na == 2) wait_vmem<(NIB + 2) * (S - 2)>();
+        else if (na == 1) wait_vmem<(NIB + 1) * (S - 2)>();
+        else wait_vmem<NIB * (S - 2)>();
     };
 
     // ---- checkpointed x: thread t takes the 16 codes of columns
-    //      16 (t % TR/16) .. +15 of slice row t / (TR/16), expands them and
-    //      writes the 32-byte chunk the transposed layout has there
-    constexpr int CPR = TR / 16;
-    const int qrow = tid / CPR, qchunk = tid % CPR;
+    //      16 (t % 8) .. +15 of slice row t / 8, expands them and writes the
+    //      32-byte chunk the transposed layout has there
+    const int qrow = tid / 8, qchunk = tid % 8;
     const int qcol = min(row0 + 16 * qchunk, K - 16);
-    u32x4 qd;
-    uint32_t qs = 0;
-    auto fetch_codes = [&](int t) {
-        const int64_t m = min(red_lo + t * RD + qrow, red_hi - 1);
-        qd = *reinterpret_cast<const u32x4*>(a.aq + m * K + qcol);
-        qs = a.as[m * (K >> 5) + (qcol >> 5)];
+    // Two sets of registers: codes are fetched two steps before they are put,
+    // so the wait for them leaves a whole step of loads in flight.
+    u32x4 qd[2];
+    uint32_t qs[2];
+    auto fetch_codes = [&](int t, int set) {
+        const int64_t m = min(red_lo + t * 32 + qrow, red_hi - 1);
+        qd[set] = *reinterpret_cast<const u32x4*>(a.aq + m * K + qcol);
+        qs[set] = a.as[m * (K >> 5) + (qcol >> 5)];
     };
-    auto put_codes = [&](int t, int stage) {
+    auto put_codes = [&](int t, int set, int stage) {
         u32x4 l, h;
-        mx8_expand16(qd, qs, l, h);
-        if (red_lo + t * RD + qrow >= red_hi) l = h = u32x4{0u, 0u, 0u, 0u};
+        mx8_expand16(qd[set], qs[set], l, h);
+        if (red_lo + t * 32 + qrow >= red_hi) l = h = u32x4{0u, 0u, 0u, 0u};
         uint16_t* p = ring + stage * kSt + qrow * TR + 16 * (qchunk ^ trans_key<kSpread>(qrow));
         *reinterpret_cast<u32x4*>(p) = l;
         *reinterpret_cast<u32x4*>(p + 8) = h;
     };
 
-    const int wm = (tid >> 6) / WN, wn = (tid >> 6) % WN;
+    // ---- LDS addresses of this lane's fragments in stage 0
     const int lr = lane & 15, lg = lane >> 4;
-    v4f acc[4][4];
+    const unsigned ring_lds = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)ring;
+    constexpr int kHalfA = 16 * TR * 2, kHalfB = (kSpread ? 16 : 4) * TC * 2;
+    unsigned ra[4], rb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 16 * (2 * i + wm) + lr;   // interleaved blocks; only ra[0] with 2048-byte steps is used
+        ra[i] = ring_lds + (kW ? tr_addr<true, TR>(lg, 64 * wm + 16 * i, lr)
+                               : (unsigned)(2 * (row * 32 + 8 * (lg ^ direct_key<32>(row)))));
+        const int br = 16 * NJ * wn + lr;
+        rb[i] = ring_lds + 2 * T::kSliceA +
+                (MODE == kBwdX ? (unsigned)(2 * (br * 32 + 8 * (lg ^ direct_key<32>(br))))
+                               : tr_addr<kSpread, TC>(lg, frag_col<MODE, NJ>(wn, i), lr));
+    }
+
+    v4f acc[4][NJ];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    constexpr int kHalfA = (kSpread ? 16 : 4) * TR * 2, kBlkA = 32 * TR * 2;
-    constexpr int kHalfB = (kSpread ? 16 : 4) * TC * 2, kBlkB = 32 * TC * 2;
-    const unsigned ring_lds = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)ring;
-    unsigned a_tr[4], b_tr[4], a_dir[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a_tr[i] = tr_addr<kSpread, TR>(lg, wm * 64 + i * 16, lr);
-        // the gated tile: blocks 0, 1 gate columns, 2, 3 the same up columns
-        const int bc = MODE == kGated ? (i < 2 ? 0 : TC / 2) + wn * 32 + (i & 1) * 16 : wn * 64 + i * 16;
-        b_tr[i] = tr_addr<kSpread, TC>(lg, bc, lr);
-        const int row = wm * 64 + i * 16 + lr;
-        a_dir[i] = (unsigned)(2 * (row * RD + 8 * (lg ^ direct_key<RD>(row))));
-    }
-
-    const int nsl = (red_hi - red_lo + RD - 1) / RD;
-#pragma unroll
-    for (int t = 0; t < S - 1; ++t)
-        if (t < nsl) issue(t, t);
     if constexpr (MODE == kBwdWQ) {
-        // slices 0 .. S-3 now; slice u >= S-2 is fetched S-1 steps ahead and
-        // written one step later
+        if (nsl > 0) {
+            fetch_codes(0, 0);
+            issue(0, 0);
+            put_codes(0, 0, 0);
+        }
+        if (nsl > 1) {
+            fetch_codes(1, 0);
+            issue(1, 1);
+        }
+        if (nsl > 2) fetch_codes(2, 1);
+    } else {
 #pragma unroll
-        for (int t = 0; t < S - 2; ++t)
-            if (t < nsl) {
-                fetch_codes(t);
-                put_codes(t, t);
-            }
-        if (S - 2 < nsl) fetch_codes(S - 2);
+        for (int t = 0; t < S - 1; ++t)
+            if (t < nsl) issue(t, t);
     }
     int stage = 0;
-    for (int t = 0; t < nsl; ++t) {
-        if constexpr (MODE == kBwdWQ) {
-            // codes of slice t + S - 2 were fetched last step; the wait for
-            // them covers every older load, slice t's included
-            const int st = stage + S - 2 >= S ? stage - 2 : stage + S - 2;
-            if (t + S - 2 < nsl) put_codes(t + S - 2, st);
-        }
-        if (t + S - 2 < nsl) wait_vmem<(NIA + NIB) * (S - 2)>(); else wait_vmem<0>();
+    auto step = [&](int t, auto set_) {
+        constexpr int set = decltype(set_)::value;   // t % 2, for the codes
+        if constexpr (MODE == kBwdWQ)
+            if (t + 1 < nsl) put_codes(t + 1, set, stage == S - 1 ? 0 : stage + 1);
+        wait_slice(t);
         stage_barrier();
-        if (t + S - 1 < nsl) {
-            issue(t + S - 1, stage == 0 ? S - 1 : stage - 1);
-            if constexpr (MODE == kBwdWQ) fetch_codes(t + S - 1);
-        }
-        const uint16_t* ta = ring + stage * kSt;
-        const uint16_t* tb = ta + D::kSliceA;
-        const unsigned sbase = ring_lds + (unsigned)(stage * kSt * 2);
-        v8bf atr[2][4], btr[2][4];
-        const unsigned bs = sbase + (unsigned)(D::kSliceA * 2);
-        if constexpr (!A_TR && B_TR && NB == 1) {
-            const unsigned ad[4] = {sbase + a_dir[0], sbase + a_dir[1], sbase + a_dir[2], sbase + a_dir[3]};
-            const unsigned bd[4] = {bs + b_tr[0], bs + b_tr[1], bs + b_tr[2], bs + b_tr[3]};
-            direct_tr_slice<kHalfB>(atr[0], btr[0], ad, bd);
-        } else if constexpr (A_TR && B_TR && NB == 1) {
-            const unsigned ad[4] = {sbase + a_tr[0], sbase + a_tr[1], sbase + a_tr[2], sbase + a_tr[3]};
-            const unsigned bd[4] = {bs + b_tr[0], bs + b_tr[1], bs + b_tr[2], bs + b_tr[3]};
-            tr_slice_pair<kHalfA, kHalfB>(atr[0], btr[0], ad, bd);
+        if (t + S - 1 < nsl) issue(t + S - 1, stage == 0 ? S - 1 : stage - 1);
+        if constexpr (MODE == kBwdWQ)
+            if (t + S < nsl) fetch_codes(t + S, set);
+        const unsigned so = (unsigned)(stage * kSt * 2);
+        v8bf af[4], bf[NJ];
+        if constexpr (MODE == kBwdX) {
+            read_direct_direct<NJ>(af, bf, ra[0] + so, rb[0] + so);
         } else {
-            if constexpr (A_TR) {
-                const unsigned ad[4] = {sbase + a_tr[0], sbase + a_tr[1], sbase + a_tr[2], sbase + a_tr[3]};
-                tr_slice<NB, kHalfA, kBlkA>(atr, ad);
-            }
-            if constexpr (B_TR) {
-                const unsigned bd[4] = {bs + b_tr[0], bs + b_tr[1], bs + b_tr[2], bs + b_tr[3]};
-                tr_slice<NB, kHalfB, kBlkB>(btr, bd);
+            const unsigned bd[4] = {rb[0] + so, rb[1] + so, rb[2] + so, rb[3] + so};
+            if constexpr (kW) {
+                const unsigned ad[4] = {ra[0] + so, ra[1] + so, ra[2] + so, ra[3] + so};
+                if constexpr (NJ == 8) read_tr_tr8<kHalfA, kHalfB>(af, bf, ad, bd);
+                else tr_slice_pair<kHalfA, kHalfB>(af, bf, ad, bd);
+            } else if constexpr (NJ == 8) {
+                read_direct_tr8<kHalfB>(af, bf, ra[0] + so, bd);
+            } else {
+                const unsigned ad[4] = {ra[0] + so, ra[1] + so, ra[2] + so, ra[3] + so};
+                direct_tr_slice<kHalfB>(af, bf, ad, bd);
             }
         }
-        const int valid = red_hi - (red_lo + t * RD);
+        if constexpr (kW) {   // rows past the group's end repeat its last row: dropped
+            const int valid = red_hi - (red_lo + t * 32);
+            if (valid < 32) {
 #pragma unroll
-        for (int s = 0; s < NB; ++s) {
-            v8bf af[4], bf[4];
+                for (int i = 0; MODE == kBwdW && i < 4; ++i) af[i] = zero_rows_past<kSpread>(af[i], 0, lg, valid);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (A_TR || (B_TR && NB == 1))
-                    af[i] = atr[s][i];
-                else
-                    af[i] = swz_read_direct<RD>(ta, wm * 64 + i * 16 + lr, s * 4 + lg);
+                for (int j = 0; j < NJ; ++j) bf[j] = zero_rows_past<kSpread>(bf[j], 0, lg, valid);
             }
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (B_TR)
-                    bf[j] = btr[s][j];
-                else
-                    bf[j] = swz_read_direct<RD>(tb, wn * 64 + j * 16 + lr, s * 4 + lg);
-            }
-            if constexpr (kW) {   // rows past the group's end repeat its last row: dropped
-                if (valid < RD) {
+        for (int i = 0; i < 4; ++i) {
+            if (i >= nb) break;
 #pragma unroll
-                    for (int i = 0; MODE == kBwdW && i < 4; ++i) af[i] = zero_rows_past<kSpread>(af[i], s, lg, valid);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) bf[j] = zero_rows_past<kSpread>(bf[j], s, lg, valid);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
         }
         stage = stage == S - 1 ? 0 : stage + 1;
+    };
+    if constexpr (MODE == kBwdWQ) {
+        for (int t = 0; t < nsl; t += 2) {
+            step(t, std::integral_constant<int, 0>{});
+            if (t + 1 < nsl) step(t + 1, std::integral_constant<int, 1>{});
+        }
+    } else {
+        for (int t = 0; t < nsl; ++t) step(t, std::integral_constant<int, 0>{});
     }
     __syncthreads();
 
     if constexpr (MODE == kGated) {
-        gated_epilogue<OUT_BF16, SAVE, TR, TC, WN, NTHR>(a, it, acc, ring);
+        gated_epilogue<OUT_BF16, SAVE, NJ>(a, it, acc, ring);
     } else {
-        // each wave stages its 64 x 64 block and stores whole row segments
+        // each wave stages 64 rows x 64 columns at a time and stores whole row
+        // segments; widths are multiples of 64, so a wave's 64 columns are all
+        // inside or all outside
         const int ocols = MODE == kBwdX ? K : NN;
         const int64_t obase = kW ? (int64_t)g * K * NN : 0;
-        const int col0 = c0 + wn * 64;
-        if (col0 >= ocols) return;   // widths are multiples of 64
-        if constexpr (OUT_BF16) {
-            constexpr int kEpiRow = 64 + 8;
-            static_assert(NW * 64 * kEpiRow <= S * kSt, "epilogue staging fits the ring");
-            uint16_t* ep = ring + (tid >> 6) * 64 * kEpiRow;
+        auto tile_row = [&](int r) { return kW ? 64 * wm + r : 32 * (r >> 4) + 16 * wm + (r & 15); };
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < NJ / 4; ++q) {
+            if constexpr (OUT_BF16) {
+                constexpr int kEpiRow = 64 + 8;
+                static_assert(4 * 64 * kEpiRow <= S * kSt, "epilogue staging fits the ring");
+                uint16_t* ep = ring + wave * 64 * kEpiRow;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint2*>(ep + (16 * i + lr) * kEpiRow + 16 * j + 4 * lg) =
-                        make_uint2(pack_rne(acc[i][j][0], acc[i][j][1]), pack_rne(acc[i][j][2], acc[i][j][3]));
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            const int orow = lane >> 3, ocol = (lane & 7) * 8;
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int r = 8 * q + orow;
-                const uint4 v = *reinterpret_cast<const uint4*>(ep + r * kEpiRow + ocol);
-                const int row = row0 + wm * 64 + r;
-                if (row < hi)
-                    store_out(reinterpret_cast<uint16_t*>(a.out) + obase + (int64_t)row * ocols + col0 + ocol, v);
-            }
-        } else {
+                    for (int j = 0; j < 4; ++j) {
+                        const v4f v = acc[i][4 * q + j];
+                        *reinterpret_cast<uint2*>(ep + (16 * i + lr) * kEpiRow + 16 * j + 4 * lg) =
+                            make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]));
+                    }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                const int orow = lane >> 3, ocol = (lane & 7) * 8;
+                const int col = c0 + frag_col<MODE, NJ>(wn, 4 * q + ocol / 16) + ocol % 16;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + wm * 64 + i * 16 + lr;
-                if (row >= hi) continue;
+                for (int p = 0; p < 8; ++p) {
+                    const int r = 8 * p + orow;
+                    const uint4 v = *reinterpret_cast<const uint4*>(ep + r * kEpiRow + ocol);
+                    const int row = row0 + tile_row(r);
+                    if (row < hi && col < ocols)
+                        store_out(reinterpret_cast<uint16_t*>(a.out) + obase + (int64_t)row * ocols + col, v);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + obase + (int64_t)row * ocols + col0 + 16 * j + 4 * lg) =
-                        make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = row0 + tile_row(16 * i + lr);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int col = c0 + frag_col<MODE, NJ>(wn, 4 * q + j) + 4 * lg;
+                        if (row < hi && col < ocols)
+                            *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.out) + obase + (int64_t)row * ocols + col) =
+                                acc[i][4 * q + j];
+                    }
+                }
             }
         }
     }
 }
 
-template <int MODE, bool OUT_BF16, int SAVE, int S, int RES, int WM, int WN>
+template <int MODE, bool OUT_BF16, int SAVE, int NJ>
 hipError_t launch(FfnArgs a, hipStream_t stream) {
-    constexpr int TR = 64 * WM, TC = 64 * WN;
+    using T = FfnTile<NJ>;
     int64_t nblocks;
     if constexpr (MODE == kBwdW || MODE == kBwdWQ) {
-        a.ntiles_r = (a.K + TR - 1) / TR;
-        a.ntiles_c = (a.NN + TC - 1) / TC;
+        a.ntiles_r = (a.K + T::kTR - 1) / T::kTR;
+        a.ntiles_c = (a.NN + T::kTC - 1) / T::kTC;
         nblocks = (int64_t)a.G * a.ntiles_r * a.ntiles_c;
     } else {
-        const int cols = MODE == kGated ? a.NN / 2 : a.K, tc = MODE == kGated ? TC / 2 : TC;
+        const int cols = MODE == kGated ? a.NN / 2 : a.K, tc = MODE == kGated ? T::kTC / 2 : T::kTC;
         a.ntiles_r = 0;
         a.ntiles_c = (cols + tc - 1) / tc;
-        nblocks = max_work_items(a.M, a.G < a.M ? a.G : a.M, TR) * a.ntiles_c;
+        nblocks = max_work_items(a.M, a.G < a.M ? a.G : a.M, T::kTR) * a.ntiles_c;
     }
     if (nblocks > 0x7fffffff) return hipErrorInvalidConfiguration;
     a.nblocks = (int)nblocks;
-    hipLaunchKernelGGL((ffn_kernel<MODE, OUT_BF16, SAVE, S, RES, WM, WN>), dim3((unsigned)nblocks), dim3(64 * WM * WN),
-                       0, stream, a);
+    hipLaunchKernelGGL((ffn_kernel<MODE, OUT_BF16, SAVE, NJ>), dim3((unsigned)nblocks), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -614,7 +835,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     FfnItem it;
-    if (!ffn_item<kGated, TR, 2 * CT, NTHR>(a, s_info, it)) return;
+    if (!ffn_item<kGated, TR, 2 * CT>(a, s_info, it)) return;
     if (it.g == a.G) {
         zero_tail<kGated, OUT_BF16, SAVE, 2 * CT, NTHR>(a, it);
         return;
@@ -747,23 +968,19 @@ hipError_t launch_few(FfnArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int MODE, int SAVE = kSaveNone>
-hipError_t launch_any(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    return out_bf16 ? launch<MODE, true, SAVE, 3, 3, 2, 2>(a, stream) : launch<MODE, false, SAVE, 3, 3, 2, 2>(a, stream);
+// 256 columns a tile or 128.  The wide tile reads its rows half as often and
+// feeds each MFMA from fewer LDS reads, but two workgroups fill a CU instead
+// of three smaller ones: it pays once the narrow tiles would need more than
+// one round of the chip (three a CU) and the columns do not leave more than a
+// sixth of it unused.  Measured (us, 128 / 256 columns; shard: 8192 rows, 32
+// experts, K = 2048, 2N = 1024; production: 65536 rows, 256 experts): forward
+// shard 73.7 / 75.9, production 465 / 385; dX 73.9 / 72.4, 502 / 461; weight
+// gradient 63.0 / 60.3, 607 / 522 (dX and the gradient with the 11 and 75 us
+// of the activation's gradient in both figures).
+bool wide_tiles(int64_t row_tiles, int64_t cols) {
+    const int64_t wide = (cols + 255) / 256;
+    return row_tiles * ((cols + 127) / 128) > 3 * device_cus() && wide * 256 * 5 <= cols * 6;
 }
-
-}  // namespace
-
-int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G) {
-    // of the 128-row tiles; the few-row form only takes grids near the chip's size
-    return max_work_items(M, G < M ? G : M, 128) * ((N + 63) / 64);
-}
-
-int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G) {
-    return max_work_items(M, G < M ? G : M, 128) * ((K + 127) / 128);
-}
-
-int64_t ffn_dw_blocks(int64_t K, int64_t NN, int64_t G) { return G * ((K + 127) / 128) * ((NN + 127) / 128); }
 
 // The few-row form is for grids that the 128-row tiles leave unfilled.  With
 // B busy experts (at most min(G, M)) of few rows each, those tiles make B N/64
@@ -791,8 +1008,31 @@ hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
         if (rows <= 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, busy, stream);
         return launch_few_mb<OUT_BF16, SAVE, 4>(a, busy, stream);
     }
-    return launch<kGated, OUT_BF16, SAVE, 3, 3, 2, 2>(a, stream);
+    return wide_tiles(max_work_items(a.M, busy, 128), a.NN) ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream)
+                                                            : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
 }
+
+template <int MODE>
+hipError_t launch_bwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
+    const int64_t rows = MODE == kBwdX ? max_work_items(a.M, a.G < a.M ? a.G : a.M, 128)
+                                       : (int64_t)a.G * ((a.K + 127) / 128);
+    if (wide_tiles(rows, MODE == kBwdX ? a.K : a.NN))
+        return out_bf16 ? launch<MODE, true, kSaveNone, 8>(a, stream) : launch<MODE, false, kSaveNone, 8>(a, stream);
+    return out_bf16 ? launch<MODE, true, kSaveNone, 4>(a, stream) : launch<MODE, false, kSaveNone, 4>(a, stream);
+}
+
+}  // namespace
+
+int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G) {
+    // of the 128-row tiles; the few-row form only takes grids near the chip's size
+    return max_work_items(M, G < M ? G : M, 128) * ((N + 63) / 64);
+}
+
+int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G) {
+    return max_work_items(M, G < M ? G : M, 128) * ((K + 127) / 128);
+}
+
+int64_t ffn_dw_blocks(int64_t K, int64_t NN, int64_t G) { return G * ((K + 127) / 128) * ((NN + 127) / 128); }
 
 hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
     if (a.gu_q != nullptr) return out_bf16 ? launch_gated<kSaveMx8, true>(a, stream) : launch_gated<kSaveMx8, false>(a, stream);
@@ -801,11 +1041,11 @@ hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream)
 }
 
 hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    return launch_any<kBwdX>(a, out_bf16, stream);
+    return launch_bwd<kBwdX>(a, out_bf16, stream);
 }
 
 hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    return a.aq != nullptr ? launch_any<kBwdWQ>(a, out_bf16, stream) : launch_any<kBwdW>(a, out_bf16, stream);
+    return a.aq != nullptr ? launch_bwd<kBwdWQ>(a, out_bf16, stream) : launch_bwd<kBwdW>(a, out_bf16, stream);
 }
 
 }  // namespace gmm

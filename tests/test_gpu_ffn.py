@@ -550,3 +550,32 @@ FEW = [
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 def test_forward_few_rows(shape, save, dt):
     test_forward(shape, save, dt)
+
+
+# Grids large enough for the tiles of 256 columns (forward and dw; dX), full and partly filled.
+WIDE = [
+    ([2, 0, 5] * 50, 400, 64, 512),
+    ([140, 3, 0, 200, 129] * 8, 3800, 128, 1344),
+    ([140, 3, 0, 200, 129] * 8, 3800, 1344, 64),
+]
+WIDE_IDS = ["M%d_K%d_N%d_G%d" % (M, K, N, len(s)) for s, M, K, N in WIDE]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=WIDE_IDS)
+@pytest.mark.parametrize("save", ["none", "bf16", "mx8"])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_forward_wide(shape, save, dt):
+    test_forward(shape, save, dt)
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=WIDE_IDS)
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mx8"])
+@pytest.mark.parametrize("dxt,dwt", [(BF, BF), (F32, F32)], ids=["bf16", "f32"])
+def test_backward_wide(shape, mx, dxt, dwt):
+    test_backward(shape, mx, dxt, dwt)
+
+
+@pytest.mark.parametrize("shape", [([70, 0, 33] * 20, 2100, 256, 1088)], ids=["G60"])
+@pytest.mark.parametrize("dwt", [BF, F32], ids=["bf16", "f32"])
+def test_weight_gradient_wide(shape, dwt):
+    test_weight_gradient(shape, dwt)
