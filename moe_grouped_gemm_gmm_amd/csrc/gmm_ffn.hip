@@ -17,6 +17,7 @@
 #include "gmm_mx8.hpp"
 #include "gmm_tile.hpp"
 
+#include <cmath>
 #include <type_traits>
 
 namespace gmm {
@@ -57,9 +58,8 @@ __device__ __forceinline__ WorkItem even_item(int g, int glo, int ghi, int idx, 
     return it;
 }
 
-template <int CAP>
-__device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ group_sizes, int G, int M, int ntiles,
-                                                   int b, int& col) {
+__device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ group_sizes, int G, int M, int cap,
+                                                   int ntiles, int b, int& col) {
     col = 0;
     const int lane = lane_id();
     // Up to 256 groups the clamped ranges and item offsets stay in registers,
@@ -78,7 +78,7 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
                 lo[k] = ch.lo;
                 hi[k] = ch.hi;
                 carry = ch.next_carry;
-                cn[k] = group_items<true>(ch.lo, ch.hi, CAP);
+                cn[k] = group_items<true>(ch.lo, ch.hi, cap);
                 const int incl = wave_incl_scan(cn[k]);
                 W[k] = items + incl - cn[k];
                 items += lane_value(incl, 63);
@@ -88,15 +88,15 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
         for (int base = 0; base < G; base += 64) {
             const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
             carry = ch.next_carry;
-            items += lane_value(wave_incl_scan(group_items<true>(ch.lo, ch.hi, CAP)), 63);
+            items += lane_value(wave_incl_scan(group_items<true>(ch.lo, ch.hi, cap)), 63);
         }
     }
     const int total = min(carry, M);
-    const int L = xcd_balance(b, (items + tail_items<true>(total, M, CAP)) * ntiles);
+    const int L = xcd_balance(b, (items + tail_items<true>(total, M, cap)) * ntiles);
     if (L < 0) return WorkItem{-1, 0, 0, 0};
     const int w = L / ntiles;
     col = L % ntiles;
-    if (w >= items) return tail_item<true>(G, M, total, items, CAP, w);
+    if (w >= items) return tail_item<true>(G, M, total, items, cap, w);
     if (inreg) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -104,7 +104,7 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
             if (m) {
                 const int src = __ffsll((long long)m) - 1;
                 return even_item(64 * k + src, lane_value(lo[k], src), lane_value(hi[k], src),
-                                 w - lane_value(W[k], src), CAP);
+                                 w - lane_value(W[k], src), cap);
             }
         }
     } else {
@@ -113,12 +113,12 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
         for (int base = 0; base < G; base += 64) {
             const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
             carry = ch.next_carry;
-            const int c = group_items<true>(ch.lo, ch.hi, CAP), incl = wave_incl_scan(c), Wb = first + incl - c;
+            const int c = group_items<true>(ch.lo, ch.hi, cap), incl = wave_incl_scan(c), Wb = first + incl - c;
             const unsigned long long m = __ballot(c > 0 && w >= Wb && w < Wb + c);
             if (m) {
                 const int src = __ffsll((long long)m) - 1;
                 return even_item(base + src, lane_value(ch.lo, src), lane_value(ch.hi, src), w - lane_value(Wb, src),
-                                 CAP);
+                                 cap);
             }
             first += lane_value(incl, 63);
         }
@@ -127,8 +127,9 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
 }
 
 // Work item of a workgroup; every mode's block 0 also writes the call's
-// device status word.  TR x TC: tile rows and columns of the product.
-template <int MODE, int TR, int TC>
+// device status word.  TR x TC: tile rows and columns of the product; CAP: rows
+// an item may have (0: a.cap of them).
+template <int MODE, int TR, int TC, int CAP = TR>
 __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int* s_info, FfnItem& it) {
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     if (wave == 1 && blockIdx.x == 0) {
@@ -154,7 +155,7 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int* s_info, FfnItem&
     } else {
         if (wave == 0) {
             int col;
-            const WorkItem wi = even_work_item<TR>(a.group_sizes, a.G, a.M, a.ntiles_c, blockIdx.x, col);
+            const WorkItem wi = even_work_item(a.group_sizes, a.G, a.M, CAP > 0 ? CAP : a.cap, a.ntiles_c, blockIdx.x, col);
             if (lane == 0) { s_info[0] = wi.g; s_info[1] = wi.lo; s_info[2] = wi.hi; s_info[3] = col; }
         }
         __syncthreads();
@@ -736,6 +737,524 @@ hipError_t launch(FfnArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// ----------------------------------------- 160 x 256 tiles, load waves --
+// The forward and dX on tiles of up to 160 rows x 256 columns, one workgroup
+// per CU: 8 waves (2 x 4) multiply, each 80 x 64 in 32 x 32 x 16 MFMAs, and 4
+// waves do nothing but issue the loads into a ring of 3 stages, 64 deep (156
+// KB).  A CU holds about 22 KB of cache misses in flight (a bare stream of
+// load-to-LDS instructions reaches 38 GB/s per CU whatever the depth of its
+// ring), and a load-to-LDS instruction beyond that waits at issue, with the
+// wave that issues it: in a wave that also multiplies the two times add up.
+// Direct rows are loaded 128 bytes at a time, whole cache lines (in 64-byte
+// pieces, 32 deep, the rows of x cost the shard's forward 14 of its 56 us).
+//
+// With two multiplying waves per SIMD the LDS reads cannot hide behind other
+// waves, so they are interleaved with the MFMAs of the quarter step before
+// (ws_step).  One barrier a stage: at the barrier of step u the multiplying
+// waves have read all of stage u and the load waves have waited for stage
+// u + 1; after it stage u + 1 may be read and slice u + 3 loaded over slice u.
+//
+// The wave rows take alternate 32-row blocks and a wave multiplies only its
+// blocks that hold rows (a loop compiled for each count), so an item's cost
+// follows its rows; 8 rows of A past the item's end are not loaded.
+//
+// LDS layout: direct operands as 128-byte rows, chunk c of row r at c ^ (r %
+// 8); transposed B as two slices of 32 rows x 512 bytes, 32-byte chunk k of
+// row r at k ^ (2 (r % 4)): one pass of a transposed read covers rows 4n ..
+// 4n+3 of two neighbouring chunks.
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// One quarter step of a wave: the products of 16 reduction indices (NB 32-row
+// blocks x 2 column blocks of 32 x 32 x 16) with the fragments already in
+// registers, and between them the LDS reads of the next 16, all in one asm
+// block that waits for its reads at its end, so that they take the matrix
+// unit's time and no register is read before its load.  A comes from NB
+// direct fragments 8192 bytes apart; B from two transposed fragments 256 bytes
+// apart, second halves 2048 bytes on (BTR), or two direct ones 4096 bytes
+// apart.  OB is added to transposed B's address.
+template <int OB>
+__device__ __forceinline__ void ws_step(std::integral_constant<int, 1>, std::integral_constant<bool, true>, v16f (&acc)[3][2],
+                                         const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
+                                         unsigned b) {
+    v4i na0;
+    u64 nb0, nb1, nb2, nb3;
+    asm volatile(
+        "s_nop 1\n\t"
+        "v_mfma_f32_32x32x16_bf16 %0, %8, %7, %0\n\t"
+        "ds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %4, %11 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %5, %11 offset:%14\n\t"
+        "v_mfma_f32_32x32x16_bf16 %1, %9, %7, %1\n\t"
+        "ds_read_b64_tr_b16 %6, %11 offset:%15\n\t"
+        "ds_read_b128 %2, %10 offset:0\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "+v"(acc[0][0]), "+v"(acc[0][1]),
+          "=&v"(na0), "=&v"(nb0), "=&v"(nb1), "=&v"(nb2), "=&v"(nb3)
+        : "v"(fa[0]), "v"(fb[0]), "v"(fb[1]), "v"(a), "v"(b),
+          "i"(OB), "i"(OB + 2048), "i"(OB + 256), "i"(OB + 2304)
+        : "memory");
+    ga[0] = __builtin_bit_cast(v8bf, na0);
+    gb[0] = __builtin_bit_cast(v8bf, u64x2{nb0, nb1});
+    gb[1] = __builtin_bit_cast(v8bf, u64x2{nb2, nb3});
+}
+
+template <int OB>
+__device__ __forceinline__ void ws_step(std::integral_constant<int, 1>, std::integral_constant<bool, false>, v16f (&acc)[3][2],
+                                         const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
+                                         unsigned b) {
+    v4i na0;
+    v4i nb0, nb1;
+    asm volatile(
+        "s_nop 1\n\t"
+        "v_mfma_f32_32x32x16_bf16 %0, %6, %5, %0\n\t"
+        "ds_read_b128 %3, %9 offset:%10\n\t"
+        "ds_read_b128 %4, %9 offset:%11\n\t"
+        "v_mfma_f32_32x32x16_bf16 %1, %7, %5, %1\n\t"
+        "ds_read_b128 %2, %8 offset:0\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "+v"(acc[0][0]), "+v"(acc[0][1]),
+          "=&v"(na0), "=&v"(nb0), "=&v"(nb1)
+        : "v"(fa[0]), "v"(fb[0]), "v"(fb[1]), "v"(a), "v"(b),
+          "i"(0), "i"(4096)
+        : "memory");
+    ga[0] = __builtin_bit_cast(v8bf, na0);
+    gb[0] = __builtin_bit_cast(v8bf, nb0);
+    gb[1] = __builtin_bit_cast(v8bf, nb1);
+}
+
+template <int OB>
+__device__ __forceinline__ void ws_step(std::integral_constant<int, 2>, std::integral_constant<bool, true>, v16f (&acc)[3][2],
+                                         const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
+                                         unsigned b) {
+    v4i na0, na1;
+    u64 nb0, nb1, nb2, nb3;
+    asm volatile(
+        "s_nop 1\n\t"
+        "v_mfma_f32_32x32x16_bf16 %0, %12, %10, %0\n\t"
+        "ds_read_b64_tr_b16 %6, %15 offset:%16\n\t"
+        "ds_read_b64_tr_b16 %7, %15 offset:%17\n\t"
+        "v_mfma_f32_32x32x16_bf16 %1, %13, %10, %1\n\t"
+        "ds_read_b64_tr_b16 %8, %15 offset:%18\n\t"
+        "ds_read_b64_tr_b16 %9, %15 offset:%19\n\t"
+        "v_mfma_f32_32x32x16_bf16 %2, %12, %11, %2\n\t"
+        "ds_read_b128 %4, %14 offset:0\n\t"
+        "ds_read_b128 %5, %14 offset:8192\n\t"
+        "v_mfma_f32_32x32x16_bf16 %3, %13, %11, %3\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]),
+          "=&v"(na0), "=&v"(na1), "=&v"(nb0), "=&v"(nb1), "=&v"(nb2), "=&v"(nb3)
+        : "v"(fa[0]), "v"(fa[1]), "v"(fb[0]), "v"(fb[1]), "v"(a), "v"(b),
+          "i"(OB), "i"(OB + 2048), "i"(OB + 256), "i"(OB + 2304)
+        : "memory");
+    ga[0] = __builtin_bit_cast(v8bf, na0);
+    ga[1] = __builtin_bit_cast(v8bf, na1);
+    gb[0] = __builtin_bit_cast(v8bf, u64x2{nb0, nb1});
+    gb[1] = __builtin_bit_cast(v8bf, u64x2{nb2, nb3});
+}
+
+template <int OB>
+__device__ __forceinline__ void ws_step(std::integral_constant<int, 2>, std::integral_constant<bool, false>, v16f (&acc)[3][2],
+                                         const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
+                                         unsigned b) {
+    v4i na0, na1;
+    v4i nb0, nb1;
+    asm volatile(
+        "s_nop 1\n\t"
+        "v_mfma_f32_32x32x16_bf16 %0, %10, %8, %0\n\t"
+        "ds_read_b128 %6, %13 offset:%14\n\t"
+        "v_mfma_f32_32x32x16_bf16 %1, %11, %8, %1\n\t"
+        "ds_read_b128 %7, %13 offset:%15\n\t"
+        "v_mfma_f32_32x32x16_bf16 %2, %10, %9, %2\n\t"
+        "ds_read_b128 %4, %12 offset:0\n\t"
+        "v_mfma_f32_32x32x16_bf16 %3, %11, %9, %3\n\t"
+        "ds_read_b128 %5, %12 offset:8192\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]),
+          "=&v"(na0), "=&v"(na1), "=&v"(nb0), "=&v"(nb1)
+        : "v"(fa[0]), "v"(fa[1]), "v"(fb[0]), "v"(fb[1]), "v"(a), "v"(b),
+          "i"(0), "i"(4096)
+        : "memory");
+    ga[0] = __builtin_bit_cast(v8bf, na0);
+    ga[1] = __builtin_bit_cast(v8bf, na1);
+    gb[0] = __builtin_bit_cast(v8bf, nb0);
+    gb[1] = __builtin_bit_cast(v8bf, nb1);
+}
+
+template <int OB>
+__device__ __forceinline__ void ws_step(std::integral_constant<int, 3>, std::integral_constant<bool, true>, v16f (&acc)[3][2],
+                                         const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
+                                         unsigned b) {
+    v4i na0, na1, na2;
+    u64 nb0, nb1, nb2, nb3;
+    asm volatile(
+        "s_nop 1\n\t"
+        "v_mfma_f32_32x32x16_bf16 %0, %16, %13, %0\n\t"
+        "ds_read_b64_tr_b16 %9, %19 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %10, %19 offset:%21\n\t"
+        "v_mfma_f32_32x32x16_bf16 %1, %17, %13, %1\n\t"
+        "ds_read_b64_tr_b16 %11, %19 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %12, %19 offset:%23\n\t"
+        "v_mfma_f32_32x32x16_bf16 %2, %16, %14, %2\n\t"
+        "ds_read_b128 %6, %18 offset:0\n\t"
+        "ds_read_b128 %7, %18 offset:8192\n\t"
+        "v_mfma_f32_32x32x16_bf16 %3, %17, %14, %3\n\t"
+        "ds_read_b128 %8, %18 offset:16384\n\t"
+        "v_mfma_f32_32x32x16_bf16 %4, %16, %15, %4\n\t"
+        "v_mfma_f32_32x32x16_bf16 %5, %17, %15, %5\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]), "+v"(acc[2][1]),
+          "=&v"(na0), "=&v"(na1), "=&v"(na2), "=&v"(nb0), "=&v"(nb1), "=&v"(nb2), "=&v"(nb3)
+        : "v"(fa[0]), "v"(fa[1]), "v"(fa[2]), "v"(fb[0]), "v"(fb[1]), "v"(a), "v"(b),
+          "i"(OB), "i"(OB + 2048), "i"(OB + 256), "i"(OB + 2304)
+        : "memory");
+    ga[0] = __builtin_bit_cast(v8bf, na0);
+    ga[1] = __builtin_bit_cast(v8bf, na1);
+    ga[2] = __builtin_bit_cast(v8bf, na2);
+    gb[0] = __builtin_bit_cast(v8bf, u64x2{nb0, nb1});
+    gb[1] = __builtin_bit_cast(v8bf, u64x2{nb2, nb3});
+}
+
+template <int OB>
+__device__ __forceinline__ void ws_step(std::integral_constant<int, 3>, std::integral_constant<bool, false>, v16f (&acc)[3][2],
+                                         const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
+                                         unsigned b) {
+    v4i na0, na1, na2;
+    v4i nb0, nb1;
+    asm volatile(
+        "s_nop 1\n\t"
+        "v_mfma_f32_32x32x16_bf16 %0, %14, %11, %0\n\t"
+        "ds_read_b128 %9, %17 offset:%18\n\t"
+        "v_mfma_f32_32x32x16_bf16 %1, %15, %11, %1\n\t"
+        "ds_read_b128 %10, %17 offset:%19\n\t"
+        "v_mfma_f32_32x32x16_bf16 %2, %14, %12, %2\n\t"
+        "ds_read_b128 %6, %16 offset:0\n\t"
+        "v_mfma_f32_32x32x16_bf16 %3, %15, %12, %3\n\t"
+        "ds_read_b128 %7, %16 offset:8192\n\t"
+        "v_mfma_f32_32x32x16_bf16 %4, %14, %13, %4\n\t"
+        "ds_read_b128 %8, %16 offset:16384\n\t"
+        "v_mfma_f32_32x32x16_bf16 %5, %15, %13, %5\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]), "+v"(acc[2][1]),
+          "=&v"(na0), "=&v"(na1), "=&v"(na2), "=&v"(nb0), "=&v"(nb1)
+        : "v"(fa[0]), "v"(fa[1]), "v"(fa[2]), "v"(fb[0]), "v"(fb[1]), "v"(a), "v"(b),
+          "i"(0), "i"(4096)
+        : "memory");
+    ga[0] = __builtin_bit_cast(v8bf, na0);
+    ga[1] = __builtin_bit_cast(v8bf, na1);
+    ga[2] = __builtin_bit_cast(v8bf, na2);
+    gb[0] = __builtin_bit_cast(v8bf, nb0);
+    gb[1] = __builtin_bit_cast(v8bf, nb1);
+}
+
+// The reads alone, before the first quarter step (all three blocks of A).
+template <bool BTR>
+__device__ __forceinline__ void ws_read(v8bf (&ga)[3], v8bf (&gb)[2], unsigned a, unsigned b) {
+    v4i d[3], e[2];
+    u64 o[4];
+    if constexpr (BTR) {
+        asm volatile(
+            "ds_read_b128 %0, %7\n\t"
+            "ds_read_b128 %1, %7 offset:8192\n\t"
+            "ds_read_b128 %2, %7 offset:16384\n\t"
+            "ds_read_b64_tr_b16 %3, %8\n\t"
+            "ds_read_b64_tr_b16 %4, %8 offset:2048\n\t"
+            "ds_read_b64_tr_b16 %5, %8 offset:256\n\t"
+            "ds_read_b64_tr_b16 %6, %8 offset:2304\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3])
+            : "v"(a), "v"(b)
+            : "memory");
+        gb[0] = __builtin_bit_cast(v8bf, u64x2{o[0], o[1]});
+        gb[1] = __builtin_bit_cast(v8bf, u64x2{o[2], o[3]});
+    } else {
+        asm volatile(
+            "ds_read_b128 %0, %5\n\t"
+            "ds_read_b128 %1, %5 offset:8192\n\t"
+            "ds_read_b128 %2, %5 offset:16384\n\t"
+            "ds_read_b128 %3, %6\n\t"
+            "ds_read_b128 %4, %6 offset:4096\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(d[0]), "=&v"(d[1]), "=&v"(d[2]), "=&v"(e[0]), "=&v"(e[1])
+            : "v"(a), "v"(b)
+            : "memory");
+        gb[0] = __builtin_bit_cast(v8bf, e[0]);
+        gb[1] = __builtin_bit_cast(v8bf, e[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) ga[i] = __builtin_bit_cast(v8bf, d[i]);
+}
+
+constexpr int kWsRows = 160, kWsCols = 256, kWsStages = 3, kWsThreads = 768;
+constexpr int kWsSliceA = kWsRows * 64, kWsSliceB = kWsCols * 64, kWsStage = kWsSliceA + kWsSliceB;   // elements
+constexpr int kWsBytes = kWsStages * kWsStage * 2;
+static_assert(kWsBytes <= 163840 - 1024, "the ring fits the LDS");
+
+// Stages rows of E in LDS and stores them: VAL(i, q, v) gives the four values of
+// row block i, columns 8q + 4 (lane / 32) .. +3 of each of the wave's NC column
+// blocks of 32 (at column wcol + 32 b of the tile of WID columns).
+template <typename E, int WID, int NC, typename Val>
+__device__ __forceinline__ void ws_store(E* out, int64_t ld, int row0, int rows, int col0, int cols, int wcol,
+                                          uint16_t* sm, bool mul, Val val) {
+    constexpr int C = 16 / (int)sizeof(E), P = WID + C;
+    constexpr int kFit = kWsBytes / (64 * P * (int)sizeof(E)), RI = kFit >= 3 ? 3 : kFit;
+    static_assert(kFit >= 1, "64 staged rows fit the ring");
+    const int tid = threadIdx.x, lane = lane_id(), wm = tid >> 8;
+    E* s = reinterpret_cast<E*>(sm);
+#pragma unroll
+    for (int i0 = 0; i0 < 3; i0 += RI) {
+        if (64 * i0 >= rows) break;
+        if (mul)
+#pragma unroll
+        for (int i = 0; i < (RI < 3 - i0 ? RI : 3 - i0); ++i)
+#pragma unroll
+            for (int b = 0; b < NC; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[4];
+                    val(i0 + i, b, q, v);
+                    E* d = s + (64 * i + 32 * wm + (lane & 31)) * P + wcol + 32 * b + 8 * q + 4 * (lane >> 5);
+                    if constexpr (sizeof(E) == 2)
+                        *reinterpret_cast<uint2*>(d) = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]));
+                    else
+                        *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+        __syncthreads();
+        const int n = min(rows - 64 * i0, 64 * RI);
+        for (int e = tid; e < n * (WID / C); e += kWsThreads) {
+            const int r = e / (WID / C), c = (e % (WID / C)) * C;
+            if (col0 + c < cols)
+                store_out(out + (int64_t)(row0 + 64 * i0 + r) * ld + col0 + c,
+                          *reinterpret_cast<const uint4*>(s + r * P + c));
+        }
+        __syncthreads();
+    }
+}
+
+template <int MODE, bool OUT_BF16, int SAVE>
+__global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) {
+    static_assert(MODE == kGated || MODE == kBwdX, "forward and dX");
+    constexpr int S = kWsStages, kSt = kWsStage;
+    constexpr bool kBTr = MODE == kGated;
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[S * kSt];
+    __shared__ int s_info[5];
+    const int tid = threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    FfnItem it;
+    if (!ffn_item<MODE, kWsRows, kWsCols, 0>(a, s_info, it)) return;
+    if (it.g == a.G) {
+        zero_tail<MODE, OUT_BF16, SAVE, kWsCols, kWsThreads>(a, it);
+        return;
+    }
+    const int K = a.K, NN = a.NN, N = NN / 2;
+    const int row0 = it.row0, hi = it.hi, c0 = it.c0, red = it.red_hi;
+    const int lda = MODE == kGated ? K : NN;
+    const uint16_t* wg = a.b + (int64_t)it.g * K * NN;
+
+    const int rows = hi - row0, nsl = red >> 6;
+    const bool mul = wave < 8;
+    v16f acc[3][2];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const int wm = (wave >> 2) & 1, wn = wave & 3, l32 = lane & 31, h = lane >> 5;
+
+    if (!mul) {
+        // ---- load waves, 1 KB an instruction: 8 rows of a direct operand or 2 of
+        //      transposed B.  Wave p has A's instructions p, p + 4, .. (those that
+        //      hold rows) and eight of B's 32.
+        const int p = wave - 8;
+        int na = 0;
+        const uint16_t *pa[5], *pb[8];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const DmaLane d = dma_direct<64, 8, 8>(p + 4 * i, lane);
+            na += 8 * (p + 4 * i) < rows;
+            pa[i] = a.a + (int64_t)min(row0 + d.row, hi - 1) * lda + d.col;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = p + 4 * i;
+            if constexpr (kBTr) {
+                const int r = 2 * j + (lane >> 5), c = (lane & 31) >> 1;   // row r of 64: slice r / 32
+                const int tc = 16 * (c ^ (2 * (r & 3))) + 8 * (lane & 1);
+                const int col = tc < 128 ? min(c0 + tc, N - 8) : N + min(c0 + tc - 128, N - 8);
+                pb[i] = wg + (int64_t)r * NN + col;
+            } else {
+                const DmaLane d = dma_direct<64, 8, 8>(j, lane);
+                pb[i] = wg + (int64_t)min(c0 + d.row, K - 1) * NN + d.col;
+            }
+        }
+        const int64_t bstep = kBTr ? 64 * (int64_t)NN : 64;
+        auto issue = [&](int t, int stage) {
+            uint16_t* sa = ring + stage * kSt + 512 * p;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint16_t* q = pb[i] + bstep * t;
+                __builtin_amdgcn_global_load_lds(q, (GMM_LDS void*)(sa + kWsSliceA + 2048 * i), 16, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                if (i >= na) break;
+                const uint16_t* q = pa[i] + 64 * t;
+                __builtin_amdgcn_global_load_lds(q, (GMM_LDS void*)(sa + 2048 * i), 16, 0, 0);
+            }
+        };
+        // this wave's share of a stage has landed when at most `younger` stages
+        // of 8 + na loads are outstanding (all of them, near the end)
+        auto wait_younger = [&](bool last, auto younger) {
+            constexpr int n = decltype(younger)::value;
+            if (last) wait_vmem<0>();
+            else if (na == 5) wait_vmem<13 * n>();
+            else if (na == 4) wait_vmem<12 * n>();
+            else if (na == 3) wait_vmem<11 * n>();
+            else if (na == 2) wait_vmem<10 * n>();
+            else if (na == 1) wait_vmem<9 * n>();
+            else wait_vmem<8 * n>();
+        };
+#pragma unroll
+        for (int t = 0; t < S; ++t)
+            if (t < nsl) issue(t, t);
+        wait_younger(S - 1 >= nsl, std::integral_constant<int, S - 1>{});   // stage 0
+        stage_barrier();
+        int stage = 0;
+        for (int t = 0; t < nsl; ++t) {
+            wait_younger(t + S - 1 >= nsl, std::integral_constant<int, S - 2>{});   // stage t + 1
+            stage_barrier();
+            if (t + S < nsl) issue(t + S, stage);
+            stage = stage == S - 1 ? 0 : stage + 1;
+        }
+    } else {
+    const unsigned ring_lds = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)ring;
+    unsigned ra[4], rb[4];   // of the four quarter steps, stage 0
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int row = 32 * wm + l32;
+        ra[s] = ring_lds + (unsigned)(128 * row + 16 * ((2 * s + h) ^ direct_key<64>(row)));
+        if constexpr (kBTr) {
+            const int r = 8 * h + ((lane & 15) >> 2);
+            rb[s] = ring_lds + (unsigned)(2 * kWsSliceA + 512 * r + 32 * ((2 * wn + ((lane >> 4) & 1)) ^ (2 * (r & 3))) +
+                                          8 * (lane & 3));
+        } else {
+            const int br = 64 * wn + l32;
+            rb[s] = ring_lds + (unsigned)(2 * kWsSliceA + 128 * br + 16 * ((2 * s + h) ^ direct_key<64>(br)));
+        }
+    }
+    stage_barrier();   // stage 0 is in
+    auto main_loop = [&](auto nbc) {
+        constexpr int NB = decltype(nbc)::value;
+        constexpr std::integral_constant<bool, kBTr> btr;
+        v8bf fa[3], fb[2], ga[3], gb[2];
+        if constexpr (NB > 0) ws_read<kBTr>(fa, fb, ra[0], rb[0]);
+        int stage = 0;
+        for (int t = 0; t < nsl; ++t) {
+            const int next = stage == S - 1 ? 0 : stage + 1;
+            const unsigned so = (unsigned)(stage * kSt * 2), so1 = (unsigned)(next * kSt * 2);
+            if constexpr (NB > 0) {   // transposed B: 16 rows on, the second slice, its rows 16 on
+                ws_step<8192>(nbc, btr, acc, fa, fb, ga, gb, ra[1] + so, rb[1] + so);
+                ws_step<16384>(nbc, btr, acc, ga, gb, fa, fb, ra[2] + so, rb[2] + so);
+                ws_step<24576>(nbc, btr, acc, fa, fb, ga, gb, ra[3] + so, rb[3] + so);
+            }
+            stage_barrier();
+            // past the last stage this reads one that nothing uses
+            if constexpr (NB > 0) ws_step<0>(nbc, btr, acc, ga, gb, fa, fb, ra[0] + so1, rb[0] + so1);
+            stage = next;
+        }
+    };
+    switch (((rows + 31) / 32 + 1 - wm) >> 1) {   // this wave's 32-row blocks that hold rows
+        case 0: main_loop(std::integral_constant<int, 0>{}); break;
+        case 1: main_loop(std::integral_constant<int, 1>{}); break;
+        case 2: main_loop(std::integral_constant<int, 2>{}); break;
+        default: main_loop(std::integral_constant<int, 3>{}); break;
+    }
+    // the compiler does not see the MFMAs: let the last ones finish before
+    // their results are read
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]),
+                   "+v"(acc[2][1]));
+    }
+    __syncthreads();
+
+    if constexpr (MODE == kGated) {
+        if constexpr (SAVE == kSaveBf16) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                ws_store<uint16_t, 128, 1>(a.gu + p * N, NN, row0, rows, c0, N, 32 * wn, ring, mul,
+                                            [&](int i, int, int q, float (&v)[4]) {
+#pragma unroll
+                                                for (int k = 0; k < 4; ++k) v[k] = acc[i][p][4 * q + k];
+                                            });
+        }
+        if constexpr (SAVE == kSaveMx8) {
+            // a wave's 32 gate (or up) columns of a row are one block, in lanes l and l + 32
+            constexpr int P = 256 + 16;
+            uint8_t* cm = reinterpret_cast<uint8_t*>(ring);
+            uint8_t* ss = cm + 192 * P;
+            static_assert(192 * P + 192 * 8 <= kWsBytes, "checkpoint staging fits the ring");
+            if (mul)
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) m = max(m, abs_bits(acc[i][p][r]));
+                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                    const u32x2 sw = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+                    const uint32_t c = mx8_scale_code(max(sw[0], sw[1]));
+                    const float inv = mx8_inverse(c);
+                    const int r = 64 * i + 32 * wm + l32;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint32_t*>(cm + r * P + 128 * p + 32 * wn + 8 * q + 4 * h) =
+                            e4m3x4(acc[i][p][4 * q] * inv, acc[i][p][4 * q + 1] * inv, acc[i][p][4 * q + 2] * inv,
+                                   acc[i][p][4 * q + 3] * inv);
+                    if (h == 0) ss[r * 8 + 4 * p + wn] = (uint8_t)c;
+                }
+            __syncthreads();
+            for (int e = tid; e < rows * 16; e += kWsThreads) {
+                const int r = e >> 4, c = (e & 15) * 16, col = c0 + (c & 127);
+                if (col < N)
+                    store_out(a.gu_q + (int64_t)(row0 + r) * NN + (c < 128 ? 0 : N) + col,
+                              *reinterpret_cast<const uint4*>(cm + r * P + c));
+            }
+            for (int e = tid; e < rows * 4; e += kWsThreads) {   // pairs of scale bytes: 64 columns
+                const int r = e >> 2, p = (e >> 1) & 1, b = (e & 1) * 2;
+                if (c0 + 32 * b < N)
+                    *reinterpret_cast<uint16_t*>(a.gu_s + (int64_t)(row0 + r) * (NN / 32) + (p * N + c0) / 32 + b) =
+                        *reinterpret_cast<const uint16_t*>(ss + r * 8 + 4 * p + b);
+            }
+            __syncthreads();
+        }
+        using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
+        ws_store<E, 128, 1>(reinterpret_cast<E*>(a.out), N, row0, rows, c0, N, 32 * wn, ring, mul,
+                             [&](int i, int, int q, float (&v)[4]) {
+#pragma unroll
+                                 for (int k = 0; k < 4; ++k) v[k] = silu_mul(acc[i][0][4 * q + k], acc[i][1][4 * q + k]);
+                             });
+    } else {
+        using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
+        ws_store<E, 256, 2>(reinterpret_cast<E*>(a.out), K, row0, rows, c0, K, 64 * wn, ring, mul,
+                             [&](int i, int b, int q, float (&v)[4]) {
+#pragma unroll
+                                 for (int k = 0; k < 4; ++k) v[k] = acc[i][b][4 * q + k];
+                             });
+    }
+}
+
+template <int MODE, bool OUT_BF16, int SAVE>
+hipError_t launch_ws(FfnArgs a, int cap, hipStream_t stream) {
+    a.cap = cap;
+    const int cols = MODE == kGated ? a.NN / 2 : a.K, tc = MODE == kGated ? kWsCols / 2 : kWsCols;
+    a.ntiles_r = 0;
+    a.ntiles_c = (cols + tc - 1) / tc;
+    a.nblocks = (int)(max_work_items(a.M, a.G < a.M ? a.G : a.M, cap) * a.ntiles_c);
+    hipLaunchKernelGGL((ffn_ws_kernel<MODE, OUT_BF16, SAVE>), dim3((unsigned)a.nblocks), dim3(kWsThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
 // ------------------------------------------------------------- few rows --
 // The gated forward for few rows per expert (a serving step): the work is
 // reading each busy expert's weights once, so the tile is TR = 16 MB rows by
@@ -982,6 +1501,41 @@ bool wide_tiles(int64_t row_tiles, int64_t cols) {
     return row_tiles * ((cols + 127) / 128) > 3 * device_cus() && wide * 256 * 5 <= cols * 6;
 }
 
+// Rows an item of the 160 x 256 tiles may have, or 0 where the smaller tiles
+// are taken.  One workgroup fills a CU, so the grid should be one round of the
+// chip at least three quarters full, or two where the groups are small enough
+// (two items) for the weights to be most of what is read; past that the
+// smaller tiles, which overlap one item's start and end with another's work,
+// do better, and so they do on short reductions and (forward) on groups of few
+// rows.  Of the caps that fit, the cheapest: rounds x (the weights' columns +
+// the products of the item's rows), measured as 2 : rows / 160.  The rows of an
+// item are estimated from the mean and spread of evenly routed groups.
+// Measured (us, smaller tiles / these; dX with the activation's gradient):
+// shard (8192 rows, 32 experts, K = 2048, 2N = 1024) forward 75.8 / 52.1, dX
+// 72.2 / 61.1, half its rows 65.0 / 43.1 and 55.3 / 38.2; output projection's
+// shape (K = 512, 2N = 4096) dX 123 / 92, its forward 64 / 75 (8 stages);
+// 2048 rows, 32 experts, forward 35.1 / 40.8; 16384 rows of one expert, K =
+// 4096, forward 119 / 149; under skewed (Zipf) routing, which the host does not
+// see, the shard's forward loses 74 / 84 and dX 73 / 77.
+int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean) {
+    const int64_t busy = G < M ? G : M, cus = device_cus();
+    const double mean = (double)M / (double)busy, high = mean + 2.0 * sqrt(mean);
+    if (red < min_red || mean < min_mean) return 0;
+    const int64_t rounds = mean <= 2 * kWsRows ? 2 : 1;
+    int best = 0;
+    double cost = 0.0;
+    for (int cap = 64; cap <= kWsRows; cap += 32) {
+        const int64_t n = (int64_t)ceil(high / cap), wgs = busy * n * tiles;
+        if (4 * wgs < 3 * cus || wgs > rounds * cus) continue;
+        const double c = (double)((wgs + cus - 1) / cus) * (2.0 + mean / (double)n / 160.0);
+        if (best == 0 || c < cost) {
+            best = cap;
+            cost = c;
+        }
+    }
+    return best;
+}
+
 // The few-row form is for grids that the 128-row tiles leave unfilled.  With
 // B busy experts (at most min(G, M)) of few rows each, those tiles make B N/64
 // workgroups, each streaming its columns of the weights alone; below one per
@@ -1008,12 +1562,20 @@ hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
         if (rows <= 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, busy, stream);
         return launch_few_mb<OUT_BF16, SAVE, 4>(a, busy, stream);
     }
+    const int cap = ws_cap(a.M, a.G, a.K, (a.NN + 255) / 256, 1088, 96.0);
+    if (cap > 0) return launch_ws<kGated, OUT_BF16, SAVE>(a, cap, stream);
     return wide_tiles(max_work_items(a.M, busy, 128), a.NN) ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream)
                                                             : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
 }
 
 template <int MODE>
 hipError_t launch_bwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
+    if constexpr (MODE == kBwdX) {
+        const int cap = ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 1024, 48.0);
+        if (cap > 0)
+            return out_bf16 ? launch_ws<MODE, true, kSaveNone>(a, cap, stream)
+                            : launch_ws<MODE, false, kSaveNone>(a, cap, stream);
+    }
     const int64_t rows = MODE == kBwdX ? max_work_items(a.M, a.G < a.M ? a.G : a.M, 128)
                                        : (int64_t)a.G * ((a.K + 127) / 128);
     if (wide_tiles(rows, MODE == kBwdX ? a.K : a.NN))

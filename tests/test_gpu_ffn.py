@@ -579,3 +579,25 @@ def test_backward_wide(shape, mx, dxt, dwt):
 @pytest.mark.parametrize("dwt", [BF, F32], ids=["bf16", "f32"])
 def test_weight_gradient_wide(shape, dwt):
     test_weight_gradient(shape, dwt)
+
+
+# Grids of one or two rounds of the chip with long reductions: the tiles of up to 160 rows with load waves.
+LOADWAVES = [
+    ([130, 100, 129, 0, 160, 161, 90, 31] * 3, 2500, 1088, 1088),      # forward: 24 groups, partial column tiles
+    ([150, 65, 0, 33, 100], 360, 8256, 512),                           # dX: many column tiles, a partial one
+    ([100] * 25, 2500, 1280, 1344),
+]
+LW_IDS = ["M%d_K%d_N%d_G%d" % (M, K, N, len(s)) for s, M, K, N in LOADWAVES]
+
+
+@pytest.mark.parametrize("shape", LOADWAVES, ids=LW_IDS)
+@pytest.mark.parametrize("save", ["none", "bf16", "mx8"])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_forward_load_waves(shape, save, dt):
+    test_forward(shape, save, dt)
+
+
+@pytest.mark.parametrize("shape", LOADWAVES, ids=LW_IDS)
+@pytest.mark.parametrize("dxt,dwt", [(BF, BF), (F32, F32)], ids=["bf16", "f32"])
+def test_backward_load_waves(shape, dxt, dwt):
+    test_backward(shape, False, dxt, dwt)
