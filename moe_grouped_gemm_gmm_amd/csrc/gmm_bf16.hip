@@ -145,7 +145,7 @@ __device__ __forceinline__ bool tile_item(const int32_t* __restrict__ group_size
     if constexpr (MODE == kTgmm) {
         const int L = xcd_remap(blockIdx.x, nblocks);
         if (wave == 0) {
-            const TgmmTile tt = tgmm_tile(group_sizes, G, M, ntiles_r * ntiles_c, L, placement);
+            const TgmmTile tt = tgmm_tile(group_sizes, G, M, ntiles_r * ntiles_c, L, (int)blockIdx.x, placement);
             if (lane == 0) { s_info[0] = tt.row_lo; s_info[1] = tt.row_hi; s_info[2] = tt.g; s_info[3] = tt.t; }
         }
         __syncthreads();

@@ -130,16 +130,16 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
 // device status word.  TR x TC: tile rows and columns of the product; CAP: rows
 // an item may have (0: a.cap of them).
 template <int MODE, int TR, int TC, int CAP = TR>
-__device__ __forceinline__ bool ffn_item(const FfnArgs& a, int* s_info, FfnItem& it) {
+__device__ __forceinline__ bool ffn_item(const FfnArgs& a, int block, int* s_info, FfnItem& it) {
     const int lane = lane_id(), wave = threadIdx.x >> 6;
-    if (wave == 1 && blockIdx.x == 0) {
+    if (wave == 1 && block == 0) {
         const int st = group_status(a.group_sizes, a.G, a.M);
         if (lane == 0) a.status[0] = st;
     }
     if constexpr (MODE == kBwdW || MODE == kBwdWQ) {
         if (wave == 0) {
             const TgmmTile tt = tgmm_tile(a.group_sizes, a.G, a.M, a.ntiles_r * a.ntiles_c,
-                                          xcd_remap(blockIdx.x, a.nblocks), a.placement);
+                                          xcd_remap(block, a.nblocks), block, a.placement);
             if (lane == 0) { s_info[0] = tt.row_lo; s_info[1] = tt.row_hi; s_info[2] = tt.g; s_info[3] = tt.t; }
         }
         __syncthreads();
@@ -155,7 +155,7 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int* s_info, FfnItem&
     } else {
         if (wave == 0) {
             int col;
-            const WorkItem wi = even_work_item(a.group_sizes, a.G, a.M, CAP > 0 ? CAP : a.cap, a.ntiles_c, blockIdx.x, col);
+            const WorkItem wi = even_work_item(a.group_sizes, a.G, a.M, CAP > 0 ? CAP : a.cap, a.ntiles_c, block, col);
             if (lane == 0) { s_info[0] = wi.g; s_info[1] = wi.lo; s_info[2] = wi.hi; s_info[3] = col; }
         }
         __syncthreads();
@@ -451,19 +451,19 @@ __device__ __forceinline__ int frag_col(int wn, int j) {
     return (j >= NJ / 2 ? 16 * NJ : 0) + 16 * ((NJ / 2) * wn + j % (NJ / 2));
 }
 
+// What one workgroup does: tile `block` of the product, the ring (S stages) in
+// LDS.
 template <int MODE, bool OUT_BF16, int SAVE, int NJ>
-__global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnArgs a) {
+__device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* ring, int* s_info) {
     using T = FfnTile<NJ>;
     constexpr int S = T::kS, TR = T::kTR, TC = T::kTC, NTHR = 256, kSt = T::kStage, NIB = T::kNIB;
     constexpr bool kW = MODE == kBwdW || MODE == kBwdWQ;   // both operands transposed
     constexpr bool kSpread = kW;
-    __shared__ __attribute__((aligned(1024))) uint16_t ring[S * kSt];
-    __shared__ int s_info[5];
 
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     FfnItem it;
-    if (!ffn_item<MODE, TR, TC>(a, s_info, it)) return;
+    if (!ffn_item<MODE, TR, TC>(a, block, s_info, it)) return;
     if (!kW && it.g == a.G) {
         zero_tail<MODE, OUT_BF16, SAVE, TC, NTHR>(a, it);
         return;
@@ -718,7 +718,31 @@ __global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnAr
 }
 
 template <int MODE, bool OUT_BF16, int SAVE, int NJ>
-hipError_t launch(FfnArgs a, hipStream_t stream) {
+__global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnArgs a) {
+    using T = FfnTile<NJ>;
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[T::kS * T::kStage];
+    __shared__ int s_info[5];
+    ffn_tile<MODE, OUT_BF16, SAVE, NJ>(a, blockIdx.x, ring, s_info);
+}
+
+// Both products of the backward pass in one grid (dX's blocks first, padded to
+// a multiple of the XCDs): small problems wait for launches and for their
+// last tiles, not for either product (301 rows, 5 experts, K = 512, 2N = 384:
+// 15.6 us for the gradient and two launches, 12.2 with one).
+template <bool X_BF16, bool W_BF16, bool MX8>
+__global__ __launch_bounds__(256, FfnTile<4>::kRes) void ffn_bwd_kernel(const FfnArgs x, const FfnArgs w) {
+    using T = FfnTile<4>;
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[T::kS * T::kStage];
+    __shared__ int s_info[5];
+    if ((int)blockIdx.x < x.nblocks)
+        ffn_tile<kBwdX, X_BF16, kSaveNone, 4>(x, blockIdx.x, ring, s_info);
+    else
+        ffn_tile<MX8 ? kBwdWQ : kBwdW, W_BF16, kSaveNone, 4>(w, (int)blockIdx.x - x.nblocks, ring, s_info);
+}
+
+// Tiles of a's grid; false when it is too large.
+template <int MODE, int NJ>
+bool set_grid(FfnArgs& a) {
     using T = FfnTile<NJ>;
     int64_t nblocks;
     if constexpr (MODE == kBwdW || MODE == kBwdWQ) {
@@ -731,9 +755,26 @@ hipError_t launch(FfnArgs a, hipStream_t stream) {
         a.ntiles_c = (cols + tc - 1) / tc;
         nblocks = max_work_items(a.M, a.G < a.M ? a.G : a.M, T::kTR) * a.ntiles_c;
     }
-    if (nblocks > 0x7fffffff) return hipErrorInvalidConfiguration;
     a.nblocks = (int)nblocks;
-    hipLaunchKernelGGL((ffn_kernel<MODE, OUT_BF16, SAVE, NJ>), dim3((unsigned)nblocks), dim3(256), 0, stream, a);
+    return nblocks <= 0x7fffffff;
+}
+
+template <int MODE, bool OUT_BF16, int SAVE, int NJ>
+hipError_t launch(FfnArgs a, hipStream_t stream) {
+    if (!set_grid<MODE, NJ>(a)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ffn_kernel<MODE, OUT_BF16, SAVE, NJ>), dim3((unsigned)a.nblocks), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool X_BF16, bool W_BF16>
+hipError_t launch_both(FfnArgs x, FfnArgs w, hipStream_t stream) {
+    if (!set_grid<kBwdX, 4>(x) || !set_grid<kBwdW, 4>(w)) return hipErrorInvalidConfiguration;
+    x.nblocks = (x.nblocks + kNumXcd - 1) / kNumXcd * kNumXcd;
+    const dim3 grid((unsigned)(x.nblocks + w.nblocks));
+    if (w.aq != nullptr)
+        hipLaunchKernelGGL((ffn_bwd_kernel<X_BF16, W_BF16, true>), grid, dim3(256), 0, stream, x, w);
+    else
+        hipLaunchKernelGGL((ffn_bwd_kernel<X_BF16, W_BF16, false>), grid, dim3(256), 0, stream, x, w);
     return hipGetLastError();
 }
 
@@ -1040,7 +1081,7 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     FfnItem it;
-    if (!ffn_item<MODE, kWsRows, kWsCols, 0>(a, s_info, it)) return;
+    if (!ffn_item<MODE, kWsRows, kWsCols, 0>(a, blockIdx.x, s_info, it)) return;
     if (it.g == a.G) {
         zero_tail<MODE, OUT_BF16, SAVE, kWsCols, kWsThreads>(a, it);
         return;
@@ -1354,7 +1395,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     FfnItem it;
-    if (!ffn_item<kGated, TR, 2 * CT>(a, s_info, it)) return;
+    if (!ffn_item<kGated, TR, 2 * CT>(a, blockIdx.x, s_info, it)) return;
     if (it.g == a.G) {
         zero_tail<kGated, OUT_BF16, SAVE, 2 * CT, NTHR>(a, it);
         return;
@@ -1568,17 +1609,23 @@ hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
                                                             : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
 }
 
+// Whether a product of the backward pass takes 256-column tiles.
+bool wide_bwd(const FfnArgs& a, bool dx) {
+    const int64_t rows = dx ? max_work_items(a.M, a.G < a.M ? a.G : a.M, 128) : (int64_t)a.G * ((a.K + 127) / 128);
+    return wide_tiles(rows, dx ? a.K : a.NN);
+}
+
+int dx_cap(const FfnArgs& a) { return ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 1024, 48.0); }
+
 template <int MODE>
 hipError_t launch_bwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
     if constexpr (MODE == kBwdX) {
-        const int cap = ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 1024, 48.0);
+        const int cap = dx_cap(a);
         if (cap > 0)
             return out_bf16 ? launch_ws<MODE, true, kSaveNone>(a, cap, stream)
                             : launch_ws<MODE, false, kSaveNone>(a, cap, stream);
     }
-    const int64_t rows = MODE == kBwdX ? max_work_items(a.M, a.G < a.M ? a.G : a.M, 128)
-                                       : (int64_t)a.G * ((a.K + 127) / 128);
-    if (wide_tiles(rows, MODE == kBwdX ? a.K : a.NN))
+    if (wide_bwd(a, MODE == kBwdX))
         return out_bf16 ? launch<MODE, true, kSaveNone, 8>(a, stream) : launch<MODE, false, kSaveNone, 8>(a, stream);
     return out_bf16 ? launch<MODE, true, kSaveNone, 4>(a, stream) : launch<MODE, false, kSaveNone, 4>(a, stream);
 }
@@ -1608,6 +1655,15 @@ hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
 
 hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
     return a.aq != nullptr ? launch_bwd<kBwdWQ>(a, out_bf16, stream) : launch_bwd<kBwdW>(a, out_bf16, stream);
+}
+
+hipError_t launch_ffn_bwd(const FfnArgs& x, bool x_bf16, const FfnArgs& w, bool w_bf16, hipStream_t stream) {
+    if (dx_cap(x) > 0 || wide_bwd(x, true) || wide_bwd(w, false)) {
+        const hipError_t e = launch_ffn_dx(x, x_bf16, stream);
+        return e != hipSuccess ? e : launch_ffn_dw(w, w_bf16, stream);
+    }
+    if (x_bf16) return w_bf16 ? launch_both<true, true>(x, w, stream) : launch_both<true, false>(x, w, stream);
+    return w_bf16 ? launch_both<false, true>(x, w, stream) : launch_both<false, false>(x, w, stream);
 }
 
 }  // namespace gmm

@@ -140,22 +140,20 @@ int gmm_bf16_swiglu_bwd(const void* dh, const void* rhs, const int32_t* group_si
     if (M > 0)
         GMM_TRY(hip_status(gmm::launch_gated_grad(dh, gu, gu_q, gu_scale, group_sizes, (int)M, (int)N, (int)G, dp, h,
                                                   ws_status(ws), s)));
-    if (dx != nullptr && M > 0) {
-        gmm::FfnArgs a = args_of(group_sizes, M, K, 2 * N, G, ws);
-        a.a = dp;
-        a.b = u16(rhs);
-        a.out = dx;
-        GMM_TRY(hip_status(gmm::launch_ffn_dx(a, dx_dtype == GMM_BF16, s)));
-    }
-    if (dw != nullptr) {
-        gmm::FfnArgs a = args_of(group_sizes, M, K, 2 * N, G, ws);
-        a.a = u16(lhs);
-        a.aq = lhs_q;
-        a.as = lhs_scale;
-        a.b = dp;
-        a.out = dw;
-        GMM_TRY(hip_status(gmm::launch_ffn_dw(a, dw_dtype == GMM_BF16, s)));
-    }
+    gmm::FfnArgs x = args_of(group_sizes, M, K, 2 * N, G, ws), w = x;
+    x.a = dp;
+    x.b = u16(rhs);
+    x.out = dx;
+    w.a = u16(lhs);
+    w.aq = lhs_q;
+    w.as = lhs_scale;
+    w.b = dp;
+    w.out = dw;
+    const bool want_dx = dx != nullptr && M > 0;
+    if (want_dx && dw != nullptr)
+        return hip_status(gmm::launch_ffn_bwd(x, dx_dtype == GMM_BF16, w, dw_dtype == GMM_BF16, s));
+    if (want_dx) return hip_status(gmm::launch_ffn_dx(x, dx_dtype == GMM_BF16, s));
+    if (dw != nullptr) return hip_status(gmm::launch_ffn_dw(w, dw_dtype == GMM_BF16, s));
     return GMM_OK;
 }
 

@@ -135,6 +135,8 @@ struct FfnArgs {
 hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream);
 hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream);
 hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream);
+// Both, in one launch where that pays.
+hipError_t launch_ffn_bwd(const FfnArgs& x, bool x_bf16, const FfnArgs& w, bool w_bf16, hipStream_t stream);
 
 // Upper bounds of these launches' grids.
 int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G);

@@ -61,12 +61,12 @@ __device__ __forceinline__ bool tgmm_pick(int base, int G, int lo, int hi, int c
 }
 
 // One wave; every lane gets the result.  T = tiles per group, L = the
-// block's id after the default XCD remap.  A group's rows are its clamped
+// block's id after the default XCD remap (block: before it).  A group's rows are its clamped
 // range (group_chunk: a negative size reads as 0, rows stop at M).  Up to
 // 256 groups the ranges stay in registers (one load and one scan per 64
 // groups); beyond, the second pass reads and scans them again.
 __device__ inline TgmmTile tgmm_tile(const int32_t* __restrict__ group_sizes, int G, int M, int T,
-                                     int L, int placement) {
+                                     int L, int block, int placement) {
     const bool inreg = G <= 256;
     int glo[4], ghi[4];
     // pass 1: clamped ranges, class counts and the total
@@ -125,9 +125,9 @@ __device__ inline TgmmTile tgmm_tile(const int32_t* __restrict__ group_sizes, in
     out.row_lo = out.row_hi = 0;
     int r, cls = -1;   // cls < 0: index order
     if (skewed) {
-        const int tx = T / kNumXcd, i = (int)blockIdx.x / kNumXcd;
+        const int tx = T / kNumXcd, i = block / kNumXcd;
         r = i / tx;
-        out.t = ((int)blockIdx.x % kNumXcd) * tx + i % tx;
+        out.t = (block % kNumXcd) * tx + i % tx;
         cls = 0;
         if (r >= cnt0) { r -= cnt0; cls = 1;
             if (r >= cnt1) { r -= cnt1; cls = 2;

@@ -16,26 +16,60 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _dt, _ptr, _stream, _ws, load_library
+from . import _DT, GmmError, load_library
 
 OP_BF16_SWIGLU, OP_BF16_SWIGLU_BWD, OP_TGMM_MX8 = 16, 17, 18
 FFN_EXPORTS = ("gmm_quantize_mx8", "gmm_dequantize_mx8", "gmm_bf16_swiglu", "gmm_bf16_swiglu_bwd", "tgmm_mx8")
 
 
-def _shape(t: Optional[torch.Tensor], want: tuple, name: str) -> None:
-    if t is not None and tuple(t.shape) != want:
-        raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), want))
-
-
-def _typed(t: Optional[torch.Tensor], dtypes: tuple, name: str) -> None:
-    if t is not None and t.dtype not in dtypes:
-        raise TypeError("%s has dtype %s" % (name, t.dtype))
-
-
 _BYTES = (torch.uint8, torch.float8_e4m3fn)
 _BF16 = (torch.bfloat16,)
+_FLOAT = (torch.bfloat16, torch.float32)
 _INT32 = (torch.int32,)
 _U8 = (torch.uint8,)
+
+_status_ws = {}    # device -> the status block of calls that were given no workspace
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# A serving step's calls take a few microseconds on the device, so what the
+# host does for each is kept small: addresses go to ctypes as integers, the
+# stream comes from torch's raw lookup, and calls whose workspace is only the
+# status word (nothing reads it when the caller gives no workspace) share one.
+
+def _arg(t: Optional[torch.Tensor], want, dtypes: tuple, name: str) -> Optional[int]:
+    """Address of t after checking its shape (want, unless None), dtype and layout."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+    if want is not None and t.shape != want:
+        raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), tuple(want)))
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None and t.device.index is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _status(ws: Optional[torch.Tensor], device):
+    """(address, bytes) of ws, or of the device's shared status block."""
+    if ws is None:
+        ws = _status_ws.get(device)
+        if ws is None:
+            ws = _status_ws[device] = torch.empty(256, dtype=torch.uint8, device=device)
+    elif not ws.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _check(lib, rc: int) -> None:
+    if rc != 0:
+        raise GmmError(rc, lib.gmm_last_error().decode())
 
 
 def gmm_quantize_mx8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None
@@ -44,16 +78,13 @@ def gmm_quantize_mx8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: O
     uint8 [M,K] and E8M0 scales uint8 [M,K/32]."""
     lib = load_library()
     M, K = x.shape
-    _typed(x, (torch.bfloat16, torch.float32), "x")
-    _shape(q, (M, K), "q")
-    _typed(q, _BYTES, "q")
-    _shape(scale, (M, K // 32), "scale")
-    _typed(scale, _U8, "scale")
+    xp = _arg(x, None, _FLOAT, "x")
     if q is None:
         q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     if scale is None:
         scale = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    _check(lib.gmm_quantize_mx8(_ptr(x), _dt(x), M, K, _ptr(q), _ptr(scale), _stream(x)))
+    _check(lib, lib.gmm_quantize_mx8(xp, _DT[x.dtype], M, K, _arg(q, (M, K), _BYTES, "q"),
+                                     _arg(scale, (M, K // 32), _U8, "scale"), _stream(x)))
     return q, scale
 
 
@@ -62,13 +93,10 @@ def gmm_dequantize_mx8(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dt
     """The values [M,K] (bf16 or fp32) of an 8-bit checkpoint."""
     lib = load_library()
     M, K = q.shape
-    _typed(q, _BYTES, "q")
-    _shape(scale, (M, K // 32), "scale")
-    _typed(scale, _U8, "scale")
-    _shape(out, (M, K), "out")
+    qp, sp = _arg(q, None, _BYTES, "q"), _arg(scale, (M, K // 32), _U8, "scale")
     if out is None:
         out = torch.empty((M, K), dtype=out_dtype, device=q.device)
-    _check(lib.gmm_dequantize_mx8(_ptr(q), _ptr(scale), M, K, _ptr(out), _dt(out), _stream(q)))
+    _check(lib, lib.gmm_dequantize_mx8(qp, sp, M, K, _arg(out, (M, K), _FLOAT, "out"), _DT[out.dtype], _stream(q)))
     return out
 
 
@@ -86,22 +114,14 @@ def gmm_bf16_swiglu(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Ten
     if K2 != K or N2 % 2:
         raise ValueError("lhs K=%d but rhs %s" % (K, tuple(rhs.shape)))
     N = N2 // 2
-    _typed(lhs, _BF16, "lhs")
-    _typed(rhs, _BF16, "rhs")
-    _shape(group_sizes, (G,), "group_sizes")
-    _typed(group_sizes, _INT32, "group_sizes")
-    _shape(out, (M, N), "out")
-    _shape(gu, (M, N2), "gu")
-    _typed(gu, _BF16, "gu")
-    _shape(gu_q, (M, N2), "gu_q")
-    _typed(gu_q, _BYTES, "gu_q")
-    _shape(gu_scale, (M, N2 // 32), "gu_scale")
-    _typed(gu_scale, _U8, "gu_scale")
+    args = (_arg(lhs, None, _BF16, "lhs"), _arg(rhs, None, _BF16, "rhs"),
+            _arg(group_sizes, (G,), _INT32, "group_sizes"), M, K, N, G)
+    kept = (_arg(gu, (M, N2), _BF16, "gu"), _arg(gu_q, (M, N2), _BYTES, "gu_q"),
+            _arg(gu_scale, (M, N2 // 32), _U8, "gu_scale"))
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=lhs.device)
-    ws, wsp, wsb = _ws(ws, OP_BF16_SWIGLU, M, K, N, G, lhs.device)
-    _check(lib.gmm_bf16_swiglu(_ptr(lhs), _ptr(rhs), _ptr(group_sizes), M, K, N, G, _ptr(out), _dt(out),
-                               _ptr(gu), _ptr(gu_q), _ptr(gu_scale), wsp, wsb, _stream(lhs)))
+    _check(lib, lib.gmm_bf16_swiglu(*args, _arg(out, (M, N), _FLOAT, "out"), _DT[out.dtype], *kept,
+                                    *_status(ws, lhs.device), _stream(lhs)))
     return out
 
 
@@ -124,32 +144,22 @@ def gmm_bf16_swiglu_bwd(dh: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.
     G, K, N2 = rhs.shape
     if N2 != 2 * N:
         raise ValueError("dh N=%d but rhs %s" % (N, tuple(rhs.shape)))
-    for t, name in ((dh, "dh"), (rhs, "rhs"), (lhs, "lhs"), (gu, "gu"), (h, "h")):
-        _typed(t, _BF16, name)
-    for t, name in ((lhs_q, "lhs_q"), (gu_q, "gu_q")):
-        _typed(t, _BYTES, name)
-    for t, name in ((lhs_scale, "lhs_scale"), (gu_scale, "gu_scale")):
-        _typed(t, _U8, name)
-    _shape(group_sizes, (G,), "group_sizes")
-    _typed(group_sizes, _INT32, "group_sizes")
-    _shape(lhs, (M, K), "lhs")
-    _shape(lhs_q, (M, K), "lhs_q")
-    _shape(lhs_scale, (M, K // 32), "lhs_scale")
-    _shape(gu, (M, N2), "gu")
-    _shape(gu_q, (M, N2), "gu_q")
-    _shape(gu_scale, (M, N2 // 32), "gu_scale")
-    _shape(dx, (M, K), "dx")
-    _shape(dw, (G, K, N2), "dw")
-    _shape(h, (M, N), "h")
+    args = (_arg(dh, None, _BF16, "dh"), _arg(rhs, None, _BF16, "rhs"),
+            _arg(group_sizes, (G,), _INT32, "group_sizes"), _arg(lhs, (M, K), _BF16, "lhs"),
+            _arg(lhs_q, (M, K), _BYTES, "lhs_q"), _arg(lhs_scale, (M, K // 32), _U8, "lhs_scale"),
+            _arg(gu, (M, N2), _BF16, "gu"), _arg(gu_q, (M, N2), _BYTES, "gu_q"),
+            _arg(gu_scale, (M, N2 // 32), _U8, "gu_scale"), M, K, N, G)
+    dev = dh.device
     if dx is None and want_dx:
-        dx = torch.empty((M, K), dtype=dx_dtype, device=dh.device)
+        dx = torch.empty((M, K), dtype=dx_dtype, device=dev)
     if dw is None and want_dw:
-        dw = torch.empty((G, K, N2), dtype=dw_dtype, device=dh.device)
-    ws, wsp, wsb = _ws(ws, OP_BF16_SWIGLU_BWD, M, K, N, G, dh.device)
-    _check(lib.gmm_bf16_swiglu_bwd(
-        _ptr(dh), _ptr(rhs), _ptr(group_sizes), _ptr(lhs), _ptr(lhs_q), _ptr(lhs_scale), _ptr(gu), _ptr(gu_q),
-        _ptr(gu_scale), M, K, N, G, _ptr(dx), 0 if dx is None else _dt(dx), _ptr(dw), 0 if dw is None else _dt(dw),
-        _ptr(h), wsp, wsb, _stream(dh)))
+        dw = torch.empty((G, K, N2), dtype=dw_dtype, device=dev)
+    if ws is None:
+        ws = torch.empty(256 + 4 * M * N, dtype=torch.uint8, device=dev)
+    _check(lib, lib.gmm_bf16_swiglu_bwd(
+        *args, _arg(dx, (M, K), _FLOAT, "dx"), 0 if dx is None else _DT[dx.dtype],
+        _arg(dw, (G, K, N2), _FLOAT, "dw"), 0 if dw is None else _DT[dw.dtype], _arg(h, (M, N), _BF16, "h"),
+        *_status(ws, dev), _stream(dh)))
     return dx, dw
 
 
@@ -164,17 +174,12 @@ def tgmm_mx8(x_q: torch.Tensor, x_scale: torch.Tensor, dy: torch.Tensor, group_s
     if M2 != M:
         raise ValueError("x has %d rows but dy has %d" % (M, M2))
     G = group_sizes.numel()
-    _typed(x_q, _BYTES, "x_q")
-    _typed(x_scale, _U8, "x_scale")
-    _typed(dy, _BF16, "dy")
-    _typed(group_sizes, _INT32, "group_sizes")
-    _shape(x_scale, (M, K // 32), "x_scale")
-    _shape(out, (G, K, N), "out")
+    args = (_arg(x_q, None, _BYTES, "x_q"), _arg(x_scale, (M, K // 32), _U8, "x_scale"), _arg(dy, None, _BF16, "dy"),
+            _arg(group_sizes, (G,), _INT32, "group_sizes"), M, K, N, G)
     if out is None:
         out = torch.empty((G, K, N), dtype=out_dtype, device=dy.device)
-    ws, wsp, wsb = _ws(ws, OP_TGMM_MX8, M, K, N, G, dy.device)
-    _check(lib.tgmm_mx8(_ptr(x_q), _ptr(x_scale), _ptr(dy), _ptr(group_sizes), M, K, N, G, _ptr(out), _dt(out),
-                        wsp, wsb, _stream(dy)))
+    _check(lib, lib.tgmm_mx8(*args, _arg(out, (G, K, N), _FLOAT, "out"), _DT[out.dtype], *_status(ws, dy.device),
+                             _stream(dy)))
     return out
 
 
