@@ -288,14 +288,22 @@ __device__ __forceinline__ void gated_epilogue(const FfnArgs& a, const FfnItem& 
     }
 }
 
+// 32 bytes to LDS address p.  In asm because an LDS access that the compiler
+// sees makes it wait for every load into LDS in flight; the barrier that
+// publishes the data waits for the writes.
+__device__ __forceinline__ void put32(unsigned p, const u32x4& l, const u32x4& h) {
+    asm volatile("ds_write_b128 %0, %1\n\tds_write_b128 %0, %2 offset:16" : : "v"(p), "v"(l), "v"(h) : "memory");
+}
+
 // 16 E4M3 codes of one checkpoint block -> 16 bf16 values (exact).
 __device__ __forceinline__ void mx8_expand16(const u32x4& codes, uint32_t scale_code, u32x4& lo, u32x4& hi) {
+    // one instruction for two codes: values times 2^(c - 127), rounded to bf16
+    // (exact); c = 0 stands for 2^-127, a subnormal scale
     const float s = mx8_scale(scale_code);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        float v[4];
-        mx8_values4(codes[d], s, v);
-        const uint32_t p0 = pack_rne(v[0], v[1]), p1 = pack_rne(v[2], v[3]);
+        const uint32_t p0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[d], s, false));
+        const uint32_t p1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[d], s, true));
         if (d < 2) {
             lo[2 * d] = p0;
             lo[2 * d + 1] = p1;
@@ -549,6 +557,7 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
         else wait_vmem<NIB * (S - 2)>();
     };
 
+    const unsigned ring_lds = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)ring;
     // ---- checkpointed x: thread t takes the 16 codes of columns
     //      16 (t % 8) .. +15 of slice row t / 8, expands them and writes the
     //      32-byte chunk the transposed layout has there
@@ -567,14 +576,11 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
         u32x4 l, h;
         mx8_expand16(qd[set], qs[set], l, h);
         if (red_lo + t * 32 + qrow >= red_hi) l = h = u32x4{0u, 0u, 0u, 0u};
-        uint16_t* p = ring + stage * kSt + qrow * TR + 16 * (qchunk ^ trans_key<kSpread>(qrow));
-        *reinterpret_cast<u32x4*>(p) = l;
-        *reinterpret_cast<u32x4*>(p + 8) = h;
+        put32(ring_lds + 2 * (unsigned)(stage * kSt + qrow * TR + 16 * (qchunk ^ trans_key<kSpread>(qrow))), l, h);
     };
 
     // ---- LDS addresses of this lane's fragments in stage 0
     const int lr = lane & 15, lg = lane >> 4;
-    const unsigned ring_lds = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)ring;
     constexpr int kHalfA = 16 * TR * 2, kHalfB = (kSpread ? 16 : 4) * TC * 2;
     unsigned ra[4], rb[4];
 #pragma unroll
@@ -594,32 +600,20 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    if constexpr (MODE == kBwdWQ) {
-        if (nsl > 0) {
-            fetch_codes(0, 0);
-            issue(0, 0);
-            put_codes(0, 0, 0);
-        }
-        if (nsl > 1) {
-            fetch_codes(1, 0);
-            issue(1, 1);
-        }
-        if (nsl > 2) fetch_codes(2, 1);
-    } else {
-#pragma unroll
-        for (int t = 0; t < S - 1; ++t)
-            if (t < nsl) issue(t, t);
-    }
     int stage = 0;
-    auto step = [&](int t, auto set_) {
+    // steady: at least S more slices follow (no conditions then, so that the
+    // compiler's own count of the loads younger than the codes is exact)
+    auto step = [&](int t, auto set_, auto steady_) __attribute__((always_inline)) {
         constexpr int set = decltype(set_)::value;   // t % 2, for the codes
+        constexpr bool steady = decltype(steady_)::value;
         if constexpr (MODE == kBwdWQ)
-            if (t + 1 < nsl) put_codes(t + 1, set, stage == S - 1 ? 0 : stage + 1);
-        wait_slice(t);
+            if (steady || t + 1 < nsl) put_codes(t + 1, set, stage == S - 1 ? 0 : stage + 1);
+        if constexpr (steady && MODE == kBwdWQ) wait_vmem<NIB + 2>();
+        else wait_slice(t);
         stage_barrier();
-        if (t + S - 1 < nsl) issue(t + S - 1, stage == 0 ? S - 1 : stage - 1);
+        if (steady || t + S - 1 < nsl) issue(t + S - 1, stage == 0 ? S - 1 : stage - 1);
         if constexpr (MODE == kBwdWQ)
-            if (t + S < nsl) fetch_codes(t + S, set);
+            if (steady || t + S < nsl) fetch_codes(t + S, set);
         const unsigned so = (unsigned)(stage * kSt * 2);
         v8bf af[4], bf[NJ];
         if constexpr (MODE == kBwdX) {
@@ -655,13 +649,43 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
         }
         stage = stage == S - 1 ? 0 : stage + 1;
     };
+    constexpr std::integral_constant<int, 0> set0;
+    constexpr std::integral_constant<int, 1> set1;
     if constexpr (MODE == kBwdWQ) {
-        for (int t = 0; t < nsl; t += 2) {
-            step(t, std::integral_constant<int, 0>{});
-            if (t + 1 < nsl) step(t + 1, std::integral_constant<int, 1>{});
+        int t = 0;
+        if (nsl > S + 1) {
+            fetch_codes(0, 0);
+            issue(0, 0);
+            put_codes(0, 0, 0);
+            fetch_codes(1, 0);
+            issue(1, 1);
+            fetch_codes(2, 1);
+            do {
+                step(t, set0, std::true_type{});
+                step(t + 1, set1, std::true_type{});
+                t += 2;
+            } while (t + 1 + S < nsl);
+        } else {
+            if (nsl > 0) {
+                fetch_codes(0, 0);
+                issue(0, 0);
+                put_codes(0, 0, 0);
+            }
+            if (nsl > 1) {
+                fetch_codes(1, 0);
+                issue(1, 1);
+            }
+            if (nsl > 2) fetch_codes(2, 1);
+        }
+        for (; t < nsl; t += 2) {
+            step(t, set0, std::false_type{});
+            if (t + 1 < nsl) step(t + 1, set1, std::false_type{});
         }
     } else {
-        for (int t = 0; t < nsl; ++t) step(t, std::integral_constant<int, 0>{});
+#pragma unroll
+        for (int t = 0; t < S - 1; ++t)
+            if (t < nsl) issue(t, t);
+        for (int t = 0; t < nsl; ++t) step(t, set0, std::false_type{});
     }
     __syncthreads();
 
@@ -728,7 +752,7 @@ __global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnAr
 // Both products of the backward pass in one grid (dX's blocks first, padded to
 // a multiple of the XCDs): small problems wait for launches and for their
 // last tiles, not for either product (301 rows, 5 experts, K = 512, 2N = 384:
-// 15.6 us for the gradient and two launches, 12.2 with one).
+// 15.6 us for the gradient and two launches, 11.5 with one).
 template <bool X_BF16, bool W_BF16, bool MX8>
 __global__ __launch_bounds__(256, FfnTile<4>::kRes) void ffn_bwd_kernel(const FfnArgs x, const FfnArgs w) {
     using T = FfnTile<4>;
