@@ -601,3 +601,39 @@ def test_forward_load_waves(shape, save, dt):
 @pytest.mark.parametrize("dxt,dwt", [(BF, BF), (F32, F32)], ids=["bf16", "f32"])
 def test_backward_load_waves(shape, dxt, dwt):
     test_backward(shape, False, dxt, dwt)
+
+
+def test_expert_layer_example():
+    """The example's training step: the gradients of both forms against a 64-bit layer.  Each value of a
+    checkpoint is off by at most 2^-4, evenly spread over half a step (2^-4 / sqrt 3 of the norm, 0.036); P's
+    enters dP twice over (gate and up), x's and h's the weight gradients: under 0.1 of the norm with room, and
+    under 0.02 for the bfloat16 form, whose roundings are 2^-8."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    rows, E, k, n, seed = 500, 6, 256, 128, 3
+    plain, small = mod.run(rows, E, k, n, seed)
+    assert plain["kept"] == rows * (k + 3 * n) * 2
+    assert small["kept"] == rows * (k + 2 * n) * 33 // 32
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    r = lambda shape, s: torch.randn(shape, generator=gen, device=DEV, dtype=BF).mul_(s)
+    sizes = torch.bincount(torch.randint(0, E, (rows,), generator=gen, device=DEV), minlength=E).cpu().tolist()
+    x, dy = f64(r((rows, k), 1.0)), f64(r((rows, k), 0.1))
+    wgu, wd = f64(r((E, k, 2 * n), k ** -0.5)), f64(r((E, n, k), n ** -0.5))
+    dx, dwgu, dwd, lo = np.zeros((rows, k)), np.zeros((E, k, 2 * n)), np.zeros((E, n, k)), 0
+    for e, s in enumerate(sizes):
+        q = slice(lo, lo + s)
+        lo += s
+        P = x[q] @ wgu[e]
+        g, u = P[:, :n], P[:, n:]
+        sg = 1 / (1 + np.exp(-g))
+        dh = dy[q] @ wd[e].T
+        d = np.concatenate([dh * u * sg * (1 + g * (1 - sg)), dh * g * sg], axis=1)
+        dx[q], dwgu[e], dwd[e] = d @ wgu[e].T, x[q].T @ d, (g * sg * u).T @ dy[q]
+    for o, lim in ((plain, 0.02), (small, 0.1)):
+        for got, want in zip(o["grads"], (dx, dwgu, dwd)):
+            assert np.linalg.norm(f64(got) - want) <= lim * np.linalg.norm(want)
