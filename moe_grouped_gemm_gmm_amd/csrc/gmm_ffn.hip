@@ -819,6 +819,11 @@ hipError_t launch_both(FfnArgs x, FfnArgs w, hipStream_t stream) {
 // waves have read all of stage u and the load waves have waited for stage
 // u + 1; after it stage u + 1 may be read and slice u + 3 loaded over slice u.
 //
+// A workgroup takes items until none is left.  After an item's slices one slot
+// of the ring is skipped and serves to stage its results, while the load waves
+// fill the two slots after it from the next item: the start of one item hides
+// behind the end of the one before (production dX 449 -> 414 us).
+//
 // The wave rows take alternate 32-row blocks and a wave multiplies only its
 // blocks that hold rows (a loop compiled for each count), so an item's cost
 // follows its rows; 8 rows of A past the item's end are not loaded.
@@ -1054,44 +1059,100 @@ constexpr int kWsSliceA = kWsRows * 64, kWsSliceB = kWsCols * 64, kWsStage = kWs
 constexpr int kWsBytes = kWsStages * kWsStage * 2;
 static_assert(kWsBytes <= 163840 - 1024, "the ring fits the LDS");
 
-// Stages rows of E in LDS and stores them: VAL(i, q, v) gives the four values of
-// row block i, columns 8q + 4 (lane / 32) .. +3 of each of the wave's NC column
-// blocks of 32 (at column wcol + 32 b of the tile of WID columns).
+// Items of even_work_item for a workgroup that takes many: the groups' ranges
+// and item offsets stay in registers (up to 256 groups; beyond, each item is
+// found from group_sizes again).
+struct EvenItems {
+    int lo[4], hi[4], cn[4], W[4], items, total;
+    __device__ void init(const int32_t* __restrict__ group_sizes, int G, int M, int cap) {
+        if (G > 256) return;
+        const int lane = lane_id();
+        int raw[4], carry = 0;
+        items = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[k] = group_size_at(group_sizes, G, 64 * k + lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            lo[k] = hi[k] = cn[k] = W[k] = 0;
+            if (64 * k < G) {
+                const GroupChunk ch = group_chunk_of(raw[k], M, carry);
+                lo[k] = ch.lo;
+                hi[k] = ch.hi;
+                carry = ch.next_carry;
+                cn[k] = group_items<true>(ch.lo, ch.hi, cap);
+                const int incl = wave_incl_scan(cn[k]);
+                W[k] = items + incl - cn[k];
+                items += lane_value(incl, 63);
+            }
+        }
+        total = min(carry, M);
+    }
+    __device__ WorkItem find(const int32_t* __restrict__ group_sizes, int G, int M, int cap, int ntiles, int b,
+                             int& col) const {
+        if (G > 256) return even_work_item(group_sizes, G, M, cap, ntiles, b, col);
+        col = 0;
+        const int L = xcd_balance(b, (items + tail_items<true>(total, M, cap)) * ntiles);
+        if (L < 0) return WorkItem{-1, 0, 0, 0};
+        const int w = L / ntiles;
+        col = L % ntiles;
+        if (w >= items) return tail_item<true>(G, M, total, items, cap, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned long long m = __ballot(cn[k] > 0 && w >= W[k] && w < W[k] + cn[k]);
+            if (m) {
+                const int src = __ffsll((long long)m) - 1;
+                return even_item(64 * k + src, lane_value(lo[k], src), lane_value(hi[k], src),
+                                 w - lane_value(W[k], src), cap);
+            }
+        }
+        return WorkItem{-1, 0, 0, 0};   // not reached: w < items has an owner
+    }
+};
+
+// Stages rows of E in one stage of the ring and stores them, RB 32-row blocks
+// (of the item's five) a round, two barriers a round: VAL(i, b, q, v) gives the
+// four values of the wave's row block i, columns 8q + 4 (lane / 32) .. +3 of
+// its column block b of 32 (at column wcol + 32 b of the tile's WID).
+template <typename E, int WID>
+struct WsRounds {
+    static constexpr int C = 16 / (int)sizeof(E), P = WID + C, kBlock = 32 * P * (int)sizeof(E);
+    static constexpr int RB = 2 * kWsStage / kBlock, kRounds = (5 + RB - 1) / RB;
+    static_assert(RB >= 1, "32 staged rows fit a stage");
+};
 template <typename E, int WID, int NC, typename Val>
 __device__ __forceinline__ void ws_store(E* out, int64_t ld, int row0, int rows, int col0, int cols, int wcol,
-                                          uint16_t* sm, bool mul, Val val) {
-    constexpr int C = 16 / (int)sizeof(E), P = WID + C;
-    constexpr int kFit = kWsBytes / (64 * P * (int)sizeof(E)), RI = kFit >= 3 ? 3 : kFit;
-    static_assert(kFit >= 1, "64 staged rows fit the ring");
+                                          uint16_t* sm, Val val) {
+    using R = WsRounds<E, WID>;
+    constexpr int C = R::C, P = R::P, RB = R::RB;
     const int tid = threadIdx.x, lane = lane_id(), wm = tid >> 8;
     E* s = reinterpret_cast<E*>(sm);
 #pragma unroll
-    for (int i0 = 0; i0 < 3; i0 += RI) {
-        if (64 * i0 >= rows) break;
-        if (mul)
+    for (int k = 0; k < R::kRounds; ++k) {
 #pragma unroll
-        for (int i = 0; i < (RI < 3 - i0 ? RI : 3 - i0); ++i)
+        for (int i = 0; i < 3; ++i) {
+            const int blk = 2 * i + wm - k * RB;
+            if (blk < 0 || blk >= RB || 2 * i + wm >= 5) continue;
 #pragma unroll
             for (int b = 0; b < NC; ++b)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float v[4];
-                    val(i0 + i, b, q, v);
-                    E* d = s + (64 * i + 32 * wm + (lane & 31)) * P + wcol + 32 * b + 8 * q + 4 * (lane >> 5);
+                    val(i, b, q, v);
+                    E* d = s + (32 * blk + (lane & 31)) * P + wcol + 32 * b + 8 * q + 4 * (lane >> 5);
                     if constexpr (sizeof(E) == 2)
                         *reinterpret_cast<uint2*>(d) = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]));
                     else
                         *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
                 }
-        __syncthreads();
-        const int n = min(rows - 64 * i0, 64 * RI);
-        for (int e = tid; e < n * (WID / C); e += kWsThreads) {
+        }
+        stage_barrier();
+        const int first = 32 * RB * k, n = min(rows - first, 32 * RB);
+        for (int e = tid; e < n * (WID / C); e += 512) {
             const int r = e / (WID / C), c = (e % (WID / C)) * C;
             if (col0 + c < cols)
-                store_out(out + (int64_t)(row0 + 64 * i0 + r) * ld + col0 + c,
-                          *reinterpret_cast<const uint4*>(s + r * P + c));
+                store_out(out + (int64_t)(row0 + first + r) * ld + col0 + c, *reinterpret_cast<const uint4*>(s + r * P + c));
         }
-        __syncthreads();
+        stage_barrier();
     }
 }
 
@@ -1100,61 +1161,86 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
     static_assert(MODE == kGated || MODE == kBwdX, "forward and dX");
     constexpr int S = kWsStages, kSt = kWsStage;
     constexpr bool kBTr = MODE == kGated;
+    using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
+    // barriers of an item's end
+    constexpr int kEndBarriers = 2 * WsRounds<E, MODE == kGated ? 128 : 256>::kRounds +
+                                 (SAVE == kSaveBf16 ? 4 * WsRounds<uint16_t, 128>::kRounds : SAVE == kSaveMx8 ? 2 : 0);
     __shared__ __attribute__((aligned(1024))) uint16_t ring[S * kSt];
-    __shared__ int s_info[5];
+    __shared__ __attribute__((aligned(16))) int s_info[8][4];   // items of the last rounds: g, first row, end, column tile
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    FfnItem it;
-    if (!ffn_item<MODE, kWsRows, kWsCols, 0>(a, blockIdx.x, s_info, it)) return;
-    if (it.g == a.G) {
-        zero_tail<MODE, OUT_BF16, SAVE, kWsCols, kWsThreads>(a, it);
-        return;
-    }
     const int K = a.K, NN = a.NN, N = NN / 2;
-    const int row0 = it.row0, hi = it.hi, c0 = it.c0, red = it.red_hi;
-    const int lda = MODE == kGated ? K : NN;
-    const uint16_t* wg = a.b + (int64_t)it.g * K * NN;
+    const int nsl = (MODE == kGated ? K : NN) >> 6;
+    constexpr int kItemCols = MODE == kGated ? kWsCols / 2 : kWsCols;
+    if (wave == 1 && blockIdx.x == 0) {   // the call's device status word
+        const int st = group_status(a.group_sizes, a.G, a.M);
+        if (lane == 0) a.status[0] = st;
+    }
 
-    const int rows = hi - row0, nsl = red >> 6;
-    const bool mul = wave < 8;
-    v16f acc[3][2];
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    const int wm = (wave >> 2) & 1, wn = wave & 3, l32 = lane & 31, h = lane >> 5;
-
-    if (!mul) {
+    if (wave >= 8) {
         // ---- load waves, 1 KB an instruction: 8 rows of a direct operand or 2 of
         //      transposed B.  Wave p has A's instructions p, p + 4, .. (those that
-        //      hold rows) and eight of B's 32.
-        const int p = wave - 8;
-        int na = 0;
-        const uint16_t *pa[5], *pb[8];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            const DmaLane d = dma_direct<64, 8, 8>(p + 4 * i, lane);
-            na += 8 * (p + 4 * i) < rows;
-            pa[i] = a.a + (int64_t)min(row0 + d.row, hi - 1) * lda + d.col;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = p + 4 * i;
-            if constexpr (kBTr) {
-                const int r = 2 * j + (lane >> 5), c = (lane & 31) >> 1;   // row r of 64: slice r / 32
-                const int tc = 16 * (c ^ (2 * (r & 3))) + 8 * (lane & 1);
-                const int col = tc < 128 ? min(c0 + tc, N - 8) : N + min(c0 + tc - 128, N - 8);
-                pb[i] = wg + (int64_t)r * NN + col;
-            } else {
-                const DmaLane d = dma_direct<64, 8, 8>(j, lane);
-                pb[i] = wg + (int64_t)min(c0 + d.row, K - 1) * NN + d.col;
-            }
-        }
+        //      hold rows) and eight of B's 32.  The ring's slots go to the slices
+        //      of one item after the other, with one slot after each item for its
+        //      results; loading runs two slots ahead of the barriers, into the
+        //      next item where this one ends.
+        const int p = wave - 8, lda = MODE == kGated ? K : NN;
+        EvenItems items;
+        items.init(a.group_sizes, a.G, a.M, a.cap);
         const int64_t bstep = kBTr ? 64 * (int64_t)NN : 64;
-        auto issue = [&](int t, int stage) {
-            uint16_t* sa = ring + stage * kSt + 512 * p;
+        const uint16_t *pa[5], *pb[8];
+        int na = 0, round = 0, t = 0, slot = 0, left = 0;   // of the item being loaded: slices left
+        uint32_t is_item = 0, has_rows = 0;                 // of round r, at bit r % 32
+        bool valid = true;
+        auto next_item = [&]() {
+            int col;
+            const WorkItem wi = items.find(a.group_sizes, a.G, a.M, a.cap, a.ntiles_c,
+                                           (int)(blockIdx.x + round * gridDim.x), col);
+            if (p == 0) {   // in asm: an LDS write that the compiler sees would drain the ring
+                const v4i info = {wi.g, wi.lo, wi.hi, col};
+                const unsigned at = (unsigned)(uintptr_t)(GMM_LDS int*)s_info[round & 7];
+                asm volatile("ds_write_b128 %0, %1" : : "v"(at), "v"(info) : "memory");
+            }
+            valid = wi.g >= 0;
+            left = wi.g >= 0 && wi.g < a.G ? nsl : 0;
+            const uint32_t bit = 1u << (round & 31);
+            is_item = valid ? is_item | bit : is_item & ~bit;
+            has_rows = left > 0 ? has_rows | bit : has_rows & ~bit;
+            ++round;
+            t = 0;
+            if (left == 0) return;
+            const uint16_t* wg = a.b + (int64_t)wi.g * K * NN;
+            const int c0 = col * kItemCols, rows = wi.hi - wi.lo;
+            na = 0;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const DmaLane d = dma_direct<64, 8, 8>(p + 4 * i, lane);
+                na += 8 * (p + 4 * i) < rows;
+                pa[i] = a.a + (int64_t)min(wi.lo + d.row, wi.hi - 1) * lda + d.col;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = p + 4 * i;
+                if constexpr (kBTr) {
+                    const int r = 2 * j + (lane >> 5), c = (lane & 31) >> 1;   // row r of 64: slice r / 32
+                    const int tc = 16 * (c ^ (2 * (r & 3))) + 8 * (lane & 1);
+                    const int cc = tc < 128 ? min(c0 + tc, N - 8) : N + min(c0 + tc - 128, N - 8);
+                    pb[i] = wg + (int64_t)r * NN + cc;
+                } else {
+                    const DmaLane d = dma_direct<64, 8, 8>(j, lane);
+                    pb[i] = wg + (int64_t)min(c0 + d.row, K - 1) * NN + d.col;
+                }
+            }
+        };
+        // fills the next slot; returns the loads issued (none for results, or past the last item)
+        auto advance = [&]() {
+            if (!valid) return 0;
+            uint16_t* sa = ring + slot * kSt + 512 * p;
+            slot = slot == S - 1 ? 0 : slot + 1;
+            if (left == 0) {   // the item's results go here
+                next_item();
+                return 0;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint16_t* q = pb[i] + bstep * t;
@@ -1166,34 +1252,47 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
                 const uint16_t* q = pa[i] + 64 * t;
                 __builtin_amdgcn_global_load_lds(q, (GMM_LDS void*)(sa + 2048 * i), 16, 0, 0);
             }
+            ++t;
+            --left;
+            return 8 + na;
         };
-        // this wave's share of a stage has landed when at most `younger` stages
-        // of 8 + na loads are outstanding (all of them, near the end)
-        auto wait_younger = [&](bool last, auto younger) {
-            constexpr int n = decltype(younger)::value;
-            if (last) wait_vmem<0>();
-            else if (na == 5) wait_vmem<13 * n>();
-            else if (na == 4) wait_vmem<12 * n>();
-            else if (na == 3) wait_vmem<11 * n>();
-            else if (na == 2) wait_vmem<10 * n>();
-            else if (na == 1) wait_vmem<9 * n>();
-            else wait_vmem<8 * n>();
+        // waits until only the n youngest loads are outstanding
+        auto wait_younger = [&](int n) {
+            switch (n) {
+                case 13: wait_vmem<13>(); break;
+                case 12: wait_vmem<12>(); break;
+                case 11: wait_vmem<11>(); break;
+                case 10: wait_vmem<10>(); break;
+                case 9: wait_vmem<9>(); break;
+                case 8: wait_vmem<8>(); break;
+                default: wait_vmem<0>(); break;
+            }
         };
-#pragma unroll
-        for (int t = 0; t < S; ++t)
-            if (t < nsl) issue(t, t);
-        wait_younger(S - 1 >= nsl, std::integral_constant<int, S - 1>{});   // stage 0
+        next_item();
+        // slots 0 and 1; multiplying starts when slot 0 is in
+        advance();
+        int n1 = advance();   // loads of the youngest slot
+        wait_younger(n1);
         stage_barrier();
-        int stage = 0;
-        for (int t = 0; t < nsl; ++t) {
-            wait_younger(t + S - 1 >= nsl, std::integral_constant<int, S - 2>{});   // stage t + 1
-            stage_barrier();
-            if (t + S < nsl) issue(t + S, stage);
-            stage = stage == S - 1 ? 0 : stage + 1;
+        n1 = advance();
+        for (int r = 0; is_item >> (r & 31) & 1u; ++r) {   // the item being multiplied (loading is at most three ahead)
+            for (int l = has_rows >> (r & 31) & 1u ? nsl : 0; l > 0; --l) {
+                wait_younger(n1);   // the next slot is in
+                stage_barrier();    // this one has been read
+                n1 = advance();
+            }
+            wait_younger(n1);
+#pragma unroll
+            for (int e = 0; e < kEndBarriers; ++e) stage_barrier();
+            n1 = advance();
         }
-    } else {
+        return;
+    }
+
+    // ---- multiplying waves
+    const int wm = wave >> 2, wn = wave & 3, l32 = lane & 31, h = lane >> 5;
     const unsigned ring_lds = (unsigned)(uintptr_t)(GMM_LDS uint16_t*)ring;
-    unsigned ra[4], rb[4];   // of the four quarter steps, stage 0
+    unsigned ra[4], rb[4];   // of the four quarter steps, slot 0
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const int row = 32 * wm + l32;
@@ -1207,116 +1306,141 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
             rb[s] = ring_lds + (unsigned)(2 * kWsSliceA + 128 * br + 16 * ((2 * s + h) ^ direct_key<64>(br)));
         }
     }
-    stage_barrier();   // stage 0 is in
-    auto main_loop = [&](auto nbc) {
-        constexpr int NB = decltype(nbc)::value;
-        constexpr std::integral_constant<bool, kBTr> btr;
-        v8bf fa[3], fb[2], ga[3], gb[2];
-        if constexpr (NB > 0) ws_read<kBTr>(fa, fb, ra[0], rb[0]);
-        int stage = 0;
-        for (int t = 0; t < nsl; ++t) {
-            const int next = stage == S - 1 ? 0 : stage + 1;
-            const unsigned so = (unsigned)(stage * kSt * 2), so1 = (unsigned)(next * kSt * 2);
-            if constexpr (NB > 0) {   // transposed B: 16 rows on, the second slice, its rows 16 on
-                ws_step<8192>(nbc, btr, acc, fa, fb, ga, gb, ra[1] + so, rb[1] + so);
-                ws_step<16384>(nbc, btr, acc, ga, gb, fa, fb, ra[2] + so, rb[2] + so);
-                ws_step<24576>(nbc, btr, acc, fa, fb, ga, gb, ra[3] + so, rb[3] + so);
-            }
-            stage_barrier();
-            // past the last stage this reads one that nothing uses
-            if constexpr (NB > 0) ws_step<0>(nbc, btr, acc, ga, gb, fa, fb, ra[0] + so1, rb[0] + so1);
-            stage = next;
+    int slot = 0;
+    stage_barrier();   // slot 0 is in
+    for (int round = 0;; ++round) {
+        const int g = __builtin_amdgcn_readfirstlane(s_info[round & 7][0]);
+        if (g < 0) break;
+        FfnItem it;
+        it.g = g;
+        it.row0 = it.lo = __builtin_amdgcn_readfirstlane(s_info[round & 7][1]);
+        it.hi = __builtin_amdgcn_readfirstlane(s_info[round & 7][2]);
+        it.c0 = __builtin_amdgcn_readfirstlane(s_info[round & 7][3]) * kItemCols;
+        const int row0 = it.row0, rows = it.hi - it.row0, c0 = it.c0;
+        if (g == a.G) {
+            zero_tail<MODE, OUT_BF16, SAVE, kWsCols, 512>(a, it);
+#pragma unroll
+            for (int e = 0; e < kEndBarriers; ++e) stage_barrier();
+            slot = slot == S - 1 ? 0 : slot + 1;
+            continue;
         }
-    };
-    switch (((rows + 31) / 32 + 1 - wm) >> 1) {   // this wave's 32-row blocks that hold rows
-        case 0: main_loop(std::integral_constant<int, 0>{}); break;
-        case 1: main_loop(std::integral_constant<int, 1>{}); break;
-        case 2: main_loop(std::integral_constant<int, 2>{}); break;
-        default: main_loop(std::integral_constant<int, 3>{}); break;
-    }
-    // the compiler does not see the MFMAs: let the last ones finish before
-    // their results are read
-    asm volatile("s_nop 15\n\ts_nop 15"
-                 : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]),
-                   "+v"(acc[2][1]));
-    }
-    __syncthreads();
-
-    if constexpr (MODE == kGated) {
-        if constexpr (SAVE == kSaveBf16) {
+        v16f acc[3][2];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                ws_store<uint16_t, 128, 1>(a.gu + p * N, NN, row0, rows, c0, N, 32 * wn, ring, mul,
-                                            [&](int i, int, int q, float (&v)[4]) {
+        for (int i = 0; i < 3; ++i)
 #pragma unroll
-                                                for (int k = 0; k < 4; ++k) v[k] = acc[i][p][4 * q + k];
-                                            });
-        }
-        if constexpr (SAVE == kSaveMx8) {
-            // a wave's 32 gate (or up) columns of a row are one block, in lanes l and l + 32
-            constexpr int P = 256 + 16;
-            uint8_t* cm = reinterpret_cast<uint8_t*>(ring);
-            uint8_t* ss = cm + 192 * P;
-            static_assert(192 * P + 192 * 8 <= kWsBytes, "checkpoint staging fits the ring");
-            if (mul)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) m = max(m, abs_bits(acc[i][p][r]));
-                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                    const u32x2 sw = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-                    const uint32_t c = mx8_scale_code(max(sw[0], sw[1]));
-                    const float inv = mx8_inverse(c);
-                    const int r = 64 * i + 32 * wm + l32;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint32_t*>(cm + r * P + 128 * p + 32 * wn + 8 * q + 4 * h) =
-                            e4m3x4(acc[i][p][4 * q] * inv, acc[i][p][4 * q + 1] * inv, acc[i][p][4 * q + 2] * inv,
-                                   acc[i][p][4 * q + 3] * inv);
-                    if (h == 0) ss[r * 8 + 4 * p + wn] = (uint8_t)c;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+        auto main_loop = [&](auto nbc) __attribute__((always_inline)) {
+            constexpr int NB = decltype(nbc)::value;
+            constexpr std::integral_constant<bool, kBTr> btr;
+            v8bf fa[3], fb[2], ga[3], gb[2];
+            if constexpr (NB > 0) ws_read<kBTr>(fa, fb, ra[0] + (unsigned)(slot * kSt * 2), rb[0] + (unsigned)(slot * kSt * 2));
+            for (int t = 0; t < nsl; ++t) {
+                const int next = slot == S - 1 ? 0 : slot + 1;
+                const unsigned so = (unsigned)(slot * kSt * 2), so1 = (unsigned)(next * kSt * 2);
+                if constexpr (NB > 0) {   // transposed B: 16 rows on, the second slice, its rows 16 on
+                    ws_step<8192>(nbc, btr, acc, fa, fb, ga, gb, ra[1] + so, rb[1] + so);
+                    ws_step<16384>(nbc, btr, acc, ga, gb, fa, fb, ra[2] + so, rb[2] + so);
+                    ws_step<24576>(nbc, btr, acc, fa, fb, ga, gb, ra[3] + so, rb[3] + so);
                 }
-            __syncthreads();
-            for (int e = tid; e < rows * 16; e += kWsThreads) {
-                const int r = e >> 4, c = (e & 15) * 16, col = c0 + (c & 127);
-                if (col < N)
-                    store_out(a.gu_q + (int64_t)(row0 + r) * NN + (c < 128 ? 0 : N) + col,
-                              *reinterpret_cast<const uint4*>(cm + r * P + c));
+                stage_barrier();
+                // past the last slice this reads a slot without using it
+                if constexpr (NB > 0) ws_step<0>(nbc, btr, acc, ga, gb, fa, fb, ra[0] + so1, rb[0] + so1);
+                slot = next;
             }
-            for (int e = tid; e < rows * 4; e += kWsThreads) {   // pairs of scale bytes: 64 columns
-                const int r = e >> 2, p = (e >> 1) & 1, b = (e & 1) * 2;
-                if (c0 + 32 * b < N)
-                    *reinterpret_cast<uint16_t*>(a.gu_s + (int64_t)(row0 + r) * (NN / 32) + (p * N + c0) / 32 + b) =
-                        *reinterpret_cast<const uint16_t*>(ss + r * 8 + 4 * p + b);
-            }
-            __syncthreads();
+        };
+        switch (((rows + 31) / 32 + 1 - wm) >> 1) {   // this wave's 32-row blocks that hold rows
+            case 0: main_loop(std::integral_constant<int, 0>{}); break;
+            case 1: main_loop(std::integral_constant<int, 1>{}); break;
+            case 2: main_loop(std::integral_constant<int, 2>{}); break;
+            default: main_loop(std::integral_constant<int, 3>{}); break;
         }
-        using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
-        ws_store<E, 128, 1>(reinterpret_cast<E*>(a.out), N, row0, rows, c0, N, 32 * wn, ring, mul,
-                             [&](int i, int, int q, float (&v)[4]) {
+        // the compiler does not see the MFMAs: let the last ones finish before
+        // their results are read
+        asm volatile("s_nop 15\n\ts_nop 15"
+                     : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]),
+                       "+v"(acc[2][1]));
+
+        uint16_t* sm = ring + slot * kSt;   // the item's slot for results
+        slot = slot == S - 1 ? 0 : slot + 1;
+        if constexpr (MODE == kGated) {
+            if constexpr (SAVE == kSaveBf16) {
 #pragma unroll
-                                 for (int k = 0; k < 4; ++k) v[k] = silu_mul(acc[i][0][4 * q + k], acc[i][1][4 * q + k]);
-                             });
-    } else {
-        using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
-        ws_store<E, 256, 2>(reinterpret_cast<E*>(a.out), K, row0, rows, c0, K, 64 * wn, ring, mul,
-                             [&](int i, int b, int q, float (&v)[4]) {
+                for (int p = 0; p < 2; ++p)
+                    ws_store<uint16_t, 128, 1>(a.gu + p * N, NN, row0, rows, c0, N, 32 * wn, sm,
+                                               [&](int i, int, int q, float (&v)[4]) {
 #pragma unroll
-                                 for (int k = 0; k < 4; ++k) v[k] = acc[i][b][4 * q + k];
-                             });
+                                                   for (int k = 0; k < 4; ++k) v[k] = acc[i][p][4 * q + k];
+                                               });
+            }
+            if constexpr (SAVE == kSaveMx8) {
+                // a wave's 32 gate (or up) columns of a row are one block, in lanes l and l + 32
+                constexpr int P = 256 + 16;
+                uint8_t* cm = reinterpret_cast<uint8_t*>(sm);
+                uint8_t* ss = cm + kWsRows * P;
+                static_assert(kWsRows * (P + 8) <= 2 * kWsStage, "checkpoint staging fits a stage");
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (2 * i + wm >= 5) continue;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) m = max(m, abs_bits(acc[i][p][r]));
+                        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                        const u32x2 sw = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+                        const uint32_t c = mx8_scale_code(max(sw[0], sw[1]));
+                        const float inv = mx8_inverse(c);
+                        const int r = 64 * i + 32 * wm + l32;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint32_t*>(cm + r * P + 128 * p + 32 * wn + 8 * q + 4 * h) =
+                                e4m3x4(acc[i][p][4 * q] * inv, acc[i][p][4 * q + 1] * inv, acc[i][p][4 * q + 2] * inv,
+                                       acc[i][p][4 * q + 3] * inv);
+                        if (h == 0) ss[r * 8 + 4 * p + wn] = (uint8_t)c;
+                    }
+                }
+                stage_barrier();
+                for (int e = tid; e < rows * 16; e += 512) {
+                    const int r = e >> 4, c = (e & 15) * 16, col = c0 + (c & 127);
+                    if (col < N)
+                        store_out(a.gu_q + (int64_t)(row0 + r) * NN + (c < 128 ? 0 : N) + col,
+                                  *reinterpret_cast<const uint4*>(cm + r * P + c));
+                }
+                for (int e = tid; e < rows * 4; e += 512) {   // pairs of scale bytes: 64 columns
+                    const int r = e >> 2, p = (e >> 1) & 1, b = (e & 1) * 2;
+                    if (c0 + 32 * b < N)
+                        *reinterpret_cast<uint16_t*>(a.gu_s + (int64_t)(row0 + r) * (NN / 32) + (p * N + c0) / 32 + b) =
+                            *reinterpret_cast<const uint16_t*>(ss + r * 8 + 4 * p + b);
+                }
+                stage_barrier();
+            }
+            ws_store<E, 128, 1>(reinterpret_cast<E*>(a.out), N, row0, rows, c0, N, 32 * wn, sm,
+                                [&](int i, int, int q, float (&v)[4]) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) v[k] = silu_mul(acc[i][0][4 * q + k], acc[i][1][4 * q + k]);
+                                });
+        } else {
+            ws_store<E, 256, 2>(reinterpret_cast<E*>(a.out), K, row0, rows, c0, K, 64 * wn, sm,
+                                [&](int i, int b, int q, float (&v)[4]) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) v[k] = acc[i][b][4 * q + k];
+                                });
+        }
     }
 }
 
 template <int MODE, bool OUT_BF16, int SAVE>
 hipError_t launch_ws(FfnArgs a, int cap, hipStream_t stream) {
-    a.cap = cap;
     const int cols = MODE == kGated ? a.NN / 2 : a.K, tc = MODE == kGated ? kWsCols / 2 : kWsCols;
+    a.cap = cap;
     a.ntiles_r = 0;
     a.ntiles_c = (cols + tc - 1) / tc;
     a.nblocks = (int)(max_work_items(a.M, a.G < a.M ? a.G : a.M, cap) * a.ntiles_c);
-    hipLaunchKernelGGL((ffn_ws_kernel<MODE, OUT_BF16, SAVE>), dim3((unsigned)a.nblocks), dim3(kWsThreads), 0, stream, a);
+    // one workgroup per CU, a multiple of the XCDs (the items' XCD placement counts on it)
+    const int grid = (a.nblocks < device_cus() ? a.nblocks + kNumXcd - 1 : device_cus()) / kNumXcd * kNumXcd;
+    hipLaunchKernelGGL((ffn_ws_kernel<MODE, OUT_BF16, SAVE>), dim3((unsigned)grid), dim3(kWsThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -1569,20 +1693,22 @@ bool wide_tiles(int64_t row_tiles, int64_t cols) {
 // Rows an item of the 160 x 256 tiles may have, or 0 where the smaller tiles
 // are taken.  One workgroup fills a CU, so the grid should be one round of the
 // chip at least three quarters full, or two where the groups are small enough
-// (two items) for the weights to be most of what is read; past that the
-// smaller tiles, which overlap one item's start and end with another's work,
-// do better, and so they do on short reductions and (forward) on groups of few
-// rows.  Of the caps that fit, the cheapest: rounds x (the weights' columns +
-// the products of the item's rows), measured as 2 : rows / 160.  The rows of an
-// item are estimated from the mean and spread of evenly routed groups.
+// (two items) for the weights to be most of what is read; not on short
+// reductions, nor (forward) on groups of few rows.  Of the caps that fit, the
+// cheapest: rounds x (the weights' columns + the products of the item's rows),
+// measured as 2 : rows / 160.  Over more rounds dX still gains (`many`: the
+// largest cap), the forward does not.  The rows of an item are estimated from
+// the mean and spread of evenly routed groups.
 // Measured (us, smaller tiles / these; dX with the activation's gradient):
-// shard (8192 rows, 32 experts, K = 2048, 2N = 1024) forward 75.8 / 52.1, dX
-// 72.2 / 61.1, half its rows 65.0 / 43.1 and 55.3 / 38.2; output projection's
-// shape (K = 512, 2N = 4096) dX 123 / 92, its forward 64 / 75 (8 stages);
-// 2048 rows, 32 experts, forward 35.1 / 40.8; 16384 rows of one expert, K =
-// 4096, forward 119 / 149; under skewed (Zipf) routing, which the host does not
-// see, the shard's forward loses 74 / 84 and dX 73 / 77.
-int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean) {
+// shard (8192 rows, 32 experts, K = 2048, 2N = 1024) forward 75.5 / 52.2, dX
+// 71.7 / 60.5, half its rows 64.8 / 42.7 and 55.3 / 38.1; output projection's
+// shape (K = 512, 2N = 4096) dX 123 / 93, its forward (8 slices) 64.8 / 62.2;
+// production (65536 rows, 256 experts) dX 462 / 414, forward 385 / 377, Zipf
+// 468 / 441 and 390 / 394; 2048 rows, 32 experts, forward 34.8 / 41.7; 16384
+// rows of one expert, K = 4096, forward 119 / 145, dX 162 / 165.  Under skewed
+// (Zipf) routing, which the host does not see, the shard's forward loses, 73.5
+// / 80.8.
+int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean, bool many) {
     const int64_t busy = G < M ? G : M, cus = device_cus();
     const double mean = (double)M / (double)busy, high = mean + 2.0 * sqrt(mean);
     if (red < min_red || mean < min_mean) return 0;
@@ -1598,6 +1724,7 @@ int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean) {
             cost = c;
         }
     }
+    if (best == 0 && many && busy * (int64_t)ceil(high / kWsRows) * tiles > rounds * cus) return kWsRows;
     return best;
 }
 
@@ -1627,7 +1754,7 @@ hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
         if (rows <= 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, busy, stream);
         return launch_few_mb<OUT_BF16, SAVE, 4>(a, busy, stream);
     }
-    const int cap = ws_cap(a.M, a.G, a.K, (a.NN + 255) / 256, 1088, 96.0);
+    const int cap = ws_cap(a.M, a.G, a.K, (a.NN + 255) / 256, 1088, 96.0, false);
     if (cap > 0) return launch_ws<kGated, OUT_BF16, SAVE>(a, cap, stream);
     return wide_tiles(max_work_items(a.M, busy, 128), a.NN) ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream)
                                                             : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
@@ -1639,7 +1766,7 @@ bool wide_bwd(const FfnArgs& a, bool dx) {
     return wide_tiles(rows, dx ? a.K : a.NN);
 }
 
-int dx_cap(const FfnArgs& a) { return ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 1024, 48.0); }
+int dx_cap(const FfnArgs& a) { return ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 1024, 48.0, true); }
 
 template <int MODE>
 hipError_t launch_bwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {

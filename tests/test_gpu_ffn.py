@@ -637,3 +637,23 @@ def test_expert_layer_example():
     for o, lim in ((plain, 0.02), (small, 0.1)):
         for got, want in zip(o["grads"], (dx, dwgu, dwd)):
             assert np.linalg.norm(f64(got) - want) <= lim * np.linalg.norm(want)
+
+
+def test_load_waves_many_rounds():
+    """Several items a workgroup: dX of 90 groups over many column tiles, with unused rows and empty groups."""
+    s = [37, 0, 161, 5, 160, 90, 0, 64, 33] * 10
+    p = Problem(s, sum(s) + 700, 2304, 512, seed=81)      # 9 column tiles
+    dh, w, gu = p.dev("dh", "w", "gu")
+    dx, _ = gmm.gmm_bf16_swiglu_bwd(dh, w, p.gs, gu=gu, want_dw=False)
+    P = f64(p.gu)
+    backward_check(p, f64(p.x)[:p.used], grad64(p, P), dx, None, None, P, BF, BF)
+
+
+def test_load_waves_many_groups():
+    """The same with more groups than the registers of one scan hold."""
+    s = [57, 0, 90, 5, 96, 110, 0, 74, 53] * 30
+    p = Problem(s, sum(s) + 100, 576, 512, seed=91)
+    dh, w, gu = p.dev("dh", "w", "gu")
+    dx, _ = gmm.gmm_bf16_swiglu_bwd(dh, w, p.gs, gu=gu, want_dw=False, dx_dtype=F32)
+    P = f64(p.gu)
+    backward_check(p, f64(p.x)[:p.used], grad64(p, P), dx, None, None, P, F32, BF)
