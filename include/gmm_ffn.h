@@ -11,6 +11,8 @@
  * scale byte c (E8M0: 2^(c - 127)), and each value v is kept as the E4M3 code
  * nearest to v / 2^(c - 127), ties to even.  c is the smallest byte with
  * max|v| <= 448 * 2^(c - 127), 0 for an all-zero block; nothing saturates.
+ * A NaN has no part in the maximum and reads back as NaN; so does an infinity
+ * (the format has none), whose block is scaled by 2^120.
  * Codes are [M,K] bytes, scales [M,K/32] bytes: 8.25 bits a value.  A value
  * read back is exact in bf16 (magnitudes of 1.9375 * 2^127 and more round to
  * 2^128 and read back as infinity).

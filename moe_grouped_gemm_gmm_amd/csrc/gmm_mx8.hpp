@@ -35,7 +35,9 @@ __device__ __forceinline__ float mx8_scale(uint32_t c) {
     return __uint_as_float(c == 0 ? 0x00400000u : c << 23);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Bits of |v|, 0 for a NaN: it keeps its NaN code under any scale, and the
+// block's other values theirs.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(fmaxf(fabsf(v), 0.0f)); }
 
 // Four E4M3 codes -> their values times s.
 __device__ __forceinline__ void mx8_values4(uint32_t codes, float s, float (&v)[4]) {

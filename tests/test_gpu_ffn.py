@@ -316,6 +316,50 @@ def test_quantize_borders():
     assert np.array_equal(f64(gmm.gmm_dequantize_mx8(q, s, out_dtype=F32)), want)
 
 
+def test_quantize_nan_and_infinity():
+    """NaN and infinity read back as NaN; a NaN leaves its block's scale and
+    other codes alone, an infinity takes the scale 2^120."""
+    r = np.random.default_rng(8)
+    v = r.standard_normal((5, 128)).astype(np.float32)
+    v[:, 3], v[:, 40], v[:, 70], v[:, 127] = 0.0, 0.0, 0.0, 0.0
+    bad = v.copy()
+    bad[:, 3], bad[:, 40], bad[:, 70], bad[:, 127] = np.nan, -np.nan, np.inf, -np.inf
+    for dt in (BF, F32):
+        q0, s0 = gmm.gmm_quantize_mx8(torch.from_numpy(v).to(DEV, dt))
+        q, s = gmm.gmm_quantize_mx8(torch.from_numpy(bad).to(DEV, dt))
+        back = f64(gmm.gmm_dequantize_mx8(q, s, out_dtype=F32))
+        assert np.array_equal(np.isnan(back), ~np.isfinite(bad))
+        keep = np.isfinite(bad[0, :64])
+        assert np.array_equal(raw(s)[:, :2], raw(s0)[:, :2]) and (raw(s)[:, 2:] == 247).all()
+        assert np.array_equal(raw(q)[:, :64][:, keep], raw(q0)[:, :64][:, keep])
+        assert (np.nan_to_num(back[:, 64:]) == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(8, 2, 512, 128), (300, 3, 512, 192), (8000, 8, 1088, 512)],
+                         ids=["few", "tiles", "load_waves"])
+def test_forward_checkpoint_beside_a_nan(shape):
+    """A NaN column of the weights: P's column is NaN in the checkpoint, and the
+    scales and codes beside it are those of the same weights with zeros there."""
+    M, G, K, N = shape
+    r = np.random.default_rng(9)
+    x = torch.from_numpy(r.standard_normal((M, K))).to(DEV, BF)
+    w = torch.from_numpy(r.standard_normal((G, K, 2 * N)) / 32).to(DEV, BF)
+    gs = torch.tensor([M // G] * G, dtype=torch.int32, device=DEV)
+    cols = [5, 64 + 33, N + 18]
+    got = []
+    for fill in (0.0, float("nan")):
+        w[:, :, cols] = fill
+        q = torch.empty(M, 2 * N, dtype=torch.uint8, device=DEV)
+        s = torch.empty(M, 2 * N // 32, dtype=torch.uint8, device=DEV)
+        gmm.gmm_bf16_swiglu(x, w, gs, gu_q=q, gu_scale=s)
+        got.append((raw(q)[:M // G * G], raw(s)[:M // G * G]))
+    (q0, s0), (q1, s1) = got
+    assert np.array_equal(s0, s1)
+    assert ((q1[:, cols] & 0x7F) == 0x7F).all()
+    keep = np.setdiff1d(np.arange(2 * N), cols)
+    assert np.array_equal(q0[:, keep], q1[:, keep])
+
+
 def test_dequantize_every_code():
     """All 254 finite codes under every scale whose values are normal bf16 numbers."""
     codes = np.array([c for c in range(256) if c & 0x7F != 0x7F] + [0, 0], dtype=np.uint8)     # 256 = 8 blocks
