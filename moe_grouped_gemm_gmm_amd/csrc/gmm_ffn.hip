@@ -6,13 +6,18 @@
 //   kBwdW    dw[g] = x_g^T dP_g                             (reduce over rows)
 //   kBwdWQ   the same with x from an 8-bit checkpoint
 //
+// In the gated forward a tile holds gate columns in its left half and the up
+// columns of the same outputs in its right half, arranged so that gate and up
+// of one output meet in one lane's accumulators: the activation, the product
+// and the checkpoint of P are an epilogue on registers.
+//
 // Operands move from global memory to LDS with the load-to-LDS instructions
-// into a ring of S stages (gmm_tile.hpp); each wave owns 64 x 64 of the tile.
-// The gated forward's tile holds gate columns in its left half and the up
-// columns of the same outputs in its right half, and a wave owns 32 of each,
-// so gate and up of one output meet in one lane's accumulators and the
-// activation, the product and the checkpoint of P are an epilogue on
-// registers.
+// (gmm_tile.hpp) and from there to 16 x 16 x 32 or 32 x 32 x 16 MFMAs, sums in
+// fp32.  In the order they stand here:
+//   ffn_kernel       128 x 128 or 128 x 256 tiles, every product
+//   ffn_bwd_kernel   both products of a small backward pass in one launch
+//   ffn_ws_kernel    160 x 256 tiles fed by load waves, forward and dX
+//   gated_few_kernel the forward for few rows per expert, K split over waves
 #include "gmm_launch.hpp"
 #include "gmm_mx8.hpp"
 #include "gmm_tile.hpp"
@@ -316,9 +321,10 @@ __device__ __forceinline__ void mx8_expand16(const u32x4& codes, uint32_t scale_
 
 // ---- fragment reads of one 32-deep slice, one asm block and one wait each.
 // A wave's four direct fragments of A sit 2048 bytes apart (every other 16 rows
-// of 64 bytes, the same swizzle key), direct fragments of B 1024 bytes; a wave's transposed fragments j and j + 4 of B 256 bytes
-// apart (columns 128 apart: the key only permutes the low 3 bits of the
-// 32-byte chunk); the second half of a transposed fragment HA / HB bytes on.
+// of 64 bytes, the same swizzle key), direct fragments of B 1024 bytes; a
+// wave's transposed fragments j and j + 4 of B 256 bytes apart (columns 128
+// apart: the key only permutes the low 3 bits of the 32-byte chunk); the second
+// half of a transposed fragment HA / HB bytes on.
 
 template <int HB>
 __device__ __forceinline__ void read_direct_tr8(v8bf (&fa)[4], v8bf (&fb)[8], unsigned a, const unsigned (&b)[4]) {
@@ -1692,39 +1698,53 @@ bool wide_tiles(int64_t row_tiles, int64_t cols) {
 
 // Rows an item of the 160 x 256 tiles may have, or 0 where the smaller tiles
 // are taken.  One workgroup fills a CU, so the grid should be one round of the
-// chip at least three quarters full, or two where the groups are small enough
-// (two items) for the weights to be most of what is read; not on short
-// reductions, nor (forward) on groups of few rows.  Of the caps that fit, the
-// cheapest: rounds x (the weights' columns + the products of the item's rows),
-// measured as 2 : rows / 160.  Over more rounds dX still gains (`many`: the
-// largest cap), the forward does not.  The rows of an item are estimated from
-// the mean and spread of evenly routed groups.
-// Measured (us, smaller tiles / these; dX with the activation's gradient):
-// shard (8192 rows, 32 experts, K = 2048, 2N = 1024) forward 75.5 / 52.2, dX
-// 71.7 / 60.5, half its rows 64.8 / 42.7 and 55.3 / 38.1; output projection's
-// shape (K = 512, 2N = 4096) dX 123 / 93, its forward (8 slices) 64.8 / 62.2;
-// production (65536 rows, 256 experts) dX 462 / 414, forward 385 / 377, Zipf
-// 468 / 441 and 390 / 394; 2048 rows, 32 experts, forward 34.8 / 41.7; 16384
-// rows of one expert, K = 4096, forward 119 / 145, dX 162 / 165.  Under skewed
-// (Zipf) routing, which the host does not see, the shard's forward loses, 73.5
-// / 80.8.
+// chip at least three quarters full.  Two such rounds pay for dX where the
+// groups are small enough (two items) for the weights to be most of what is
+// read, and for the forward where besides the rows of x lie a multiple of 4 KB
+// apart: the smaller tiles read those rows 64 bytes at a time and run into one
+// set of memory channels (8192 rows, 32 experts, 2N = 1024: K = 1536 47 us, K =
+// 2048 80).  Over more rounds dX still gains (`many`: the largest cap), the
+// forward does not.  Of the caps that fit, the cheapest: rounds x (the weights'
+// columns + the products of the item's rows), measured as 2 : rows / 160.  Not
+// on short reductions, nor (forward) on groups of few rows.  The rows of an
+// item are estimated from the mean and spread of evenly routed groups.
+// Measured (us, smaller tiles / these; dX with the activation's gradient; rows,
+// experts, K, 2N):
+//   one round: 8192, 32, 2048, 1024 forward 80.3 / 57.0; 16384, 64, 1024, 512
+//   36.9 / 30.5; 8192, 32, 768, 512 20.2 / 19.2; 8192, 16, 1024, 640 23.3 /
+//   24.3; dX 4096, 32, 2048, 1024 54.2 / 38.3; 8192, 16, 1024, 640 29.1 / 24.5;
+//   8192, 32, 768, 512 19.6 / 19.7
+//   two: 16384, 64, 2048, 1024 forward 122 / 104, dX 123 / 107; forward with
+//   other pitches 12000, 60, 1024, 1024 51.0 / 55.6; 10000, 64, 1536, 1024 66.1
+//   / 74.6; with three items a group 6000, 20, 2048, 1280 53.6 / 61.4; less
+//   than three quarters full: dX 5000, 12, 2048, 1024 39.5 / 46.0
+//   more: 65536, 256, 2048, 1024 dX 456 / 403, forward 385 / 377 (Zipf 390 /
+//   394); 24000, 64, 2048, 1024 dX 161 / 151; 16384, 1, 4096, 1024 forward 119 /
+//   145
+//   short or few: forward 3000, 8, 512, 2048 17.1 / 18.1; 2048, 32, 2048, 1024
+//   34.8 / 41.7
+// Under skewed (Zipf) routing, which the host does not see, the forward of 8192
+// rows loses, 73.5 / 80.8.
 int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean, bool many) {
     const int64_t busy = G < M ? G : M, cus = device_cus();
     const double mean = (double)M / (double)busy, high = mean + 2.0 * sqrt(mean);
     if (red < min_red || mean < min_mean) return 0;
-    const int64_t rounds = mean <= 2 * kWsRows ? 2 : 1;
+    const auto full = [&](int64_t wgs, int64_t r) { return 4 * wgs >= 3 * r * cus; };
     int best = 0;
     double cost = 0.0;
     for (int cap = 64; cap <= kWsRows; cap += 32) {
-        const int64_t n = (int64_t)ceil(high / cap), wgs = busy * n * tiles;
-        if (4 * wgs < 3 * cus || wgs > rounds * cus) continue;
-        const double c = (double)((wgs + cus - 1) / cus) * (2.0 + mean / (double)n / 160.0);
+        const int64_t n = (int64_t)ceil(high / cap), wgs = busy * n * tiles, r = (wgs + cus - 1) / cus;
+        if (!full(wgs, r) || r > ((many ? mean <= 2 * kWsRows : n <= 2 && red % 2048 == 0) ? 2 : 1)) continue;
+        const double c = (double)r * (2.0 + mean / (double)n / 160.0);
         if (best == 0 || c < cost) {
             best = cap;
             cost = c;
         }
     }
-    if (best == 0 && many && busy * (int64_t)ceil(high / kWsRows) * tiles > rounds * cus) return kWsRows;
+    if (best == 0 && many) {
+        const int64_t wgs = busy * (int64_t)ceil(high / kWsRows) * tiles, r = (wgs + cus - 1) / cus;
+        if (r > 1 && full(wgs, r)) return kWsRows;
+    }
     return best;
 }
 
@@ -1754,7 +1774,7 @@ hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
         if (rows <= 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, busy, stream);
         return launch_few_mb<OUT_BF16, SAVE, 4>(a, busy, stream);
     }
-    const int cap = ws_cap(a.M, a.G, a.K, (a.NN + 255) / 256, 1088, 96.0, false);
+    const int cap = ws_cap(a.M, a.G, a.K, (a.NN + 255) / 256, 768, 96.0, false);
     if (cap > 0) return launch_ws<kGated, OUT_BF16, SAVE>(a, cap, stream);
     return wide_tiles(max_work_items(a.M, busy, 128), a.NN) ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream)
                                                             : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
@@ -1766,7 +1786,7 @@ bool wide_bwd(const FfnArgs& a, bool dx) {
     return wide_tiles(rows, dx ? a.K : a.NN);
 }
 
-int dx_cap(const FfnArgs& a) { return ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 1024, 48.0, true); }
+int dx_cap(const FfnArgs& a) { return ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 512, 48.0, true); }
 
 template <int MODE>
 hipError_t launch_bwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {

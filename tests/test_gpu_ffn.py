@@ -701,3 +701,27 @@ def test_load_waves_many_groups():
     dx, _ = gmm.gmm_bf16_swiglu_bwd(dh, w, p.gs, gu=gu, want_dw=False, dx_dtype=F32)
     P = f64(p.gu)
     backward_check(p, f64(p.x)[:p.used], grad64(p, P), dx, None, None, P, F32, BF)
+
+
+# Many weight-gradient tiles: the persistent form, several tiles a workgroup.
+WGRAD = [
+    # every part of a 64-row slice, empty groups, a half row tile and a partial column tile
+    ([0, 1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 128, 129, 193, 0, 300] * 2, 2740, 576, 448),
+    # one group with most of the rows
+    ([10, 0, 70] * 6 + [2000] + [10, 0, 70] * 7, 3100, 512, 512),
+    ([5, 0, 0, 0, 90] * 50, 4750, 192, 512),              # 250 groups, most of them empty
+]
+WG_IDS = ["M%d_K%d_N%d_G%d" % (M, K, N, len(s)) for s, M, K, N in WGRAD]
+
+
+@pytest.mark.parametrize("shape", WGRAD, ids=WG_IDS)
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mx8"])
+@pytest.mark.parametrize("dxt,dwt", [(BF, BF), (F32, F32)], ids=["bf16", "f32"])
+def test_backward_many_tiles(shape, mx, dxt, dwt):
+    test_backward(shape, mx, dxt, dwt)
+
+
+@pytest.mark.parametrize("shape", [(s, M, K, 2 * N) for s, M, K, N in WGRAD], ids=WG_IDS)
+@pytest.mark.parametrize("dwt", [BF, F32], ids=["bf16", "f32"])
+def test_weight_gradient_many_tiles(shape, dwt):
+    test_weight_gradient(shape, dwt)
