@@ -372,7 +372,7 @@ __device__ __forceinline__ void read_direct_direct(v8bf (&fa)[4], v8bf (&fb)[NJ]
             "ds_read_b128 %4, %13\n\t"
             "ds_read_b128 %5, %13 offset:1024\n\t"
             "ds_read_b128 %6, %13 offset:2048\n\t"
-            "ds_read_b128 %7, %13 offset:3072\n\t"
+            "ds_read_b128 %7, %13 offset:3*1024\n\t"
             "ds_read_b128 %8, %13 offset:4096\n\t"
             "ds_read_b128 %9, %13 offset:5120\n\t"
             "ds_read_b128 %10, %13 offset:6144\n\t"
@@ -391,7 +391,7 @@ __device__ __forceinline__ void read_direct_direct(v8bf (&fa)[4], v8bf (&fb)[NJ]
             "ds_read_b128 %4, %9\n\t"
             "ds_read_b128 %5, %9 offset:1024\n\t"
             "ds_read_b128 %6, %9 offset:2048\n\t"
-            "ds_read_b128 %7, %9 offset:3072\n\t"
+            "ds_read_b128 %7, %9 offset:3*1024\n\t"
             "ds_read_b128 %1, %8 offset:2048\n\t"
             "ds_read_b128 %2, %8 offset:4096\n\t"
             "ds_read_b128 %3, %8 offset:6144\n\t"
