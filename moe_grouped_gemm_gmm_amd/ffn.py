@@ -37,8 +37,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # stream comes from torch's raw lookup, and calls whose workspace is only the
 # status word (nothing reads it when the caller gives no workspace) share one.
 
-def _arg(t: Optional[torch.Tensor], want, dtypes: tuple, name: str) -> Optional[int]:
-    """Address of t after checking its shape (want, unless None), dtype and layout."""
+def _arg(t: Optional[torch.Tensor], want, dtypes: tuple, name: str, dev: torch.device) -> Optional[int]:
+    """Address of t after checking its dtype, shape (want, unless None), layout and device: dev, that of the
+    call's first operand, which _stream checks (a host address would fault in the kernel)."""
     if t is None:
         return None
     if t.dtype not in dtypes:
@@ -47,23 +48,30 @@ def _arg(t: Optional[torch.Tensor], want, dtypes: tuple, name: str) -> Optional[
         raise ValueError("%s is %s, not %s" % (name, tuple(t.shape), tuple(want)))
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
+    if t.device != dev:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
     return t.data_ptr()
 
 
-def _stream(t: torch.Tensor) -> int:
-    if _raw_stream is not None and t.device.index is not None:
-        return _raw_stream(t.device.index)
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _stream(dev: torch.device) -> int:
+    """torch's current stream on dev."""
+    if dev.type != "cuda":
+        raise ValueError("the tensors are on %s, not on a GPU" % dev)
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _status(ws: Optional[torch.Tensor], device):
+def _status(ws: Optional[torch.Tensor], dev: torch.device):
     """(address, bytes) of ws, or of the device's shared status block."""
     if ws is None:
-        ws = _status_ws.get(device)
+        ws = _status_ws.get(dev)
         if ws is None:
-            ws = _status_ws[device] = torch.empty(256, dtype=torch.uint8, device=device)
+            ws = _status_ws[dev] = torch.empty(256, dtype=torch.uint8, device=dev)
     elif not ws.is_contiguous():
         raise ValueError("tensors must be contiguous")
+    elif ws.device != dev:
+        raise ValueError("ws is on %s, not on %s" % (ws.device, dev))
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -77,14 +85,15 @@ def gmm_quantize_mx8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: O
     """8-bit checkpoint of x [M,K] (bf16/fp32, K a multiple of 32): E4M3 codes
     uint8 [M,K] and E8M0 scales uint8 [M,K/32]."""
     lib = load_library()
+    dev = x.device
     M, K = x.shape
-    xp = _arg(x, None, _FLOAT, "x")
+    xp = _arg(x, None, _FLOAT, "x", dev)
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        q = torch.empty((M, K), dtype=torch.uint8, device=dev)
     if scale is None:
-        scale = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    _check(lib, lib.gmm_quantize_mx8(xp, _DT[x.dtype], M, K, _arg(q, (M, K), _BYTES, "q"),
-                                     _arg(scale, (M, K // 32), _U8, "scale"), _stream(x)))
+        scale = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+    _check(lib, lib.gmm_quantize_mx8(xp, _DT[x.dtype], M, K, _arg(q, (M, K), _BYTES, "q", dev),
+                                     _arg(scale, (M, K // 32), _U8, "scale", dev), _stream(dev)))
     return q, scale
 
 
@@ -92,11 +101,12 @@ def gmm_dequantize_mx8(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dt
                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values [M,K] (bf16 or fp32) of an 8-bit checkpoint."""
     lib = load_library()
+    dev = q.device
     M, K = q.shape
-    qp, sp = _arg(q, None, _BYTES, "q"), _arg(scale, (M, K // 32), _U8, "scale")
+    qp, sp = _arg(q, None, _BYTES, "q", dev), _arg(scale, (M, K // 32), _U8, "scale", dev)
     if out is None:
-        out = torch.empty((M, K), dtype=out_dtype, device=q.device)
-    _check(lib, lib.gmm_dequantize_mx8(qp, sp, M, K, _arg(out, (M, K), _FLOAT, "out"), _DT[out.dtype], _stream(q)))
+        out = torch.empty((M, K), dtype=out_dtype, device=dev)
+    _check(lib, lib.gmm_dequantize_mx8(qp, sp, M, K, _arg(out, (M, K), _FLOAT, "out", dev), _DT[out.dtype], _stream(dev)))
     return out
 
 
@@ -109,19 +119,20 @@ def gmm_bf16_swiglu(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Ten
     gu [M,2N] bf16, or gu_q [M,2N] uint8 and gu_scale [M,2N/32] uint8 (an 8-bit
     checkpoint), receives P."""
     lib = load_library()
+    dev = lhs.device
     M, K = lhs.shape
     G, K2, N2 = rhs.shape
     if K2 != K or N2 % 2:
         raise ValueError("lhs K=%d but rhs %s" % (K, tuple(rhs.shape)))
     N = N2 // 2
-    args = (_arg(lhs, None, _BF16, "lhs"), _arg(rhs, None, _BF16, "rhs"),
-            _arg(group_sizes, (G,), _INT32, "group_sizes"), M, K, N, G)
-    kept = (_arg(gu, (M, N2), _BF16, "gu"), _arg(gu_q, (M, N2), _BYTES, "gu_q"),
-            _arg(gu_scale, (M, N2 // 32), _U8, "gu_scale"))
+    args = (_arg(lhs, None, _BF16, "lhs", dev), _arg(rhs, None, _BF16, "rhs", dev),
+            _arg(group_sizes, (G,), _INT32, "group_sizes", dev), M, K, N, G)
+    kept = (_arg(gu, (M, N2), _BF16, "gu", dev), _arg(gu_q, (M, N2), _BYTES, "gu_q", dev),
+            _arg(gu_scale, (M, N2 // 32), _U8, "gu_scale", dev))
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=lhs.device)
-    _check(lib, lib.gmm_bf16_swiglu(*args, _arg(out, (M, N), _FLOAT, "out"), _DT[out.dtype], *kept,
-                                    *_status(ws, lhs.device), _stream(lhs)))
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _check(lib, lib.gmm_bf16_swiglu(*args, _arg(out, (M, N), _FLOAT, "out", dev), _DT[out.dtype], *kept,
+                                    *_status(ws, dev), _stream(dev)))
     return out
 
 
@@ -140,16 +151,16 @@ def gmm_bf16_swiglu_bwd(dh: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.
     that gradient out (None).  h [M,N] bf16, if given, receives the forward's
     output recomputed from the kept P."""
     lib = load_library()
+    dev = dh.device
     M, N = dh.shape
     G, K, N2 = rhs.shape
     if N2 != 2 * N:
         raise ValueError("dh N=%d but rhs %s" % (N, tuple(rhs.shape)))
-    args = (_arg(dh, None, _BF16, "dh"), _arg(rhs, None, _BF16, "rhs"),
-            _arg(group_sizes, (G,), _INT32, "group_sizes"), _arg(lhs, (M, K), _BF16, "lhs"),
-            _arg(lhs_q, (M, K), _BYTES, "lhs_q"), _arg(lhs_scale, (M, K // 32), _U8, "lhs_scale"),
-            _arg(gu, (M, N2), _BF16, "gu"), _arg(gu_q, (M, N2), _BYTES, "gu_q"),
-            _arg(gu_scale, (M, N2 // 32), _U8, "gu_scale"), M, K, N, G)
-    dev = dh.device
+    args = (_arg(dh, None, _BF16, "dh", dev), _arg(rhs, None, _BF16, "rhs", dev),
+            _arg(group_sizes, (G,), _INT32, "group_sizes", dev), _arg(lhs, (M, K), _BF16, "lhs", dev),
+            _arg(lhs_q, (M, K), _BYTES, "lhs_q", dev), _arg(lhs_scale, (M, K // 32), _U8, "lhs_scale", dev),
+            _arg(gu, (M, N2), _BF16, "gu", dev), _arg(gu_q, (M, N2), _BYTES, "gu_q", dev),
+            _arg(gu_scale, (M, N2 // 32), _U8, "gu_scale", dev), M, K, N, G)
     if dx is None and want_dx:
         dx = torch.empty((M, K), dtype=dx_dtype, device=dev)
     if dw is None and want_dw:
@@ -157,9 +168,9 @@ def gmm_bf16_swiglu_bwd(dh: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.
     if ws is None:
         ws = torch.empty(256 + 4 * M * N, dtype=torch.uint8, device=dev)
     _check(lib, lib.gmm_bf16_swiglu_bwd(
-        *args, _arg(dx, (M, K), _FLOAT, "dx"), 0 if dx is None else _DT[dx.dtype],
-        _arg(dw, (G, K, N2), _FLOAT, "dw"), 0 if dw is None else _DT[dw.dtype], _arg(h, (M, N), _BF16, "h"),
-        *_status(ws, dev), _stream(dh)))
+        *args, _arg(dx, (M, K), _FLOAT, "dx", dev), 0 if dx is None else _DT[dx.dtype],
+        _arg(dw, (G, K, N2), _FLOAT, "dw", dev), 0 if dw is None else _DT[dw.dtype], _arg(h, (M, N), _BF16, "h", dev),
+        *_status(ws, dev), _stream(dev)))
     return dx, dw
 
 
@@ -169,17 +180,18 @@ def tgmm_mx8(x_q: torch.Tensor, x_scale: torch.Tensor, dy: torch.Tensor, group_s
     """dW [G,K,N]: dW[g] = X_g^T dY_g with X kept as an 8-bit checkpoint
     (x_q [M,K], x_scale [M,K/32]) and dy [M,N] bf16."""
     lib = load_library()
+    dev = x_q.device
     M, K = x_q.shape
     M2, N = dy.shape
     if M2 != M:
         raise ValueError("x has %d rows but dy has %d" % (M, M2))
     G = group_sizes.numel()
-    args = (_arg(x_q, None, _BYTES, "x_q"), _arg(x_scale, (M, K // 32), _U8, "x_scale"), _arg(dy, None, _BF16, "dy"),
-            _arg(group_sizes, (G,), _INT32, "group_sizes"), M, K, N, G)
+    args = (_arg(x_q, None, _BYTES, "x_q", dev), _arg(x_scale, (M, K // 32), _U8, "x_scale", dev),
+            _arg(dy, None, _BF16, "dy", dev), _arg(group_sizes, (G,), _INT32, "group_sizes", dev), M, K, N, G)
     if out is None:
-        out = torch.empty((G, K, N), dtype=out_dtype, device=dy.device)
-    _check(lib, lib.tgmm_mx8(*args, _arg(out, (G, K, N), _FLOAT, "out"), _DT[out.dtype], *_status(ws, dy.device),
-                             _stream(dy)))
+        out = torch.empty((G, K, N), dtype=out_dtype, device=dev)
+    _check(lib, lib.tgmm_mx8(*args, _arg(out, (G, K, N), _FLOAT, "out", dev), _DT[out.dtype], *_status(ws, dev),
+                             _stream(dev)))
     return out
 
 
