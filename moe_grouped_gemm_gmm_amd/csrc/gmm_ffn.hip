@@ -1125,12 +1125,24 @@ struct WsRounds {
     static constexpr int RB = 2 * kWsStage / kBlock, kRounds = (5 + RB - 1) / RB;
     static_assert(RB >= 1, "32 staged rows fit a stage");
 };
+
+// threadIdx.x as a value that the compiler takes for new: addresses made from
+// it are made where they are used, at an item's end, instead of being held in
+// registers over the items and their main loops (with fp32 results and P kept
+// the kernel would spill 13 to 34 registers: the shard's forward with an 8-bit
+// P 64.7 us, 57.5 without the spills).
+__device__ __forceinline__ int fresh_tid() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
 template <typename E, int WID, int NC, typename Val>
-__device__ __forceinline__ void ws_store(E* out, int64_t ld, int row0, int rows, int col0, int cols, int wcol,
-                                          uint16_t* sm, Val val) {
+__device__ __forceinline__ void ws_store(int tid, E* out, int64_t ld, int row0, int rows, int col0, int cols,
+                                          int wcol, uint16_t* sm, Val val) {
     using R = WsRounds<E, WID>;
     constexpr int C = R::C, P = R::P, RB = R::RB;
-    const int tid = threadIdx.x, lane = lane_id(), wm = tid >> 8;
+    const int lane = tid & 63, wm = __builtin_amdgcn_readfirstlane(tid >> 8);
     E* s = reinterpret_cast<E*>(sm);
 #pragma unroll
     for (int k = 0; k < R::kRounds; ++k) {
@@ -1374,7 +1386,7 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
             if constexpr (SAVE == kSaveBf16) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    ws_store<uint16_t, 128, 1>(a.gu + p * N, NN, row0, rows, c0, N, 32 * wn, sm,
+                    ws_store<uint16_t, 128, 1>(fresh_tid(), a.gu + p * N, NN, row0, rows, c0, N, 32 * wn, sm,
                                                [&](int i, int, int q, float (&v)[4]) {
 #pragma unroll
                                                    for (int k = 0; k < 4; ++k) v[k] = acc[i][p][4 * q + k];
@@ -1383,6 +1395,7 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
             if constexpr (SAVE == kSaveMx8) {
                 // a wave's 32 gate (or up) columns of a row are one block, in lanes l and l + 32
                 constexpr int P = 256 + 16;
+                const int tid = fresh_tid(), l32 = tid & 31, h = (tid >> 5) & 1;
                 uint8_t* cm = reinterpret_cast<uint8_t*>(sm);
                 uint8_t* ss = cm + kWsRows * P;
                 static_assert(kWsRows * (P + 8) <= 2 * kWsStage, "checkpoint staging fits a stage");
@@ -1422,13 +1435,18 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
                 }
                 stage_barrier();
             }
-            ws_store<E, 128, 1>(reinterpret_cast<E*>(a.out), N, row0, rows, c0, N, 32 * wn, sm,
+            // h over the gate sums, so that no second set of values is live
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][0][r] = silu_mul(acc[i][0][r], acc[i][1][r]);
+            ws_store<E, 128, 1>(SAVE == kSaveNone ? tid : fresh_tid(), reinterpret_cast<E*>(a.out), N, row0, rows, c0, N, 32 * wn, sm,
                                 [&](int i, int, int q, float (&v)[4]) {
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) v[k] = silu_mul(acc[i][0][4 * q + k], acc[i][1][4 * q + k]);
+                                    for (int k = 0; k < 4; ++k) v[k] = acc[i][0][4 * q + k];
                                 });
         } else {
-            ws_store<E, 256, 2>(reinterpret_cast<E*>(a.out), K, row0, rows, c0, K, 64 * wn, sm,
+            ws_store<E, 256, 2>(tid, reinterpret_cast<E*>(a.out), K, row0, rows, c0, K, 64 * wn, sm,
                                 [&](int i, int b, int q, float (&v)[4]) {
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) v[k] = acc[i][b][4 * q + k];
