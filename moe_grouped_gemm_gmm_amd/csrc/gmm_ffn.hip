@@ -844,10 +844,17 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 // blocks x 2 column blocks of 32 x 32 x 16) with the fragments already in
 // registers, and between them the LDS reads of the next 16, all in one asm
 // block that waits for its reads at its end, so that they take the matrix
-// unit's time and no register is read before its load.  A comes from NB
-// direct fragments 8192 bytes apart; B from two transposed fragments 256 bytes
-// apart, second halves 2048 bytes on (BTR), or two direct ones 4096 bytes
-// apart.  OB is added to transposed B's address.
+// unit's time and no register is read before its load.  The compiler does not
+// see the MFMAs, so the block also waits for their results itself: 12 wait
+// states after the last one (s_nop 11, what the compiler keeps behind its own
+// builtin before anything reads or overwrites the result), and two before the
+// first for operands that vector instructions wrote.  Whatever register
+// allocation places between two blocks or behind the last is then safe.  The
+// wait falls into the time of the last MFMA (32 cycles, before which the next
+// block's first cannot start).  A comes from NB direct fragments 8192 bytes
+// apart; B from two transposed fragments 256 bytes apart, second halves 2048
+// bytes on (BTR), or two direct ones 4096 bytes apart.  OB is added to
+// transposed B's address.
 template <int OB>
 __device__ __forceinline__ void ws_step(std::integral_constant<int, 1>, std::integral_constant<bool, true>, v16f (&acc)[3][2],
                                          const v8bf (&fa)[3], const v8bf (&fb)[2], v8bf (&ga)[3], v8bf (&gb)[2], unsigned a,
@@ -863,6 +870,7 @@ __device__ __forceinline__ void ws_step(std::integral_constant<int, 1>, std::int
         "v_mfma_f32_32x32x16_bf16 %1, %9, %7, %1\n\t"
         "ds_read_b64_tr_b16 %6, %11 offset:%15\n\t"
         "ds_read_b128 %2, %10 offset:0\n\t"
+        "s_nop 11\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "+v"(acc[0][0]), "+v"(acc[0][1]),
           "=&v"(na0), "=&v"(nb0), "=&v"(nb1), "=&v"(nb2), "=&v"(nb3)
@@ -887,6 +895,7 @@ __device__ __forceinline__ void ws_step(std::integral_constant<int, 1>, std::int
         "ds_read_b128 %4, %9 offset:%11\n\t"
         "v_mfma_f32_32x32x16_bf16 %1, %7, %5, %1\n\t"
         "ds_read_b128 %2, %8 offset:0\n\t"
+        "s_nop 11\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "+v"(acc[0][0]), "+v"(acc[0][1]),
           "=&v"(na0), "=&v"(nb0), "=&v"(nb1)
@@ -916,6 +925,7 @@ __device__ __forceinline__ void ws_step(std::integral_constant<int, 2>, std::int
         "ds_read_b128 %4, %14 offset:0\n\t"
         "ds_read_b128 %5, %14 offset:8192\n\t"
         "v_mfma_f32_32x32x16_bf16 %3, %13, %11, %3\n\t"
+        "s_nop 11\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]),
           "=&v"(na0), "=&v"(na1), "=&v"(nb0), "=&v"(nb1), "=&v"(nb2), "=&v"(nb3)
@@ -944,6 +954,7 @@ __device__ __forceinline__ void ws_step(std::integral_constant<int, 2>, std::int
         "ds_read_b128 %4, %12 offset:0\n\t"
         "v_mfma_f32_32x32x16_bf16 %3, %11, %9, %3\n\t"
         "ds_read_b128 %5, %12 offset:8192\n\t"
+        "s_nop 11\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]),
           "=&v"(na0), "=&v"(na1), "=&v"(nb0), "=&v"(nb1)
@@ -977,6 +988,7 @@ __device__ __forceinline__ void ws_step(std::integral_constant<int, 3>, std::int
         "ds_read_b128 %8, %18 offset:16384\n\t"
         "v_mfma_f32_32x32x16_bf16 %4, %16, %15, %4\n\t"
         "v_mfma_f32_32x32x16_bf16 %5, %17, %15, %5\n\t"
+        "s_nop 11\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]), "+v"(acc[2][1]),
           "=&v"(na0), "=&v"(na1), "=&v"(na2), "=&v"(nb0), "=&v"(nb1), "=&v"(nb2), "=&v"(nb3)
@@ -1009,6 +1021,7 @@ __device__ __forceinline__ void ws_step(std::integral_constant<int, 3>, std::int
         "v_mfma_f32_32x32x16_bf16 %4, %14, %13, %4\n\t"
         "ds_read_b128 %8, %16 offset:16384\n\t"
         "v_mfma_f32_32x32x16_bf16 %5, %15, %13, %5\n\t"
+        "s_nop 11\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]), "+v"(acc[2][1]),
           "=&v"(na0), "=&v"(na1), "=&v"(na2), "=&v"(nb0), "=&v"(nb1)
@@ -1374,11 +1387,6 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
             case 2: main_loop(std::integral_constant<int, 2>{}); break;
             default: main_loop(std::integral_constant<int, 3>{}); break;
         }
-        // the compiler does not see the MFMAs: let the last ones finish before
-        // their results are read
-        asm volatile("s_nop 15\n\ts_nop 15"
-                     : "+v"(acc[0][0]), "+v"(acc[0][1]), "+v"(acc[1][0]), "+v"(acc[1][1]), "+v"(acc[2][0]),
-                       "+v"(acc[2][1]));
 
         uint16_t* sm = ring + slot * kSt;   // the item's slot for results
         slot = slot == S - 1 ? 0 : slot + 1;
