@@ -11,7 +11,8 @@ using namespace gmm::abi;
 
 namespace {
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+// A launch holds fewer than 2^32 threads: workgroups of 256 in one grid.
+constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
 
 // A tensor with one row per row of the problem: may be NULL when there are none.
 int check_rows_ptr(const void* p, const char* name, int64_t M) {
@@ -33,7 +34,7 @@ int check_kept(const void* plain, const uint8_t* q, const uint8_t* scale, const 
 int check_blocks(int64_t M, int64_t K) {
     if (M < 0 || M > kMaxDim) return fail(GMM_ERR_SHAPE, "M=%lld out of range", (long long)M);
     GMM_TRY(check_mult(K, gmm::kMx8BlockSize, "K"));
-    if (M * (K / 8) / 256 + 1 > kMaxGrid) return fail(GMM_ERR_SHAPE, "tensor too large");
+    if (M * (K / 8) > kMaxDim * 256) return fail(GMM_ERR_SHAPE, "tensor too large");
     return GMM_OK;
 }
 

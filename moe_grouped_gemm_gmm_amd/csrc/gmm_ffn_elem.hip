@@ -150,28 +150,48 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t* __restr
 
 }  // namespace
 
+// Threads of one launch of the two kernels above; a launch holds fewer than
+// 2^32, so tensors of 2^34 values and more take several.  A multiple of a
+// block's four lanes.
+constexpr int64_t kChunk = int64_t(1) << 31;
+
 hipError_t launch_quantize_mx8(const void* x, bool x_bf16, int64_t M, int64_t K, uint8_t* q, uint8_t* scale,
                                hipStream_t stream) {
-    const int64_t n8 = M * K / 8;
-    const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
-    if (x_bf16)
-        hipLaunchKernelGGL((quantize_mx8_kernel<Bf16Source>), grid, block, 0, stream,
-                           Bf16Source{reinterpret_cast<const uint16_t*>(x)}, n8, q, scale);
-    else
-        hipLaunchKernelGGL((quantize_mx8_kernel<F32Source>), grid, block, 0, stream,
-                           F32Source{reinterpret_cast<const float*>(x)}, n8, q, scale);
-    return hipGetLastError();
+    const int64_t total = M * K / 8;
+    for (int64_t first = 0; first < total; first += kChunk) {
+        const int64_t n8 = total - first < kChunk ? total - first : kChunk;
+        const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
+        if (x_bf16)
+            hipLaunchKernelGGL((quantize_mx8_kernel<Bf16Source>), grid, block, 0, stream,
+                               Bf16Source{reinterpret_cast<const uint16_t*>(x) + 8 * first}, n8, q + 8 * first,
+                               scale + first / 4);
+        else
+            hipLaunchKernelGGL((quantize_mx8_kernel<F32Source>), grid, block, 0, stream,
+                               F32Source{reinterpret_cast<const float*>(x) + 8 * first}, n8, q + 8 * first,
+                               scale + first / 4);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_dequantize_mx8(const uint8_t* q, const uint8_t* scale, int64_t M, int64_t K, void* out,
                                  bool out_bf16, hipStream_t stream) {
-    const int64_t n8 = M * K / 8;
-    const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
-    if (out_bf16)
-        hipLaunchKernelGGL((dequantize_mx8_kernel<true>), grid, block, 0, stream, q, scale, n8, out);
-    else
-        hipLaunchKernelGGL((dequantize_mx8_kernel<false>), grid, block, 0, stream, q, scale, n8, out);
-    return hipGetLastError();
+    const int64_t total = M * K / 8;
+    for (int64_t first = 0; first < total; first += kChunk) {
+        const int64_t n8 = total - first < kChunk ? total - first : kChunk;
+        const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
+        char* o = static_cast<char*>(out) + first * (out_bf16 ? 16 : 32);
+        if (out_bf16)
+            hipLaunchKernelGGL((dequantize_mx8_kernel<true>), grid, block, 0, stream, q + 8 * first, scale + first / 4,
+                               n8, o);
+        else
+            hipLaunchKernelGGL((dequantize_mx8_kernel<false>), grid, block, 0, stream, q + 8 * first,
+                               scale + first / 4, n8, o);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_gated_grad(const void* dh, const void* gu, const uint8_t* gu_q, const uint8_t* gu_s,
