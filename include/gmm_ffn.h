@@ -34,6 +34,20 @@ typedef enum {
 } gmm_ffn_op;
 
 /*
+ * gmm_get_tile_config of these operations (they take no override) tells which
+ * kernel a call of this shape runs; lhs_dtype is not read, M at least 1.
+ *   kernel  1 few rows: tile_m = 16, 32 or 64 rows, tile_n = 32 or 64 columns
+ *             of P, K split over the waves (a call that keeps P as a checkpoint
+ *             takes 64 columns);
+ *           2 tiles of 128 rows and tile_n = 128 or 256 columns;
+ *           3 tiles of at most tile_m rows (up to 160) and 256 columns, fed by
+ *             load waves;
+ *           4 dX and dw in one launch (GMM_OP_BF16_SWIGLU_BWD), 128 x 128 tiles.
+ *   GMM_OP_BF16_SWIGLU_BWD: dX's, in a call for both gradients.  Its weight
+ *   gradient, unless in that launch, runs as GMM_OP_TGMM_MX8 of 2N columns.
+ */
+
+/*
  * gmm_quantize_mx8 -- x [M,K] (GMM_BF16 or GMM_F32) into an 8-bit checkpoint:
  *   codes q [M,K], scales [M,K/32].  K a multiple of 32.
  */

@@ -62,6 +62,26 @@ gmm_tile_config to_public(const gmm::TileConfig& c) {
     return o;
 }
 
+// gmm_get_tile_config of the calls of gmm_ffn.h.
+int ffn_tile_config(int op, int64_t M, int64_t K, int64_t N, int64_t G, int out_dtype, gmm_tile_config* cfg) {
+    if (cfg == nullptr) return fail(GMM_ERR_NULL, "cfg is NULL");
+    GMM_TRY(check_out_dtype(out_dtype, "out"));
+    GMM_TRY(check_groups(M, G));
+    GMM_TRY(check_mult(K, 64, "K"));
+    GMM_TRY(check_mult(N, 64, "N"));
+    if (M < 1 || N > kMaxDim / 2) return fail(GMM_ERR_SHAPE, "M=%lld, N=%lld out of range", (long long)M, (long long)N);
+    const int m = (int)M, k = (int)K, n = (int)N, g = (int)G;
+    const gmm::FfnChoice c = op == GMM_OP_BF16_SWIGLU       ? gmm::gated_fwd_choice(m, k, 2 * n, g, false)
+                             : op == GMM_OP_BF16_SWIGLU_BWD ? gmm::ffn_bwd_choice(m, k, 2 * n, g)
+                                                            : gmm::ffn_dw_choice(k, n, g);
+    *cfg = gmm_tile_config{};
+    cfg->kernel = c.kernel;
+    cfg->waves = c.waves;
+    cfg->tile_m = c.rows;
+    cfg->tile_n = c.cols;
+    return GMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,6 +146,7 @@ int gmm_set_tile_config(int op, const gmm_tile_config* cfg) {
 
 int gmm_get_tile_config(int op, int64_t M, int64_t K, int64_t N, int64_t G, int lhs_dtype,
                         int out_dtype, gmm_tile_config* cfg) {
+    if (op >= GMM_OP_BF16_SWIGLU && op <= GMM_OP_TGMM_MX8) return ffn_tile_config(op, M, K, N, G, out_dtype, cfg);
     if (op < GMM_OP_FP8_FWD || op > GMM_OP_FP8_INT4_FWD)
         return fail(GMM_ERR_SHAPE, "op %d has no tile configuration", op);
     if (cfg == nullptr) return fail(GMM_ERR_NULL, "cfg is NULL");

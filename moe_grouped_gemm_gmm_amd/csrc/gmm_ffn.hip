@@ -1785,49 +1785,64 @@ int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean, bool 
 constexpr int kFewMaxRows = 64;   // mean rows an expert: up to 4 blocks of 16
 
 template <bool OUT_BF16, int SAVE, int MB>
-hipError_t launch_few_mb(const FfnArgs& a, int busy, hipStream_t stream) {
+hipError_t launch_few_mb(const FfnArgs& a, const FfnChoice& c, hipStream_t stream) {
     if constexpr (SAVE != kSaveMx8)
-        if ((int64_t)busy * (a.NN / 32) <= device_cus())
-            return launch_few<OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
+        if (c.cols == 32) return launch_few<OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
     return launch_few<OUT_BF16, SAVE, MB, 32, 4, 3>(a, stream);
 }
 
 template <int SAVE, bool OUT_BF16>
 hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
-    const int busy = a.G < a.M ? a.G : a.M, rows = (a.M + busy - 1) / busy;
-    if (rows <= kFewMaxRows && (int64_t)busy * (a.NN / 128) < device_cus()) {
-        if (rows <= 16) return launch_few_mb<OUT_BF16, SAVE, 1>(a, busy, stream);
-        if (rows <= 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, busy, stream);
-        return launch_few_mb<OUT_BF16, SAVE, 4>(a, busy, stream);
+    const FfnChoice c = gated_fwd_choice(a.M, a.K, a.NN, a.G, SAVE == kSaveMx8);
+    if (c.kernel == kFfnFewRows) {
+        if (c.rows == 16) return launch_few_mb<OUT_BF16, SAVE, 1>(a, c, stream);
+        if (c.rows == 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, c, stream);
+        return launch_few_mb<OUT_BF16, SAVE, 4>(a, c, stream);
     }
-    const int cap = ws_cap(a.M, a.G, a.K, (a.NN + 255) / 256, 768, 96.0, false);
-    if (cap > 0) return launch_ws<kGated, OUT_BF16, SAVE>(a, cap, stream);
-    return wide_tiles(max_work_items(a.M, busy, 128), a.NN) ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream)
-                                                            : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
+    if (c.kernel == kFfnLoadWaves) return launch_ws<kGated, OUT_BF16, SAVE>(a, c.rows, stream);
+    return c.cols == 256 ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream) : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
 }
-
-// Whether a product of the backward pass takes 256-column tiles.
-bool wide_bwd(const FfnArgs& a, bool dx) {
-    const int64_t rows = dx ? max_work_items(a.M, a.G < a.M ? a.G : a.M, 128) : (int64_t)a.G * ((a.K + 127) / 128);
-    return wide_tiles(rows, dx ? a.K : a.NN);
-}
-
-int dx_cap(const FfnArgs& a) { return ws_cap(a.M, a.G, a.NN, (a.K + 255) / 256, 512, 48.0, true); }
 
 template <int MODE>
-hipError_t launch_bwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    if constexpr (MODE == kBwdX) {
-        const int cap = dx_cap(a);
-        if (cap > 0)
-            return out_bf16 ? launch_ws<MODE, true, kSaveNone>(a, cap, stream)
-                            : launch_ws<MODE, false, kSaveNone>(a, cap, stream);
-    }
-    if (wide_bwd(a, MODE == kBwdX))
+hipError_t launch_bwd(const FfnArgs& a, const FfnChoice& c, bool out_bf16, hipStream_t stream) {
+    if constexpr (MODE == kBwdX)
+        if (c.kernel == kFfnLoadWaves)
+            return out_bf16 ? launch_ws<MODE, true, kSaveNone>(a, c.rows, stream)
+                            : launch_ws<MODE, false, kSaveNone>(a, c.rows, stream);
+    if (c.cols == 256)
         return out_bf16 ? launch<MODE, true, kSaveNone, 8>(a, stream) : launch<MODE, false, kSaveNone, 8>(a, stream);
     return out_bf16 ? launch<MODE, true, kSaveNone, 4>(a, stream) : launch<MODE, false, kSaveNone, 4>(a, stream);
 }
 
 }  // namespace
+
+FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8) {
+    const int busy = G < M ? G : M, rows = (M + busy - 1) / busy;
+    if (rows <= kFewMaxRows && (int64_t)busy * (NN / 128) < device_cus()) {
+        // a checkpoint's block is 32 columns of one row: the wider tile's
+        const bool narrow = !keep_mx8 && (int64_t)busy * (NN / 32) <= device_cus();
+        return {kFfnFewRows, narrow ? 8 : 4, rows <= 16 ? 16 : (rows <= 32 ? 32 : 64), narrow ? 32 : 64};
+    }
+    const int cap = ws_cap(M, G, K, (NN + 255) / 256, 768, 96.0, false);
+    if (cap > 0) return {kFfnLoadWaves, 12, cap, 256};
+    return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
+}
+
+FfnChoice ffn_dx_choice(int M, int K, int NN, int G) {
+    const int cap = ws_cap(M, G, NN, (K + 255) / 256, 512, 48.0, true);
+    if (cap > 0) return {kFfnLoadWaves, 12, cap, 256};
+    return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, G < M ? G : M, 128), K) ? 256 : 128};
+}
+
+FfnChoice ffn_dw_choice(int K, int NN, int G) {
+    return {kFfnTiles, 4, 128, wide_tiles((int64_t)G * ((K + 127) / 128), NN) ? 256 : 128};
+}
+
+FfnChoice ffn_bwd_choice(int M, int K, int NN, int G) {
+    FfnChoice c = ffn_dx_choice(M, K, NN, G);
+    if (c.kernel == kFfnTiles && c.cols == 128 && ffn_dw_choice(K, NN, G).cols == 128) c.kernel = kFfnBoth;
+    return c;
+}
 
 int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G) {
     // of the 128-row tiles; the few-row form only takes grids near the chip's size
@@ -1847,15 +1862,16 @@ hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream)
 }
 
 hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    return launch_bwd<kBwdX>(a, out_bf16, stream);
+    return launch_bwd<kBwdX>(a, ffn_dx_choice(a.M, a.K, a.NN, a.G), out_bf16, stream);
 }
 
 hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
-    return a.aq != nullptr ? launch_bwd<kBwdWQ>(a, out_bf16, stream) : launch_bwd<kBwdW>(a, out_bf16, stream);
+    const FfnChoice c = ffn_dw_choice(a.K, a.NN, a.G);
+    return a.aq != nullptr ? launch_bwd<kBwdWQ>(a, c, out_bf16, stream) : launch_bwd<kBwdW>(a, c, out_bf16, stream);
 }
 
 hipError_t launch_ffn_bwd(const FfnArgs& x, bool x_bf16, const FfnArgs& w, bool w_bf16, hipStream_t stream) {
-    if (dx_cap(x) > 0 || wide_bwd(x, true) || wide_bwd(w, false)) {
+    if (ffn_bwd_choice(x.M, x.K, x.NN, x.G).kernel != kFfnBoth) {
         const hipError_t e = launch_ffn_dx(x, x_bf16, stream);
         return e != hipSuccess ? e : launch_ffn_dw(w, w_bf16, stream);
     }

@@ -138,6 +138,17 @@ hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream);
 // Both, in one launch where that pays.
 hipError_t launch_ffn_bwd(const FfnArgs& x, bool x_bf16, const FfnArgs& w, bool w_bf16, hipStream_t stream);
 
+// The kernel and tiles that a call takes (decided by its sizes alone; M >= 1).
+enum FfnKernel { kFfnFewRows = 1, kFfnTiles = 2, kFfnLoadWaves = 3, kFfnBoth = 4 };
+struct FfnChoice {
+    int kernel, waves, rows, cols;   // FfnKernel; waves of a workgroup; rows and columns of a tile
+};
+FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8);
+FfnChoice ffn_dx_choice(int M, int K, int NN, int G);
+FfnChoice ffn_dw_choice(int K, int NN, int G);
+// dX's choice in a backward call for dX and dW: kFfnBoth when one launch computes both.
+FfnChoice ffn_bwd_choice(int M, int K, int NN, int G);
+
 // Upper bounds of these launches' grids.
 int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G);
 int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G);
