@@ -1,7 +1,14 @@
 """GPU: the gated block's kernels for large grids (tiles fed by load waves) in
 every item height and round count that their rule can choose, each problem with
 the kernel it is meant for asked from gmm_get_tile_config first, against the
-64-bit computations and tolerances of test_gpu_ffn.py."""
+64-bit computations and tolerances of test_gpu_ffn.py.
+
+dP, the operand of both products of the backward pass, is rounded to bf16.
+Against gradients of a dP rounded in the 64-bit computation too, what remains
+is the fp32 evaluation: it moves a value by at most 2^-18 of its terms, so at
+most 2 x 2^-18 / 2^-8 = 2^-9 of the values round to the other neighbour, by at
+most 2^-7; the norm of that is sqrt(2^-9) 2^-7, under 2^-11 of dP's, and twice
+that bounds the products."""
 import numpy as np
 import pytest
 import torch
@@ -184,3 +191,28 @@ def test_graph_replays():
         assert torch.isfinite(junk)
         for k, v in o.items():
             assert torch.equal(v, eager[k]), (rep, k)
+
+
+def bf16_64(v):
+    """v (float64) rounded to bf16, half to even: 8 significant bits (no overflow or subnormal in these tests)."""
+    m, e = np.frexp(v)
+    return np.ldexp(np.rint(m * 256) / 256, e)
+
+
+@pytest.mark.parametrize("shape", [T.SHAPES[6], FORMS["tall"][:4]], ids=["small", "load_waves"])
+def test_operand_rounding_is_the_only_one_before_the_result(shape):
+    """dx and dw of fp32 against the gradients of a dP rounded to bf16 in 64 bits."""
+    p = T.Problem(*shape, seed=5)
+    dh, w, x, gu = p.dev("dh", "w", "x", "gu")
+    dx, dw = gmm.gmm_bf16_swiglu_bwd(dh, w, p.gs, lhs=x, gu=gu, dx_dtype=F32, dw_dtype=F32)
+    d = T.grad64(p, T.f64(p.gu))
+    w64, x64 = T.f64(p.w), T.f64(p.x)[:p.used]
+    errs = []
+    for e in (bf16_64(d), d):
+        rdx, rdw = np.zeros((p.M, p.K)), np.zeros((p.G, p.K, 2 * p.N))
+        for g, r in p.groups():
+            rdx[r], rdw[g] = e[r] @ w64[g].T, x64[r].T @ e[r]
+        errs.append([np.linalg.norm(T.f64(a) - b) / np.linalg.norm(b) for a, b in ((dx, rdx), (dw, rdw))])
+    assert max(errs[0]) <= 2.0 ** -10, errs
+    # a rounding that is spread evenly over half a step: about sqrt(1/3) 2^-8 x 0.75, never above 2^-8
+    assert max(errs[1]) <= 2.0 ** -8, errs
