@@ -26,9 +26,12 @@
  *    the caller, needing no initialisation.  The call writes int32 word 0 of
  *    ws with its device status: 0, or an OR of GMM_DEV_SUM_GT_M and
  *    GMM_DEV_NEGATIVE_SIZE (group_sizes broke the contract).  Read it with
- *    gmm_device_status after the call.  Calls that share a workspace and may
- *    run at the same time race on it (the kernels' results are unaffected;
- *    only the status word is).  A missing or too small workspace is
+ *    gmm_device_status after the call.  Where the workspace is the 256 bytes of
+ *    that status block, calls that share one and may run at the same time race
+ *    on the status word only (the results are unaffected).  A larger workspace
+ *    holds data of the call (gmm_bf16_swiglu_bwd of gmm_ffn.h keeps dP there):
+ *    such a call needs a workspace of its own until it has finished, or both
+ *    calls' results are wrong.  A missing or too small workspace is
  *    GMM_ERR_WORKSPACE.
  *  - `stream` is a hipStream_t (NULL = the default stream).  Every call only
  *    enqueues work on it and returns.
@@ -97,8 +100,9 @@ GMM_API const char *gmm_last_error(void);
 
 /*
  * gmm_workspace_bytes -- bytes of workspace the grouped call `op` (a gmm_op)
- *   needs for this shape (today 256 for every op: the status block); 0 for
- *   an unknown op.  Sizes are not checked here.
+ *   needs for this shape (256, the status block, for every op but
+ *   gmm_bf16_swiglu_bwd's, 256 + 4 M N); 0 for an unknown op.  Sizes are not
+ *   checked here.
  */
 GMM_API size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G);
 

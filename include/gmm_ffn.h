@@ -98,7 +98,10 @@ GMM_API int gmm_bf16_swiglu(const void *lhs, const void *rhs, const int32_t *gro
  * dw:  [G,K,2N], dw_dtype GMM_BF16 or GMM_F32, or NULL (not wanted).
  * h:   NULL, or [M,N] bf16 that receives the forward's output recomputed
  *      from the kept P (the next product's weight gradient needs it).
- * ws:  gmm_workspace_bytes(GMM_OP_BF16_SWIGLU_BWD, ...) holds dP.
+ * ws:  gmm_workspace_bytes(GMM_OP_BF16_SWIGLU_BWD, ...) = 256 + 4 M N bytes, the
+ *      status block and dP.  It is written and read by the call's kernels, so
+ *      a call needs a workspace of its own until it has finished: two calls on
+ *      different streams that share one overwrite each other's dP.
  */
 GMM_API int gmm_bf16_swiglu_bwd(const void *dh, const void *rhs, const int32_t *group_sizes,
                                 const void *lhs, const uint8_t *lhs_q, const uint8_t *lhs_scale,

@@ -106,7 +106,8 @@ def gmm_dequantize_mx8(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dt
     qp, sp = _arg(q, None, _BYTES, "q", dev), _arg(scale, (M, K // 32), _U8, "scale", dev)
     if out is None:
         out = torch.empty((M, K), dtype=out_dtype, device=dev)
-    _check(lib, lib.gmm_dequantize_mx8(qp, sp, M, K, _arg(out, (M, K), _FLOAT, "out", dev), _DT[out.dtype], _stream(dev)))
+    _check(lib, lib.gmm_dequantize_mx8(qp, sp, M, K, _arg(out, (M, K), _FLOAT, "out", dev), _DT[out.dtype],
+                                       _stream(dev)))
     return out
 
 
@@ -149,7 +150,9 @@ def gmm_bf16_swiglu_bwd(dh: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.
     layer's input (lhs in bf16, or its checkpoint lhs_q, lhs_scale) and the
     kept P (gu in bf16, or gu_q, gu_scale).  want_dx / want_dw False leaves
     that gradient out (None).  h [M,N] bf16, if given, receives the forward's
-    output recomputed from the kept P."""
+    output recomputed from the kept P.  ws, if given (workspace(OP_BF16_SWIGLU_BWD,
+    ...)), holds dP until the call's kernels have finished: a call that may run at
+    the same time on another stream needs another one."""
     lib = load_library()
     dev = dh.device
     M, N = dh.shape

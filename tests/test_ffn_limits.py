@@ -3,6 +3,8 @@ dimension.  A call whose launches would not fit is refused with the other
 shape errors, before anything is enqueued; the checkpoint calls split instead
 (tested on the GPU)."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -44,3 +46,22 @@ def test_products(lib):
     assert lib.gmm_bf16_swiglu(P(A), P(A), P(A), 1 << 26, 64, 1 << 11, 4, P(A), 1, None, None, None, P(A), 256,
                                None) == SHAPE                               # h: 2^24 tiles
     assert lib.tgmm_mx8(P(A), P(A), P(A), P(A), 64, 1 << 18, 1 << 14, 64, P(A), 1, P(A), 256, None) == SHAPE
+
+
+def test_headers_say_which_workspaces_hold_data(lib):
+    """Calls that run at the same time may share a workspace only where it is the status block alone: each
+    operation whose workspace is larger is named in gmm.h beside that permission, and in its own header."""
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    read = lambda f: re.sub(r"[\s*]+", " ", open(os.path.join(include, f)).read())
+    gmm_h, ffn_h = read("gmm.h"), read("gmm_ffn.h")
+    ops = dict(re.findall(r"GMM_OP_\w+ = (\d+),? / (\w+) /", gmm_h + ffn_h))
+    assert len(ops) == 11
+    rule = re.search(r"- Workspace:.*?- `stream`", gmm_h).group()
+    size = re.search(r"gmm_workspace_bytes -- .*?GMM_API", gmm_h).group()
+    data = [call for op, call in ops.items() if lib.gmm_workspace_bytes(int(op), 1000, 256, 128, 4) > 256]
+    assert data == ["gmm_bf16_swiglu_bwd"]
+    for call in data:
+        assert call in rule and call in size
+    assert "for every op" not in size
+    own = re.search(r"gmm_bf16_swiglu_bwd -- .*?GMM_API", ffn_h).group()
+    assert "workspace of its own" in own and "workspace of its own" in rule
