@@ -100,9 +100,8 @@ GMM_API const char *gmm_last_error(void);
 
 /*
  * gmm_workspace_bytes -- bytes of workspace the grouped call `op` (a gmm_op)
- *   needs for this shape (256, the status block, for every op but
- *   gmm_bf16_swiglu_bwd's, 256 + 4 M N); 0 for an unknown op.  Sizes are not
- *   checked here.
+ *   needs for this shape: 256, the status block, and for gmm_bf16_swiglu_bwd
+ *   4 M N more; 0 for an unknown op.  Sizes are not checked here.
  */
 GMM_API size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G);
 
