@@ -64,6 +64,24 @@ def test_forward(name, save, dt):
     T.test_forward(FORMS[name][:4], save, dt)
 
 
+# Few rows an expert on grids too large for 16 + 16 columns a tile: sizes, M, K, N, tile rows.
+FEW = {
+    "rows_16": ([3, 0, 16, 17, 1] * 6, 300, 320, 512, 16),
+    "rows_32": ([17, 32, 0, 33, 5] * 4, 450, 320, 512, 32),
+    "rows_64": ([64, 65, 0, 63, 5, 100] * 3, 1000, 192, 576, 64),
+}
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("save", ["none", "bf16", "mx8"])
+@pytest.mark.parametrize("name", list(FEW))
+def test_forward_few_rows(name, save, dt):
+    sizes, M, K, N, rows = FEW[name]
+    c = gmm.get_tile_config(gmm.OP_BF16_SWIGLU, M, K, N, len(sizes))
+    assert (c["kernel"], c["tile_m"], c["tile_n"]) == (1, rows, 64)
+    T.test_forward(FEW[name][:4], save, dt)
+
+
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("name", [n for n in FORMS if FORMS[n][5]])
 def test_dx(name, dt):
