@@ -63,16 +63,48 @@ __device__ __forceinline__ WorkItem even_item(int g, int glo, int ghi, int idx, 
     return it;
 }
 
-__device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ group_sizes, int G, int M, int cap,
-                                                   int ntiles, int b, int& col) {
-    col = 0;
-    const int lane = lane_id();
-    // Up to 256 groups the clamped ranges and item offsets stay in registers,
-    // every load issued before the first scan; beyond, a second pass.
-    const bool inreg = G <= 256;
-    int lo[4], hi[4], cn[4], W[4], raw[4];
+// The item of block b (g < 0: none) and its column tile for more than 256
+// groups, in two passes over group_sizes.
+__device__ inline WorkItem even_item_scan(const int32_t* __restrict__ group_sizes, int G, int M, int cap, int ntiles,
+                                          int b, int& col) {
     int carry = 0, items = 0;
-    if (inreg) {
+    for (int base = 0; base < G; base += 64) {
+        const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
+        carry = ch.next_carry;
+        items += lane_value(wave_incl_scan(group_items<true>(ch.lo, ch.hi, cap)), 63);
+    }
+    const int total = min(carry, M);
+    const int L = xcd_balance(b, (items + tail_items<true>(total, M, cap)) * ntiles);
+    if (L < 0) return WorkItem{-1, 0, 0, 0};
+    const int w = L / ntiles;
+    col = L % ntiles;
+    if (w >= items) return tail_item<true>(G, M, total, items, cap, w);
+    int first = 0;
+    carry = 0;
+    for (int base = 0; base < G; base += 64) {
+        const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
+        carry = ch.next_carry;
+        const int c = group_items<true>(ch.lo, ch.hi, cap), incl = wave_incl_scan(c), Wb = first + incl - c;
+        const unsigned long long m = __ballot(c > 0 && w >= Wb && w < Wb + c);
+        if (m) {
+            const int src = __ffsll((long long)m) - 1;
+            return even_item(base + src, lane_value(ch.lo, src), lane_value(ch.hi, src), w - lane_value(Wb, src), cap);
+        }
+        first += lane_value(incl, 63);
+    }
+    return WorkItem{-1, 0, 0, 0};   // not reached: w < items has an owner
+}
+
+// The items of a call, for one wave: up to 256 groups the clamped ranges and
+// item offsets stay in registers, every load issued before the first scan;
+// beyond, each item is found from group_sizes.
+struct EvenItems {
+    int lo[4], hi[4], cn[4], W[4], items, total;
+    __device__ __forceinline__ void init(const int32_t* __restrict__ group_sizes, int G, int M, int cap) {
+        if (G > 256) return;
+        const int lane = lane_id();
+        int raw[4], carry = 0;
+        items = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) raw[k] = group_size_at(group_sizes, G, 64 * k + lane);
 #pragma unroll
@@ -89,20 +121,18 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
                 items += lane_value(incl, 63);
             }
         }
-    } else {
-        for (int base = 0; base < G; base += 64) {
-            const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
-            carry = ch.next_carry;
-            items += lane_value(wave_incl_scan(group_items<true>(ch.lo, ch.hi, cap)), 63);
-        }
+        total = min(carry, M);
     }
-    const int total = min(carry, M);
-    const int L = xcd_balance(b, (items + tail_items<true>(total, M, cap)) * ntiles);
-    if (L < 0) return WorkItem{-1, 0, 0, 0};
-    const int w = L / ntiles;
-    col = L % ntiles;
-    if (w >= items) return tail_item<true>(G, M, total, items, cap, w);
-    if (inreg) {
+    // the item of block b (g < 0: none) and its column tile
+    __device__ __forceinline__ WorkItem find(const int32_t* __restrict__ group_sizes, int G, int M, int cap, int ntiles,
+                                             int b, int& col) const {
+        col = 0;
+        if (G > 256) return even_item_scan(group_sizes, G, M, cap, ntiles, b, col);
+        const int L = xcd_balance(b, (items + tail_items<true>(total, M, cap)) * ntiles);
+        if (L < 0) return WorkItem{-1, 0, 0, 0};
+        const int w = L / ntiles;
+        col = L % ntiles;
+        if (w >= items) return tail_item<true>(G, M, total, items, cap, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const unsigned long long m = __ballot(cn[k] > 0 && w >= W[k] && w < W[k] + cn[k]);
@@ -112,29 +142,14 @@ __device__ __forceinline__ WorkItem even_work_item(const int32_t* __restrict__ g
                                  w - lane_value(W[k], src), cap);
             }
         }
-    } else {
-        int first = 0;
-        carry = 0;
-        for (int base = 0; base < G; base += 64) {
-            const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
-            carry = ch.next_carry;
-            const int c = group_items<true>(ch.lo, ch.hi, cap), incl = wave_incl_scan(c), Wb = first + incl - c;
-            const unsigned long long m = __ballot(c > 0 && w >= Wb && w < Wb + c);
-            if (m) {
-                const int src = __ffsll((long long)m) - 1;
-                return even_item(base + src, lane_value(ch.lo, src), lane_value(ch.hi, src), w - lane_value(Wb, src),
-                                 cap);
-            }
-            first += lane_value(incl, 63);
-        }
+        return WorkItem{-1, 0, 0, 0};   // not reached: w < items has an owner
     }
-    return WorkItem{-1, 0, 0, 0};   // not reached: w < items has an owner
-}
+};
 
 // Work item of a workgroup; every mode's block 0 also writes the call's
-// device status word.  TR x TC: tile rows and columns of the product; CAP: rows
-// an item may have (0: a.cap of them).
-template <int MODE, int TR, int TC, int CAP = TR>
+// device status word.  TR x TC: tile rows (the most an item has) and columns of
+// the product.
+template <int MODE, int TR, int TC>
 __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int block, int* s_info, FfnItem& it) {
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     if (wave == 1 && block == 0) {
@@ -144,7 +159,7 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int block, int* s_inf
     if constexpr (MODE == kBwdW || MODE == kBwdWQ) {
         if (wave == 0) {
             const TgmmTile tt = tgmm_tile(a.group_sizes, a.G, a.M, a.ntiles_r * a.ntiles_c,
-                                          xcd_remap(block, a.nblocks), block, a.placement);
+                                          xcd_remap(block, a.nblocks), block, /*placement*/ 0);
             if (lane == 0) { s_info[0] = tt.row_lo; s_info[1] = tt.row_hi; s_info[2] = tt.g; s_info[3] = tt.t; }
         }
         __syncthreads();
@@ -160,7 +175,9 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int block, int* s_inf
     } else {
         if (wave == 0) {
             int col;
-            const WorkItem wi = even_work_item(a.group_sizes, a.G, a.M, CAP > 0 ? CAP : a.cap, a.ntiles_c, block, col);
+            EvenItems items;
+            items.init(a.group_sizes, a.G, a.M, TR);
+            const WorkItem wi = items.find(a.group_sizes, a.G, a.M, TR, a.ntiles_c, block, col);
             if (lane == 0) { s_info[0] = wi.g; s_info[1] = wi.lo; s_info[2] = wi.hi; s_info[3] = col; }
         }
         __syncthreads();
@@ -751,7 +768,7 @@ template <int MODE, bool OUT_BF16, int SAVE, int NJ>
 __global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnArgs a) {
     using T = FfnTile<NJ>;
     __shared__ __attribute__((aligned(1024))) uint16_t ring[T::kS * T::kStage];
-    __shared__ int s_info[5];
+    __shared__ int s_info[4];
     ffn_tile<MODE, OUT_BF16, SAVE, NJ>(a, blockIdx.x, ring, s_info);
 }
 
@@ -763,7 +780,7 @@ template <bool X_BF16, bool W_BF16, bool MX8>
 __global__ __launch_bounds__(256, FfnTile<4>::kRes) void ffn_bwd_kernel(const FfnArgs x, const FfnArgs w) {
     using T = FfnTile<4>;
     __shared__ __attribute__((aligned(1024))) uint16_t ring[T::kS * T::kStage];
-    __shared__ int s_info[5];
+    __shared__ int s_info[4];
     if ((int)blockIdx.x < x.nblocks)
         ffn_tile<kBwdX, X_BF16, kSaveNone, 4>(x, blockIdx.x, ring, s_info);
     else
@@ -1077,56 +1094,6 @@ constexpr int kWsRows = 160, kWsCols = 256, kWsStages = 3, kWsThreads = 768;
 constexpr int kWsSliceA = kWsRows * 64, kWsSliceB = kWsCols * 64, kWsStage = kWsSliceA + kWsSliceB;   // elements
 constexpr int kWsBytes = kWsStages * kWsStage * 2;
 static_assert(kWsBytes <= 163840 - 1024, "the ring fits the LDS");
-
-// Items of even_work_item for a workgroup that takes many: the groups' ranges
-// and item offsets stay in registers (up to 256 groups; beyond, each item is
-// found from group_sizes again).
-struct EvenItems {
-    int lo[4], hi[4], cn[4], W[4], items, total;
-    __device__ void init(const int32_t* __restrict__ group_sizes, int G, int M, int cap) {
-        if (G > 256) return;
-        const int lane = lane_id();
-        int raw[4], carry = 0;
-        items = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) raw[k] = group_size_at(group_sizes, G, 64 * k + lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            lo[k] = hi[k] = cn[k] = W[k] = 0;
-            if (64 * k < G) {
-                const GroupChunk ch = group_chunk_of(raw[k], M, carry);
-                lo[k] = ch.lo;
-                hi[k] = ch.hi;
-                carry = ch.next_carry;
-                cn[k] = group_items<true>(ch.lo, ch.hi, cap);
-                const int incl = wave_incl_scan(cn[k]);
-                W[k] = items + incl - cn[k];
-                items += lane_value(incl, 63);
-            }
-        }
-        total = min(carry, M);
-    }
-    __device__ WorkItem find(const int32_t* __restrict__ group_sizes, int G, int M, int cap, int ntiles, int b,
-                             int& col) const {
-        if (G > 256) return even_work_item(group_sizes, G, M, cap, ntiles, b, col);
-        col = 0;
-        const int L = xcd_balance(b, (items + tail_items<true>(total, M, cap)) * ntiles);
-        if (L < 0) return WorkItem{-1, 0, 0, 0};
-        const int w = L / ntiles;
-        col = L % ntiles;
-        if (w >= items) return tail_item<true>(G, M, total, items, cap, w);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const unsigned long long m = __ballot(cn[k] > 0 && w >= W[k] && w < W[k] + cn[k]);
-            if (m) {
-                const int src = __ffsll((long long)m) - 1;
-                return even_item(64 * k + src, lane_value(lo[k], src), lane_value(hi[k], src),
-                                 w - lane_value(W[k], src), cap);
-            }
-        }
-        return WorkItem{-1, 0, 0, 0};   // not reached: w < items has an owner
-    }
-};
 
 // Stages rows of E in one stage of the ring and stores them, RB 32-row blocks
 // (of the item's five) a round, two barriers a round: VAL(i, b, q, v) gives the
@@ -1568,7 +1535,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
     constexpr int kRow = 2 * CT + 4;                           // fp32 staging row
     constexpr int kRing = NW * S * kSt;
     __shared__ __attribute__((aligned(1024))) uint16_t ring[kRing];
-    __shared__ int s_info[5];
+    __shared__ int s_info[4];
     static_assert(NW * TR * kRow * 2 <= kRing, "the partial sums fit the rings");
     static_assert(kRing * 2 <= 163840 - 1024, "the rings fit the LDS");
 

@@ -129,7 +129,7 @@ struct FfnArgs {
     void* out;                            // h [M,NN/2], dx [M,K] or dw [G,K,NN]
     uint16_t* gu;                         // the forward's P, or NULL
     uint8_t *gu_q, *gu_s;                 // the forward's P as a checkpoint, or NULL
-    int ntiles_c, ntiles_r, nblocks, placement, cap;   // set by the launcher (placement: of tgmm_tile)
+    int ntiles_c, ntiles_r, nblocks, cap;   // set by the launcher (cap: rows of a load-wave item)
     int32_t* status;
 };
 hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream);
