@@ -774,8 +774,9 @@ __global__ __launch_bounds__(256, FfnTile<NJ>::kRes) void ffn_kernel(const FfnAr
 
 // Both products of the backward pass in one grid (dX's blocks first, padded to
 // a multiple of the XCDs): small problems wait for launches and for their
-// last tiles, not for either product (301 rows, 5 experts, K = 512, 2N = 384:
-// 15.6 us for the gradient and two launches, 11.5 with one).
+// last tiles, not for either product (301 rows, 5 experts, K = 512, 2N = 384, on
+// the device: 15.6 us for the activation's gradient and two launches, 10.6 with
+// one, 2.9 and 8.1 of it the two kernels).
 template <bool X_BF16, bool W_BF16, bool MX8>
 __global__ __launch_bounds__(256, FfnTile<4>::kRes) void ffn_bwd_kernel(const FfnArgs x, const FfnArgs w) {
     using T = FfnTile<4>;
@@ -803,7 +804,7 @@ bool set_grid(FfnArgs& a) {
         nblocks = max_work_items(a.M, a.G < a.M ? a.G : a.M, T::kTR) * a.ntiles_c;
     }
     a.nblocks = (int)nblocks;
-    return nblocks <= 0x7fffffff;
+    return nblocks < (int64_t)1 << 24;   // 2^32 threads
 }
 
 template <int MODE, bool OUT_BF16, int SAVE, int NJ>
@@ -829,10 +830,12 @@ hipError_t launch_both(FfnArgs x, FfnArgs w, hipStream_t stream) {
 // The forward and dX on tiles of up to 160 rows x 256 columns, one workgroup
 // per CU: 8 waves (2 x 4) multiply, each 80 x 64 in 32 x 32 x 16 MFMAs, and 4
 // waves do nothing but issue the loads into a ring of 3 stages, 64 deep (156
-// KB).  A CU holds about 22 KB of cache misses in flight (a bare stream of
-// load-to-LDS instructions reaches 38 GB/s per CU whatever the depth of its
-// ring), and a load-to-LDS instruction beyond that waits at issue, with the
-// wave that issues it: in a wave that also multiplies the two times add up.
+// KB).  A load-to-LDS instruction that the memory system cannot take yet waits
+// at issue, with the wave that issues it: in a wave that also multiplies the
+// two times add up (8192 rows, 32 experts, K = 2048, 2N = 1024: forward 80 us
+// on the smaller tiles, 57 on these).  By the counters the forward moves 32 GB/s
+// a CU into LDS, with the matrix units 30 % and the LDS 25 % busy; dX 34 GB/s,
+// 32 and 34 %.
 // Direct rows are loaded 128 bytes at a time, whole cache lines (in 64-byte
 // pieces, 32 deep, the rows of x cost the shard's forward 14 of its 56 us).
 //
@@ -845,7 +848,8 @@ hipError_t launch_both(FfnArgs x, FfnArgs w, hipStream_t stream) {
 // A workgroup takes items until none is left.  After an item's slices one slot
 // of the ring is skipped and serves to stage its results, while the load waves
 // fill the two slots after it from the next item: the start of one item hides
-// behind the end of the one before (production dX 449 -> 414 us).
+// behind the end of the one before (dX of 65536 rows, 256 experts with the
+// activation's gradient 462 -> 414 us).
 //
 // The wave rows take alternate 32-row blocks and a wave multiplies only its
 // blocks that hold rows (a loop compiled for each count), so an item's cost
@@ -1456,11 +1460,12 @@ hipError_t launch_ws(FfnArgs a, int cap, hipStream_t stream) {
 // up columns in 32-byte chunks, chunk k at k ^ key: the 8 rows that one pass
 // of a transposed read covers (0-3 and 8-11 of 16) fall on each bank once.
 //
-// What bounds it: a pass over one token's 8 experts (33 MB) takes 17.7 us, of
-// which 3.4 us are launch and prologue; a bare read of as many cold bytes
-// takes 10.4 us.  Deeper rings and more waves change nothing; weights that lie
-// contiguously for each workgroup would (14 us), but the layout is the
-// caller's.
+// What bounds it: a pass over one token's 8 experts (33 MB) takes 18 us with cold
+// weights, of which 3.4 us are launch and prologue; a bare read of as many cold
+// bytes takes 10.4 us.  With 16 + 16 columns a row of weights is two pieces of 32
+// bytes, so the L2s get four requests for each cache line (1.06 million in all).
+// Deeper rings and more waves change nothing; weights that lie contiguously for
+// each workgroup would (14 us), but the layout is the caller's.
 template <int CT>
 __device__ __forceinline__ int few_key(int r) {
     return CT == 32 ? ((r >> 1) & 1) | ((r >> 2) & 2) : (r >> 3) & 1;
@@ -1716,8 +1721,10 @@ bool wide_tiles(int64_t row_tiles, int64_t cols) {
 //   145
 //   short or few: forward 3000, 8, 512, 2048 17.1 / 18.1; 2048, 32, 2048, 1024
 //   34.8 / 41.7
+//   odd sizes: 1777, 13, 1088, 1408 forward 22.7 / 21.1 (a third of the experts
+//   empty: 21.1 / 21.1), dX 25.8 / 23.8; 2000, 11, 1536, 1280 forward 26.5 / 24.6
 // Under skewed (Zipf) routing, which the host does not see, the forward of 8192
-// rows loses, 73.5 / 80.8.
+// rows loses, 79.0 / 88.8; its dX does not, 75.0 / 72.8.
 int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean, bool many) {
     const int64_t busy = G < M ? G : M, cus = device_cus();
     const double mean = (double)M / (double)busy, high = mean + 2.0 * sqrt(mean);
