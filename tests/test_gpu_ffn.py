@@ -625,10 +625,11 @@ def test_weight_gradient_wide(shape, dwt):
     test_weight_gradient(shape, dwt)
 
 
-# Grids of one or two rounds of the chip with long reductions: the tiles of up to 160 rows with load waves.
+# Long reductions: the first forward and the first and last dX take the tiles with load waves, the others those of 128
+# rows (every form of the load waves: test_gpu_ffn_forms.py).
 LOADWAVES = [
     ([130, 100, 129, 0, 160, 161, 90, 31] * 3, 2500, 1088, 1088),      # forward: 24 groups, partial column tiles
-    ([150, 65, 0, 33, 100], 360, 8256, 512),                           # dX: many column tiles, a partial one
+    ([150, 65, 0, 33, 100], 360, 8256, 512),                           # many column tiles of dX, a partial one
     ([100] * 25, 2500, 1280, 1344),
 ]
 LW_IDS = ["M%d_K%d_N%d_G%d" % (M, K, N, len(s)) for s, M, K, N in LOADWAVES]
@@ -703,7 +704,7 @@ def test_load_waves_many_groups():
     backward_check(p, f64(p.x)[:p.used], grad64(p, P), dx, None, None, P, F32, BF)
 
 
-# Many weight-gradient tiles: the persistent form, several tiles a workgroup.
+# Many weight-gradient tiles, one a workgroup.
 WGRAD = [
     # every part of a 64-row slice, empty groups, a half row tile and a partial column tile
     ([0, 1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 128, 129, 193, 0, 300] * 2, 2740, 576, 448),
