@@ -85,6 +85,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in EXPORTS[3:]:
         getattr(lib, name).restype = I
     ffn._declare(lib)
+    moe._declare(lib)
     _lib = lib
     return lib
 
@@ -435,6 +436,8 @@ def gmm_bf16_dx(dy: torch.Tensor, w: torch.Tensor, group_sizes: torch.Tensor,
     return out
 
 
-from . import ffn  # noqa: E402  (uses the helpers above)
+from . import ffn, moe  # noqa: E402  (they use the helpers above)
 from .ffn import (FFN_EXPORTS, OP_BF16_SWIGLU, OP_BF16_SWIGLU_BWD, OP_TGMM_MX8,  # noqa: E402,F401
                   gmm_bf16_swiglu, gmm_bf16_swiglu_bwd, gmm_dequantize_mx8, gmm_quantize_mx8, tgmm_mx8)
+from .moe import (MAX_TOPK, MOE_EXPORTS, OP_SORT_TOKENS, gmm_combine, gmm_combine_bwd, gmm_dispatch,  # noqa: E402,F401
+                  gmm_route, gmm_route_bwd, gmm_sort_tokens)

@@ -10,9 +10,11 @@
 #include <initializer_list>
 
 #include "../../include/gmm_ffn.h"
+#include "../../include/gmm_moe.h"
 #include "gmm_check.hpp"
 #include "gmm_config.hpp"
 #include "gmm_launch.hpp"
+#include "gmm_moe.hpp"
 
 namespace gmm {
 namespace abi {
@@ -102,7 +104,7 @@ const char* gmm_status_string(int status) {
 const char* gmm_last_error(void) { return g_last_error; }
 
 size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G) {
-    (void)K; (void)G;
+    (void)K;
     switch (op) {
         case GMM_OP_METADATA:
         case GMM_OP_FP8_FWD:
@@ -118,6 +120,8 @@ size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G) {
             return kWsStatusBytes;
         case GMM_OP_BF16_SWIGLU_BWD:   // and dP, bf16 [M,2N]
             return kWsStatusBytes + (M > 0 && N > 0 ? (size_t)M * 4 * (size_t)N : 0);
+        case GMM_OP_SORT_TOKENS:       // and the runs' counts of every expert
+            return kWsStatusBytes + 4 * (size_t)gmm::sort_count_words(M, G);
         default:
             return 0;
     }

@@ -1,0 +1,445 @@
+// Tokens sorted by expert and back: the order of the slots, and the rows moved
+// into it and out of it with their weights and gradients.
+//
+// The order is a counting sort that keeps equal experts in slot order.  A
+// workgroup counts the experts of its run of slots in LDS; a slot's row is
+//     slots of lower experts + slots of its expert in earlier runs
+//     + in earlier waves of the run + in earlier slots of the wave,
+// the last from ballots on the expert's bits, so nothing depends on the order
+// in which workgroups or atomics run (the LDS atomics only count).
+//
+// Moving rows is bound by memory: a workgroup takes one token, reads its row
+// once and touches the token's k rows, whole rows at a time, so that every
+// byte of the sorted buffer crosses the chip once and the token's row is read
+// once instead of k times.
+#include "gmm_launch.hpp"
+#include "gmm_moe.hpp"
+#include "gmm_mx8.hpp"
+
+#include <type_traits>
+
+namespace gmm {
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------- the order --
+
+constexpr int kRun = 2048;        // slots of a run, the least
+constexpr int kMaxRuns = 1024;
+constexpr int kSumRuns = 32;      // up to here every workgroup adds up the runs before its own
+constexpr int kOneRun = 4096;     // up to here (and 1024 experts) one workgroup does everything
+
+struct Runs {
+    int count, slots;   // slots: of one run, a multiple of 256
+};
+Runs runs_of(int64_t n) {
+    const int64_t c = (n + kRun - 1) / kRun, r = c < 1 ? 1 : (c < kMaxRuns ? c : kMaxRuns);
+    const int64_t s = ((n + r - 1) / r + 255) / 256 * 256;
+    return Runs{(int)(n > 0 ? (n + s - 1) / s : 1), (int)(s > 0 ? s : 256)};
+}
+
+// The local expert of a slot, G where it has none here.
+__device__ __forceinline__ int expert_of(const int32_t* __restrict__ ids, int slot, int end, int first, int G) {
+    if (slot >= end) return G;
+    const unsigned e = (unsigned)ids[slot] - (unsigned)first;
+    return ids[slot] >= 0 && e < (unsigned)G ? (int)e : G;
+}
+
+// counts[run, g]: slots of expert g in the run.
+template <int GMAX>
+__global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ ids, int n, int first, int G, int run,
+                                                    int32_t* __restrict__ counts) {
+    __shared__ int hist[GMAX];
+    for (int g = threadIdx.x; g < G; g += 256) hist[g] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)blockIdx.x * run;
+    const int hi = (int)(lo + run < n ? lo + run : n);
+    for (int64_t s = lo + threadIdx.x; s < hi; s += 256) {
+        const int e = expert_of(ids, (int)s, hi, first, G);
+        if (e < G) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < G; g += 256) counts[(int64_t)blockIdx.x * G + g] = hist[g];
+}
+
+// counts[run, g] -> slots of expert g in earlier runs, and totals[g] behind
+// them: 64 experts a workgroup, each of 16 waves a sixteenth of the runs.
+__global__ __launch_bounds__(1024) void scan_kernel(int32_t* __restrict__ counts, int runs, int G) {
+    __shared__ int part[16][64];
+    const int lane = lane_id(), wave = threadIdx.x >> 6, g = blockIdx.x * 64 + lane;
+    const int per = (runs + 15) / 16, lo = min(runs, wave * per), hi = min(runs, lo + per);
+    int sum = 0;
+    if (g < G)
+        for (int r = lo; r < hi; ++r) sum += counts[(int64_t)r * G + g];
+    part[wave][lane] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += part[w][lane];
+    if (g >= G) return;
+    for (int r = lo; r < hi; ++r) {
+        const int c = counts[(int64_t)r * G + g];
+        counts[(int64_t)r * G + g] = before;
+        before += c;
+    }
+    if (wave == 15) counts[(int64_t)runs * G + g] = before;
+}
+
+enum Before { kAlone = 0, kSum = 1, kScanned = 2 };   // one run; runs added up here; runs added up by scan_kernel
+
+// Rows of a run's slots.  NW waves, each a contiguous NW-th of the run.
+template <int NW, int GMAX, int BEFORE>
+__global__ __launch_bounds__(64 * NW) void place_kernel(const int32_t* __restrict__ ids, int n, int first, int G,
+                                                        int M, int run, int runs, const int32_t* __restrict__ counts,
+                                                        int32_t* __restrict__ group_sizes, int32_t* __restrict__ row_of,
+                                                        int32_t* __restrict__ slot_of, int32_t* __restrict__ status) {
+    constexpr int NT = 64 * NW, EPT = (GMAX + NT - 1) / NT;
+    __shared__ int next[NW][GMAX];   // counts of each wave, then the row of its next slot of each expert
+    __shared__ int wave_sum[NW];
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    for (int e = tid; e < NW * GMAX; e += NT) next[e / GMAX][e % GMAX] = 0;
+    __syncthreads();
+    const int64_t run_lo = (int64_t)blockIdx.x * run;
+    const int run_hi = (int)(run_lo + run < n ? run_lo + run : n);
+    const int part = (run + NT - 1) / NT * 64;
+    const int64_t lo = run_lo + (int64_t)wave * part;
+    const int hi = (int)(lo + part < run_hi ? lo + part : run_hi);
+    for (int64_t s = lo + lane; s < hi; s += 64) {
+        const int e = expert_of(ids, (int)s, hi, first, G);
+        if (e < G) atomicAdd(&next[wave][e], 1);
+    }
+    __syncthreads();
+    // thread t: experts t EPT .. + EPT - 1, so that a scan over threads is one over experts
+    int before[EPT], total[EPT], sum = 0;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        const int g = tid * EPT + i;
+        before[i] = total[i] = 0;
+        if (g < G) {
+            if constexpr (BEFORE == kAlone) {
+                for (int w = 0; w < NW; ++w) total[i] += next[w][g];
+            } else if constexpr (BEFORE == kSum) {
+                for (int r = 0; r < runs; ++r) {
+                    const int c = counts[(int64_t)r * G + g];
+                    total[i] += c;
+                    before[i] += r < (int)blockIdx.x ? c : 0;
+                }
+            } else {
+                before[i] = counts[(int64_t)blockIdx.x * G + g];
+                total[i] = counts[(int64_t)runs * G + g];
+            }
+        }
+        sum += total[i];
+    }
+    const int incl = wave_incl_scan(sum);
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    int base = incl - sum, all = 0;
+    for (int w = 0; w < NW; ++w) {
+        base += w < wave ? wave_sum[w] : 0;
+        all += wave_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        const int g = tid * EPT + i;
+        if (g >= G) break;
+        if (blockIdx.x == 0) group_sizes[g] = min(base + total[i], M) - min(base, M);
+        int row = base + before[i];
+        for (int w = 0; w < NW; ++w) {
+            const int c = next[w][g];
+            next[w][g] = row;
+            row += c;
+        }
+        base += total[i];
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) status[0] = all > M ? kDevSumGtM : 0;
+    for (int64_t r = (int64_t)all + (int64_t)blockIdx.x * NT + tid; r < M; r += (int64_t)gridDim.x * NT) slot_of[r] = -1;
+    const int bits = 32 - __clz(G);   // of G itself: the slots without an expert match each other too
+    for (int64_t s0 = lo; s0 < hi; s0 += 64) {
+        const int s = (int)s0 + lane;
+        const int e = expert_of(ids, s, hi, first, G);
+        unsigned long long same = ~0ull;   // lanes of the same expert
+        for (int b = 0; b < bits; ++b) {
+            const unsigned long long m = __ballot((e >> b) & 1);
+            same &= (e >> b) & 1 ? m : ~m;
+        }
+        const unsigned long long below = same & ((1ull << lane) - 1ull);
+        int row = -1;
+        if (e < G) row = next[wave][e] + __popcll(below);
+        __builtin_amdgcn_wave_barrier();
+        if (e < G && below == 0) next[wave][e] = row + __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        if (s < hi) {
+            const bool fits = row >= 0 && row < M;
+            row_of[s] = fits ? row : -1;
+            if (fits) slot_of[row] = s;
+        }
+    }
+}
+
+// ------------------------------------------------------------ moved rows --
+
+// 16 bytes of a row as fp32 values, and back.
+template <bool BF16>
+struct Vec {
+    static constexpr int N = BF16 ? 8 : 4;
+    __device__ static void get(const u32x4& d, float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16) {
+                v[2 * i] = bf16_lo(d[i]);
+                v[2 * i + 1] = bf16_hi(d[i]);
+            } else {
+                v[i] = __uint_as_float(d[i]);
+            }
+        }
+    }
+};
+// N consecutive values read or written as bf16 or fp32.
+template <bool BF16, int N>
+__device__ __forceinline__ void get_n(const void* p, int64_t e, float (&v)[N]) {
+    constexpr int V = Vec<BF16>::N;
+    if constexpr (N >= V) {
+#pragma unroll
+        for (int i = 0; i < N; i += V) {
+            float u[V];
+            Vec<BF16>::get(*reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + (e + i) * (BF16 ? 2 : 4)), u);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[i + q] = u[q];
+        }
+    } else {   // four bf16 values
+        const uint2 d = *reinterpret_cast<const uint2*>(static_cast<const char*>(p) + e * 2);
+        v[0] = bf16_lo(d.x);
+        v[1] = bf16_hi(d.x);
+        v[2] = bf16_lo(d.y);
+        v[3] = bf16_hi(d.y);
+    }
+}
+template <bool BF16, int N>
+__device__ __forceinline__ void put_n(void* p, int64_t e, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        if constexpr (!BF16)
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + e + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        else if constexpr (N == 4)
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + e) = make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]));
+        else if (i % 8 == 0)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + e + i) =
+                make_uint4(pack_rne(v[i], v[i + 1]), pack_rne(v[i + 2], v[i + 3]), pack_rne(v[i + 4], v[i + 5]),
+                           pack_rne(v[i + 6], v[i + 7]));
+    }
+}
+
+// The rows of a token's choices: lane j < k holds choice j's row and weight;
+// `mask` has the choices that have a row.
+struct Choices {
+    int row;
+    float w;
+    unsigned long long mask;
+};
+__device__ __forceinline__ Choices choices_of(const MoveArgs& a, int64_t t) {
+    Choices c;
+    const int lane = lane_id();
+    c.row = lane < a.k ? a.row_of[t * a.k + lane] : -1;
+    c.w = lane < a.k && a.weights != nullptr ? a.weights[t * a.k + lane] : 1.0f;
+    c.mask = __ballot(c.row >= 0 && c.row < a.M);
+    return c;
+}
+
+constexpr int kTailRows = 16;   // rows a unit behind the tokens' looks at
+
+// Zeros in the rows r0 .. r0 + 15 of out that no slot owns (row_bytes a
+// multiple of 16), by 256 threads.
+__device__ __forceinline__ void zero_unowned(const MoveArgs& a, int64_t r0, void* out, int64_t row_bytes) {
+    const int lane = lane_id();
+    const int64_t r = r0 + lane, slots = a.T * a.k;
+    bool none = false;
+    if (lane < kTailRows && r < a.M) {
+        const int s = a.slot_of[r];
+        none = s < 0 || s >= slots;
+    }
+    for (unsigned long long m = __ballot(none); m != 0; m &= m - 1) {
+        char* p = static_cast<char*>(out) + (r0 + __ffsll((long long)m) - 1) * row_bytes;
+        for (int64_t b = 16 * (int64_t)threadIdx.x; b < row_bytes; b += 16 * 256)
+            *reinterpret_cast<u32x4*>(p + b) = u32x4{0u, 0u, 0u, 0u};
+    }
+}
+
+// A unit is a token, or 16 rows of the sorted buffer to look for unowned ones.
+__device__ __forceinline__ int64_t move_units(const MoveArgs& a) { return a.T + (a.M + kTailRows - 1) / kTailRows; }
+
+__global__ __launch_bounds__(256) void dispatch_kernel(const MoveArgs a, const char* __restrict__ x, int64_t row_bytes,
+                                                       char* __restrict__ out) {
+    for (int64_t u = blockIdx.x; u < move_units(a); u += gridDim.x) {
+        if (u >= a.T) {
+            zero_unowned(a, (u - a.T) * kTailRows, out, row_bytes);
+            continue;
+        }
+        const Choices c = choices_of(a, u);
+        if (c.mask == 0) continue;
+        for (int64_t b = 16 * (int64_t)threadIdx.x; b < row_bytes; b += 16 * 256) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(x + u * row_bytes + b);
+            for (unsigned long long m = c.mask; m != 0; m &= m - 1)
+                *reinterpret_cast<u32x4*>(out + (int64_t)lane_value(c.row, __ffsll((long long)m) - 1) * row_bytes + b) = v;
+        }
+    }
+}
+
+template <bool Y_BF16, bool OUT_BF16>
+__global__ __launch_bounds__(256) void combine_kernel(const MoveArgs a, const void* __restrict__ y, const void* residual,
+                                                      void* out) {
+    constexpr int N = Vec<Y_BF16>::N;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const Choices c = choices_of(a, t);
+        for (int64_t e = N * (int64_t)threadIdx.x; e < a.K; e += N * 256) {
+            float s[N];
+            if (residual != nullptr) {
+                get_n<OUT_BF16, N>(residual, t * a.K + e, s);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[i] = 0.0f;
+            }
+            for (unsigned long long m = c.mask; m != 0; m &= m - 1) {
+                const int j = __ffsll((long long)m) - 1;
+                const float w = __int_as_float(lane_value(__float_as_int(c.w), j));
+                float v[N];
+                get_n<Y_BF16, N>(y, (int64_t)lane_value(c.row, j) * a.K + e, v);
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[i] = __builtin_fmaf(w, v[i], s[i]);
+            }
+            put_n<OUT_BF16, N>(out, t * a.K + e, s);
+        }
+    }
+}
+
+__device__ __forceinline__ float wave_sum_f(float x) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
+    return x;
+}
+
+template <bool D_BF16, bool Y_BF16>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(const MoveArgs a, const void* __restrict__ dout,
+                                                          const void* __restrict__ y, void* __restrict__ dy,
+                                                          float* __restrict__ dweights) {
+    constexpr int N = Vec<Y_BF16>::N;
+    __shared__ float part[4];
+    const int64_t units = dy != nullptr ? move_units(a) : a.T;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        if (u >= a.T) {
+            zero_unowned(a, (u - a.T) * kTailRows, dy, a.K * (Y_BF16 ? 2 : 4));
+            continue;
+        }
+        const Choices c = choices_of(a, u);
+        for (int j = 0; j < a.k; ++j) {
+            float dot = 0.0f;
+            if (c.mask >> j & 1) {
+                const int64_t row = lane_value(c.row, j);
+                const float w = __int_as_float(lane_value(__float_as_int(c.w), j));
+                for (int64_t e = N * (int64_t)threadIdx.x; e < a.K; e += N * 256) {
+                    float d[N];
+                    get_n<D_BF16, N>(dout, u * a.K + e, d);
+                    if (dweights != nullptr) {
+                        float v[N];
+                        get_n<Y_BF16, N>(y, row * a.K + e, v);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) dot = __builtin_fmaf(d[i], v[i], dot);
+                    }
+                    if (dy != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) d[i] *= w;
+                        put_n<Y_BF16, N>(dy, row * a.K + e, d);
+                    }
+                }
+            }
+            if (dweights == nullptr) continue;
+            dot = wave_sum_f(dot);
+            __syncthreads();
+            if (lane_id() == 0) part[threadIdx.x >> 6] = dot;
+            __syncthreads();
+            if (threadIdx.x == 0) dweights[u * a.k + j] = ((part[0] + part[1]) + part[2]) + part[3];
+        }
+    }
+}
+
+dim3 unit_grid(int64_t units) {
+    return dim3((unsigned)(units < 1 ? 1 : (units < (1 << 20) ? units : 1 << 20)));
+}
+
+template <int NW, int GMAX, int BEFORE>
+hipError_t place(const int32_t* ids, int n, int first, int G, int M, Runs r, const int32_t* counts, int32_t* group_sizes,
+                 int32_t* row_of, int32_t* slot_of, int32_t* status, hipStream_t stream) {
+    hipLaunchKernelGGL((place_kernel<NW, GMAX, BEFORE>), dim3((unsigned)r.count), dim3(64 * NW), 0, stream, ids, n, first,
+                       G, M, r.slots, r.count, counts, group_sizes, row_of, slot_of, status);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t sort_count_words(int64_t n, int64_t G) { return G <= 0 ? 0 : ((int64_t)runs_of(n > 0 ? n : 0).count + 1) * G; }
+
+hipError_t launch_sort_tokens(const int32_t* ids, int n, int first, int G, int M, int32_t* group_sizes, int32_t* row_of,
+                              int32_t* slot_of, int32_t* counts, int32_t* status, hipStream_t stream) {
+    if (n <= kOneRun && G <= 1024) {
+        const Runs one{1, n > 0 ? n : 1};
+        if (G <= 256)
+            return place<16, 256, kAlone>(ids, n, first, G, M, one, counts, group_sizes, row_of, slot_of, status, stream);
+        return place<16, 1024, kAlone>(ids, n, first, G, M, one, counts, group_sizes, row_of, slot_of, status, stream);
+    }
+    const Runs r = runs_of(n);
+    if (G <= 256)
+        hipLaunchKernelGGL((count_kernel<256>), dim3((unsigned)r.count), dim3(256), 0, stream, ids, n, first, G, r.slots, counts);
+    else
+        hipLaunchKernelGGL((count_kernel<4096>), dim3((unsigned)r.count), dim3(256), 0, stream, ids, n, first, G, r.slots, counts);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (r.count <= kSumRuns) {
+        if (G <= 256)
+            return place<4, 256, kSum>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
+        return place<4, 4096, kSum>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
+    }
+    hipLaunchKernelGGL(scan_kernel, dim3((unsigned)((G + 63) / 64)), dim3(1024), 0, stream, counts, r.count, G);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (G <= 256)
+        return place<4, 256, kScanned>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
+    return place<4, 4096, kScanned>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
+}
+
+hipError_t launch_dispatch(const MoveArgs& a, const void* x, bool bf16, void* out, hipStream_t stream) {
+    const int64_t units = a.T + (a.M + kTailRows - 1) / kTailRows;
+    hipLaunchKernelGGL(dispatch_kernel, unit_grid(units), dim3(256), 0, stream, a, static_cast<const char*>(x),
+                       a.K * (bf16 ? 2 : 4), static_cast<char*>(out));
+    return hipGetLastError();
+}
+
+hipError_t launch_combine(const MoveArgs& a, const void* y, bool y_bf16, const void* residual, void* out, bool out_bf16,
+                          hipStream_t stream) {
+    const dim3 grid = unit_grid(a.T), block(256);
+    if (y_bf16) {
+        if (out_bf16) hipLaunchKernelGGL((combine_kernel<true, true>), grid, block, 0, stream, a, y, residual, out);
+        else hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, stream, a, y, residual, out);
+    } else {
+        if (out_bf16) hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, stream, a, y, residual, out);
+        else hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, stream, a, y, residual, out);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const MoveArgs& a, const void* dout, bool dout_bf16, const void* y, bool y_bf16, void* dy,
+                              float* dweights, hipStream_t stream) {
+    const int64_t units = a.T + (dy != nullptr ? (a.M + kTailRows - 1) / kTailRows : 0);
+    const dim3 grid = unit_grid(units), block(256);
+    if (dout_bf16) {
+        if (y_bf16) hipLaunchKernelGGL((combine_bwd_kernel<true, true>), grid, block, 0, stream, a, dout, y, dy, dweights);
+        else hipLaunchKernelGGL((combine_bwd_kernel<true, false>), grid, block, 0, stream, a, dout, y, dy, dweights);
+    } else {
+        if (y_bf16) hipLaunchKernelGGL((combine_bwd_kernel<false, true>), grid, block, 0, stream, a, dout, y, dy, dweights);
+        else hipLaunchKernelGGL((combine_bwd_kernel<false, false>), grid, block, 0, stream, a, dout, y, dy, dweights);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace gmm

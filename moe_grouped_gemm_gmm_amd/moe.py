@@ -1,0 +1,194 @@
+"""What stands around the experts' products of a mixture-of-experts layer
+(include/gmm_moe.h): the router, tokens sorted by expert and back, and grouped
+products with bias, activation and residual.
+
+Argument marshalling only, in the manner of the package's other calls: outputs
+are allocated with torch unless given, every call goes to torch's current
+stream of the tensors' device, the checks are the C ABI's.  A layer forward:
+
+    ids, weights = gmm_route(logits, k)
+    group_sizes, row_of, slot_of = gmm_sort_tokens(ids, G)
+    rows = gmm_dispatch(x, row_of, slot_of)
+    y = ...                                       # the experts' products
+    out = gmm_combine(y, row_of, weights=weights, residual=x)
+
+and backward:
+
+    dy, dweights = gmm_combine_bwd(dout, y, row_of, slot_of, weights)
+    drows = ...                                   # the products' gradients
+    dx = gmm_combine(drows, row_of, residual=dout)
+    dlogits = gmm_route_bwd(dweights, logits, ids)
+"""
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _DT, ffn, load_library
+from .ffn import _BF16, _FLOAT, _INT32, _arg, _check, _stream
+
+OP_SORT_TOKENS, OP_BF16_LINEAR, OP_BF16_LINEAR_BWD = 32, 33, 34
+MOE_EXPORTS = ("gmm_route", "gmm_route_bwd", "gmm_sort_tokens", "gmm_dispatch", "gmm_combine", "gmm_combine_bwd")
+SCORES = {"softmax": 0, "sigmoid": 1}
+MAX_TOPK = 64
+
+_F32 = (torch.float32,)
+
+
+def _named(value: str, table: dict, what: str) -> int:
+    if value not in table:
+        raise ValueError("%s %r is not one of %s" % (what, value, ", ".join(sorted(table))))
+    return table[value]
+
+
+def gmm_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+              normalize: bool = True, scale: float = 1.0, ids: Optional[torch.Tensor] = None,
+              weights: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The k experts of every token and their weights: (ids int32 [T,k], weights
+    fp32 [T,k]) from logits [T,E] (bf16/fp32).  score: "softmax" or "sigmoid" of
+    the logits.  bias [E] fp32: the choice is by score + bias, the weights are of
+    the score.  normalize: a token's weights sum to scale.  A logit of -infinity
+    or NaN switches the expert off; a choice that cannot be made is -1 with
+    weight 0."""
+    lib = load_library()
+    dev = logits.device
+    T, E = logits.shape
+    lp, bp = _arg(logits, None, _FLOAT, "logits", dev), _arg(bias, (E,), _F32, "bias", dev)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _check(lib, lib.gmm_route(lp, _DT[logits.dtype], bp, T, E, k, _named(score, SCORES, "score"), int(normalize), scale,
+                              _arg(ids, (T, k), _INT32, "ids", dev), _arg(weights, (T, k), _F32, "weights", dev),
+                              _stream(dev)))
+    return ids, weights
+
+
+def gmm_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                  normalize: bool = True, scale: float = 1.0, out_dtype: Optional[torch.dtype] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of gmm_route's weights with respect to the logits, [T,E] (of the
+    logits' dtype unless given), ids held fixed.  score, normalize and scale as
+    given to gmm_route."""
+    lib = load_library()
+    dev = logits.device
+    T, E = logits.shape
+    T2, k = ids.shape
+    if T2 != T:
+        raise ValueError("logits has %d rows but ids has %d" % (T, T2))
+    args = (_arg(dweights, (T, k), _F32, "dweights", dev), _arg(logits, None, _FLOAT, "logits", dev),
+            _DT[logits.dtype], _arg(ids, None, _INT32, "ids", dev), T, E, k, _named(score, SCORES, "score"),
+            int(normalize), scale)
+    if out is None:
+        out = torch.empty((T, E), dtype=out_dtype or logits.dtype, device=dev)
+    _check(lib, lib.gmm_route_bwd(*args, _arg(out, (T, E), _FLOAT, "out", dev), _DT[out.dtype], _stream(dev)))
+    return out
+
+
+def gmm_sort_tokens(ids: torch.Tensor, G: int, first: int = 0, rows: Optional[int] = None,
+                    group_sizes: Optional[torch.Tensor] = None, row_of: Optional[torch.Tensor] = None,
+                    slot_of: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None
+                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The order of the slots (token t's choice j is slot t k + j) by expert:
+    (group_sizes int32 [G], row_of int32 [T,k], slot_of int32 [rows]) from ids
+    int32 [T,k].  Experts first .. first + G - 1 are sorted; a slot with another
+    id has row -1.  rows (default T k): the sorted buffer's; slots past it have
+    row -1 and device_status(ws) tells."""
+    lib = load_library()
+    dev = ids.device
+    T, k = ids.shape
+    M = T * k if rows is None else rows
+    ip = _arg(ids, None, _INT32, "ids", dev)
+    if group_sizes is None:
+        group_sizes = torch.empty(G, dtype=torch.int32, device=dev)
+    if row_of is None:
+        row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if slot_of is None:
+        slot_of = torch.empty(max(M, 0), dtype=torch.int32, device=dev)
+    if ws is None:
+        ws = torch.empty(max(lib.gmm_workspace_bytes(OP_SORT_TOKENS, T * k, 0, 0, G), 16), dtype=torch.uint8, device=dev)
+    _check(lib, lib.gmm_sort_tokens(ip, T, k, first, G, M, _arg(group_sizes, (G,), _INT32, "group_sizes", dev),
+                                    _arg(row_of, (T, k), _INT32, "row_of", dev),
+                                    _arg(slot_of, (max(M, 0),), _INT32, "slot_of", dev), *ffn._status(ws, dev),
+                                    _stream(dev)))
+    return group_sizes, row_of, slot_of
+
+
+def gmm_dispatch(x: torch.Tensor, row_of: torch.Tensor, slot_of: torch.Tensor, out: Optional[torch.Tensor] = None
+                 ) -> torch.Tensor:
+    """Tokens x [T,K] (bf16/fp32) in the sorted order, [M,K]; rows without a slot
+    are zeros."""
+    lib = load_library()
+    dev = x.device
+    T, K = x.shape
+    T2, k = row_of.shape
+    if T2 != T:
+        raise ValueError("x has %d rows but row_of has %d" % (T, T2))
+    M = slot_of.numel()
+    args = (_arg(x, None, _FLOAT, "x", dev), _DT[x.dtype], _arg(row_of, None, _INT32, "row_of", dev),
+            _arg(slot_of, (M,), _INT32, "slot_of", dev), T, k, M, K)
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=dev)
+    _check(lib, lib.gmm_dispatch(*args, _arg(out, (M, K), (x.dtype,), "out", dev), _stream(dev)))
+    return out
+
+
+def gmm_combine(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Results y [M,K] back to their tokens, [T,K] (of y's dtype unless given):
+    residual + the sum of a token's rows, each times its weight (fp32 [T,k]).
+    Without weights the gradient of gmm_dispatch."""
+    lib = load_library()
+    dev = y.device
+    M, K = y.shape
+    T, k = row_of.shape
+    if out is None:
+        out = torch.empty((T, K), dtype=out_dtype or y.dtype, device=dev)
+    _check(lib, lib.gmm_combine(_arg(y, None, _FLOAT, "y", dev), _DT[y.dtype], _arg(row_of, None, _INT32, "row_of", dev),
+                                _arg(weights, (T, k), _F32, "weights", dev),
+                                _arg(residual, (T, K), (out.dtype,), "residual", dev), T, k, M, K,
+                                _arg(out, (T, K), _FLOAT, "out", dev), _DT[out.dtype], _stream(dev)))
+    return out
+
+
+def gmm_combine_bwd(dout: torch.Tensor, y: Optional[torch.Tensor], row_of: torch.Tensor, slot_of: torch.Tensor,
+                    weights: Optional[torch.Tensor], want_dy: bool = True, want_dweights: bool = True,
+                    dy_dtype: Optional[torch.dtype] = None, dy: Optional[torch.Tensor] = None,
+                    dweights: Optional[torch.Tensor] = None
+                    ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of gmm_combine from dout [T,K]: (dy [M,K], dweights fp32 [T,k]).
+    y is needed for dweights, weights for dy; dy has y's dtype (without y:
+    dy_dtype, or dout's).  want_dy / want_dweights False leaves that one out
+    (None).  The residual's gradient is dout."""
+    lib = load_library()
+    dev = dout.device
+    T, K = dout.shape
+    T2, k = row_of.shape
+    if T2 != T:
+        raise ValueError("dout has %d rows but row_of has %d" % (T, T2))
+    M = slot_of.numel()
+    dt = y.dtype if y is not None else (dy.dtype if dy is not None else dy_dtype or dout.dtype)
+    args = (_arg(dout, None, _FLOAT, "dout", dev), _DT[dout.dtype], _arg(y, (M, K), _FLOAT, "y", dev), _DT.get(dt, -1),
+            _arg(row_of, None, _INT32, "row_of", dev), _arg(slot_of, (M,), _INT32, "slot_of", dev),
+            _arg(weights, (T, k), _F32, "weights", dev), T, k, M, K)
+    if dy is None and want_dy:
+        dy = torch.empty((M, K), dtype=dt, device=dev)
+    if dweights is None and want_dweights:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _check(lib, lib.gmm_combine_bwd(*args, _arg(dy, (M, K), (dt,), "dy", dev),
+                                    _arg(dweights, (T, k), _F32, "dweights", dev), _stream(dev)))
+    return dy, dweights
+
+
+def _declare(lib) -> None:
+    """ctypes signatures of this header's calls."""
+    P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    lib.gmm_route.argtypes = [P, I, P, I64, I64, I64, I, I, F, P, P, P]
+    lib.gmm_route_bwd.argtypes = [P, P, I, P, I64, I64, I64, I, I, F, P, I, P]
+    lib.gmm_sort_tokens.argtypes = [P, I64, I64, I64, I64, I64, P, P, P, P, SZ, P]
+    lib.gmm_dispatch.argtypes = [P, I, P, P, I64, I64, I64, I64, P, P]
+    lib.gmm_combine.argtypes = [P, I, P, P, P, I64, I64, I64, I64, P, I, P]
+    lib.gmm_combine_bwd.argtypes = [P, I, P, I, P, P, P, I64, I64, I64, I64, P, P, P]
+    for name in MOE_EXPORTS:
+        getattr(lib, name).restype = I

@@ -1,0 +1,230 @@
+"""GPU: the router and its gradient against the formulas in 64 bits.
+
+Bounds.  With u = 2^-24 (half a step of fp32) and d the largest |logit - top|
+of a case: the difference l - top is off by d u, so exp(l - top) by d u plus
+its own rounding (2 u), a sum of E positive terms in lanes of up to 64 and 6
+lane moves by 70 u, quotients and products by u each.  A weight is then off by
+at most (2 d + 100) u of itself, and a gradient by (4 d + 300) u of the terms it
+is made of (a sum of k products more), besides the rounding of what it is
+stored as.  Values below the smallest normal number lose bits: 2^-126 is added.
+"""
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_gmm_amd as gmm
+import moe_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+U, TINY = 2.0 ** -24, 2.0 ** -126
+
+
+def inputs(T, E, dt, seed, spread=1.5):
+    g = torch.Generator().manual_seed(seed)
+    l = (torch.randn(T, E, generator=g) * spread + torch.randn(E, generator=g) * 0.5).to(dt)
+    return l, torch.randn(E, generator=g) * 0.1
+
+
+def span(l):
+    """The largest |logit - top| among experts that are on, and at least 1."""
+    c = ref.clean(l)
+    with np.errstate(invalid="ignore"):
+        d = c.max(axis=1, keepdims=True) - c
+    d = np.abs(d[np.isfinite(d)])
+    return max(1.0, min(200.0, float(d.max(initial=0)) + float(np.abs(c[np.isfinite(c)]).max(initial=0))))
+
+
+def check_fwd(l, k, bias, score, normalize, scale):
+    b = None if bias is None else bias.to(DEV)
+    ids, w = gmm.gmm_route(l.to(DEV), k, bias=b, score=score, normalize=normalize, scale=scale)
+    torch.cuda.synchronize()
+    ln = l.double().numpy()
+    rid, rw = ref.route(ln, k, None if bias is None else bias.double().numpy(), score, normalize, scale)
+    assert ids.dtype == torch.int32 and np.array_equal(ids.cpu().numpy(), rid)
+    got = w.double().cpu().numpy()
+    assert np.all(np.isfinite(got))
+    assert np.all(np.abs(got - rw) <= (2 * span(ln) + 100) * U * np.abs(rw) + TINY * abs(scale))
+    return ids
+
+
+def check_bwd(l, ids, score, normalize, scale, out_dtype, seed=5):
+    T, k = ids.shape
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(seed))
+    got = gmm.gmm_route_bwd(dw.to(DEV), l.to(DEV), ids.to(DEV), score=score, normalize=normalize, scale=scale,
+                            out_dtype=out_dtype)
+    torch.cuda.synchronize()
+    assert got.dtype == (out_dtype or l.dtype)
+    ln = l.double().numpy()
+    want, mag = ref.route_bwd(dw.double().numpy(), ln, ids.cpu().numpy(), score, normalize, scale)
+    half = torch.finfo(got.dtype).eps / 2
+    g = got.double().cpu().numpy()
+    assert np.all(np.isfinite(g))
+    assert np.all(np.abs(g - want) <= (4 * span(ln) + 300) * U * mag + half * np.abs(want) + 4 * TINY * abs(scale))
+
+
+FORMS = [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)]
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (1, 256, 8), (130, 7, 3), (65, 8, 8), (33, 13, 4), (37, 30, 16),
+                                   (203, 60, 6), (64, 64, 64), (19, 65, 8), (41, 255, 7), (500, 256, 8), (9, 257, 10),
+                                   (21, 512, 16), (7, 1000, 64), (5, 1025, 8), (3, 4096, 64), (5, 3001, 9)])
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("bias", [False, True])
+def test_choice_weights_and_gradient(T, E, k, dt, bias):
+    for i, (score, normalize) in enumerate(FORMS):
+        l, b = inputs(T, E, dt, 100 * T + E + i)
+        scale = 1.0 if i % 2 else 2.5
+        ids = check_fwd(l, k, b if bias else None, score, normalize, scale)
+        check_bwd(l, ids, score, normalize, scale, None if i < 2 else (BF if dt == F32 else F32))
+
+
+@pytest.mark.parametrize("score,normalize", FORMS)
+@pytest.mark.parametrize("E", [8, 60, 256, 700])
+def test_equal_keys_go_to_the_lower_index(score, normalize, E):
+    l = torch.randint(-2, 3, (77, E), generator=torch.Generator().manual_seed(E)).float() * 0.5
+    l[5] = 0.0
+    l[6, ::2] = -0.0                       # one zero
+    for dt in (F32, BF):
+        check_fwd(l.to(dt), min(8, E), None, score, normalize, 1.0)
+        check_fwd(l.to(dt), min(8, E), torch.zeros(E), score, normalize, 1.0)
+
+
+@pytest.mark.parametrize("score,normalize", FORMS)
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E", [8, 60, 256, 300])
+def test_experts_that_are_off(score, normalize, bias, E):
+    """-infinity and NaN switch an expert off; a token with fewer than k others, or none, gets -1."""
+    l, b = inputs(40, E, F32, E)
+    l[:, 1] = float("-inf")
+    l[:, 3] = float("nan")
+    l[4] = float("-inf")
+    l[5] = float("nan")
+    l[6, 5:] = float("-inf")
+    l[7, 2] = torch.finfo(F32).min        # the lowest value of the type is a logit like any other
+    l[8] = torch.finfo(F32).min
+    k = 6
+    ids = check_fwd(l, k, b if bias else None, score, normalize, 1.5)
+    off = ((ids == 1) | (ids == 3)).any(1)
+    off[8] = False                        # every expert of token 8 is on
+    assert (ids[4:6] == -1).all() and not off.any() and (ids[6] == -1).sum() == 3
+    check_bwd(l, ids, score, normalize, 1.5, None)
+    g = gmm.gmm_route_bwd(torch.ones(40, k, device=DEV), l.to(DEV), ids, score=score, normalize=normalize)
+    assert (g[4:6] == 0).all() and (g[:8, [1, 3]] == 0).all() and (g[9:, [1, 3]] == 0).all()
+
+
+@pytest.mark.parametrize("score,normalize", FORMS)
+def test_far_logits(score, normalize):
+    """Infinities, and logits whose exponentials overflow or vanish: shares of the chosen scores still add up."""
+    l, b = inputs(12, 64, F32, 9)
+    l[0, 10] = float("inf")
+    l[1] -= 500.0
+    l[2] += 500.0
+    l[3, :32] -= 90.0
+    l[4] *= 60.0
+    l[5, 3] = 3e38
+    l[6, 3], l[6, 9] = float("inf"), float("inf")
+    for bias in (None, b):
+        ids = check_fwd(l, 8, bias, score, normalize, 1.0)
+        check_bwd(l, ids, score, normalize, 1.0, None)
+    if normalize:
+        w = gmm.gmm_route(l.to(DEV), 8, score=score)[1]
+        assert torch.allclose(w.sum(1), torch.ones(12, device=DEV), atol=1e-5)
+
+
+def test_bias_chooses_and_does_not_weigh():
+    l, _ = inputs(50, 32, F32, 21)
+    b = torch.zeros(32)
+    b[7], b[11], b[13], b[15] = 100.0, float("-inf"), float("nan"), float("inf")
+    ids = check_fwd(l, 4, b, "sigmoid", True, 1.0)
+    assert (ids[:, 0] == 15).all() and (ids[:, 1] == 7).all() and not ((ids == 11) | (ids == 13)).any()
+    # a bias that takes every expert but two away
+    b[:] = float("-inf")
+    b[3] = b[9] = 0.0
+    ids = check_fwd(l, 4, b, "softmax", True, 1.0)
+    assert (ids[:, 2:] == -1).all()
+
+
+def test_choice_between_scores_that_32_bits_cannot_tell_apart():
+    """Keys whose 64-bit values differ below fp32's resolution."""
+    E = 64
+    l = torch.full((4, E), 3.0)
+    l[:, 17] = torch.nextafter(torch.tensor(3.0), torch.tensor(4.0))
+    l[1] += 12.0
+    check_fwd(l, 3, torch.full((E,), 0.25), "sigmoid", True, 1.0)
+    check_fwd(l, 3, torch.full((E,), 0.25), "softmax", True, 1.0)
+
+
+def test_gradient_of_bad_and_repeated_ids():
+    """Ids outside the experts take no part; an expert named twice gets both gradients."""
+    l, _ = inputs(6, 40, F32, 31)
+    ids = torch.tensor([[0, 1, 2], [-1, 5, 40], [-2147483648, 2147483647, 7], [9, 9, 9], [3, 4, 3], [-1, -1, -1]],
+                       dtype=torch.int32)
+    for score, normalize in FORMS:
+        if normalize:
+            continue
+        check_bwd(l, ids, score, normalize, 1.0, None)
+    for score in ("softmax", "sigmoid"):
+        clean_ids = torch.where((ids >= 0) & (ids < 40), ids, torch.full_like(ids, -1))
+        check_bwd(l, clean_ids, score, True, 1.0, None)
+        dw = torch.randn(6, 3, device=DEV)
+        a = gmm.gmm_route_bwd(dw, l.to(DEV), ids.to(DEV), score=score)
+        assert torch.equal(a, gmm.gmm_route_bwd(dw, l.to(DEV), clean_ids.to(DEV), score=score))
+
+
+@pytest.mark.parametrize("score,normalize", FORMS)
+def test_gradient_against_differences(score, normalize):
+    """Central differences of the 64-bit weights: the gradient is that of what the forward computes."""
+    l, b = inputs(5, 24, F32, 41, spread=1.0)
+    ids, _ = gmm.gmm_route(l.to(DEV), 4, bias=b.to(DEV), score=score, normalize=normalize, scale=2.0)
+    dw = torch.randn(5, 4, generator=torch.Generator().manual_seed(3))
+    g = gmm.gmm_route_bwd(dw.to(DEV), l.to(DEV), ids, score=score, normalize=normalize, scale=2.0).double().cpu().numpy()
+    idn, ln, h = ids.cpu().numpy(), l.double().numpy(), 1e-5
+
+    def value(z):
+        s = ref.share(z, idn, score) if normalize else np.take_along_axis(ref.scores(z, score), idn, 1)
+        return (2.0 * s * dw.double().numpy()).sum(axis=1)
+
+    for e in range(24):
+        up, down = ln.copy(), ln.copy()
+        up[:, e] += h
+        down[:, e] -= h
+        # fp32 gradient (400 u of terms up to 2 |dw| < 10) and h^2 of third derivatives
+        assert np.all(np.abs((value(up) - value(down)) / (2 * h) - g[:, e]) <= 400 * U * 10 + 1e-7)
+
+
+def test_outputs_given_and_rows_left_alone():
+    l, _ = inputs(70, 60, BF, 51)
+    ids = torch.full((72, 6), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((72, 6), -7.0, device=DEV)
+    a, b = gmm.gmm_route(l.to(DEV), 6)
+    gmm.gmm_route(l.to(DEV), 6, ids=ids[:70], weights=w[:70])
+    assert torch.equal(ids[:70], a) and torch.equal(w[:70], b) and (ids[70:] == -7).all() and (w[70:] == -7).all()
+    dl = torch.full((72, 60), -7.0, device=DEV)
+    gmm.gmm_route_bwd(torch.ones(70, 6, device=DEV), l.to(DEV), a, out=dl[:70])
+    assert (dl[70:] == -7).all() and not (dl[:70] == -7).any()
+
+
+def test_no_tokens():
+    ids, w = gmm.gmm_route(torch.zeros(0, 16, device=DEV), 4)
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+    assert gmm.gmm_route_bwd(w, torch.zeros(0, 16, device=DEV), ids).shape == (0, 16)
+
+
+def test_other_streams_and_repeats():
+    l, b = inputs(3000, 256, F32, 61)
+    ld, bd = l.to(DEV), b.to(DEV)
+    want = gmm.gmm_route(ld, 8, bias=bd, score="sigmoid")
+    dw = torch.randn(3000, 8, device=DEV)
+    gwant = gmm.gmm_route_bwd(dw, ld, want[0], score="sigmoid")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            o = gmm.gmm_route(ld, 8, bias=bd, score="sigmoid")
+            got.append(o + (gmm.gmm_route_bwd(dw, ld, o[0], score="sigmoid"),))
+    torch.cuda.synchronize()
+    for o in got:
+        assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1]) and torch.equal(o[2], gwant)
