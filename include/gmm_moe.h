@@ -144,6 +144,46 @@ GMM_API int gmm_combine_bwd(const void *dout, int dout_dtype, const void *y, int
                             int64_t T, int64_t k, int64_t M, int64_t K, void *dy, float *dweights,
                             void *stream);
 
+/*
+ * gmm_bf16_linear -- grouped product with its epilogue in one kernel:
+ *     pre = lhs . rhs[g] + bias[g],   out = act(pre) + residual,
+ *   the sums, the activation and the residual in fp32, out rounded once.  The
+ *   few-row form a serving step needs is chosen inside, from M, N and G.
+ * lhs: [M,K] bf16.  rhs: [G,K,N] bf16.  K and N multiples of 64.
+ * bias: [G,N], bias_dtype GMM_BF16 or GMM_F32, or NULL.
+ * act: a gmm_activation.
+ * residual: [M,N] of out_dtype, or NULL; it may be out itself.
+ * out: [M,N], GMM_BF16 or GMM_F32.
+ * pre: NULL, or [M,N] bf16 that receives pre, which the backward pass needs
+ *   unless act is GMM_ACT_NONE.
+ * Rows at or past the groups' total: out and pre are zeros there, whatever
+ *   lhs and residual hold.
+ */
+GMM_API int gmm_bf16_linear(const void *lhs, const void *rhs, const int32_t *group_sizes, int64_t M,
+                            int64_t K, int64_t N, int64_t G, const void *bias, int bias_dtype,
+                            int act, const void *residual, void *out, int out_dtype, void *pre,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * gmm_bf16_linear_bwd -- its backward pass (the residual's gradient is dout):
+ *     dpre = dout * act'(pre)   (fp32; act' of ReLU is 0 at 0),
+ *     dx = dpre . rhs[g]^T,   dw[g] = lhs_g^T dpre_g,   db[g] = column sums of dpre_g,
+ *   the products with dpre rounded to bf16 (unless act is GMM_ACT_NONE, where
+ *   it is dout) and fp32 accumulation, db summed in fp32 from the unrounded
+ *   values; an empty group's dw and db are 0.
+ * dout: [M,N] bf16.  pre: [M,N] bf16 as gmm_bf16_linear kept it (not read, and
+ *   may be NULL, with GMM_ACT_NONE).  rhs: [G,K,N] bf16 (needed for dx).
+ * lhs: [M,K] bf16 (needed for dw).
+ * dx [M,K], dw [G,K,N], db [G,N]: each GMM_BF16 or GMM_F32, NULL where not
+ *   wanted (all: GMM_ERR_NULL).
+ * ws: gmm_workspace_bytes(GMM_OP_BF16_LINEAR_BWD, ...) bytes, the status block,
+ *   dpre and partial sums of db; a call needs one of its own until it has finished.
+ */
+GMM_API int gmm_bf16_linear_bwd(const void *dout, const void *rhs, const int32_t *group_sizes,
+                                const void *lhs, const void *pre, int act, int64_t M, int64_t K,
+                                int64_t N, int64_t G, void *dx, int dx_dtype, void *dw, int dw_dtype,
+                                void *db, int db_dtype, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

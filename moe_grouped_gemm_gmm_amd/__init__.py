@@ -439,5 +439,6 @@ def gmm_bf16_dx(dy: torch.Tensor, w: torch.Tensor, group_sizes: torch.Tensor,
 from . import ffn, moe  # noqa: E402  (they use the helpers above)
 from .ffn import (FFN_EXPORTS, OP_BF16_SWIGLU, OP_BF16_SWIGLU_BWD, OP_TGMM_MX8,  # noqa: E402,F401
                   gmm_bf16_swiglu, gmm_bf16_swiglu_bwd, gmm_dequantize_mx8, gmm_quantize_mx8, tgmm_mx8)
-from .moe import (MAX_TOPK, MOE_EXPORTS, OP_SORT_TOKENS, gmm_combine, gmm_combine_bwd, gmm_dispatch,  # noqa: E402,F401
-                  gmm_route, gmm_route_bwd, gmm_sort_tokens)
+from .moe import (ACTIVATIONS, MAX_TOPK, MOE_EXPORTS, OP_BF16_LINEAR, OP_BF16_LINEAR_BWD,  # noqa: E402,F401
+                  OP_SORT_TOKENS, SCORES, gmm_bf16_linear, gmm_bf16_linear_bwd, gmm_combine, gmm_combine_bwd,
+                  gmm_dispatch, gmm_route, gmm_route_bwd, gmm_sort_tokens)

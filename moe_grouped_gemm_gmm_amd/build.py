@@ -15,7 +15,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgmm.so")
 SOURCES = ["gmm_api.cpp", "gmm_config.cpp", "gmm_quant.hip", "gmm_fp8.hip", "gmm_bf16.hip",
            "gmm_noalloc.hip", "gmm_probe.hip", "gmm_ffn_api.cpp", "gmm_ffn.hip", "gmm_ffn_elem.hip",
-           "gmm_moe_api.cpp", "gmm_route.hip", "gmm_tokens.hip"]
+           "gmm_moe_api.cpp", "gmm_route.hip", "gmm_tokens.hip", "gmm_linear.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

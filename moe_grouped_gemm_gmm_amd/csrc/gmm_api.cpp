@@ -117,11 +117,15 @@ size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G) {
             return kWsStatusBytes;
         case GMM_OP_BF16_SWIGLU:
         case GMM_OP_TGMM_MX8:
+        case GMM_OP_BF16_LINEAR:
             return kWsStatusBytes;
         case GMM_OP_BF16_SWIGLU_BWD:   // and dP, bf16 [M,2N]
             return kWsStatusBytes + (M > 0 && N > 0 ? (size_t)M * 4 * (size_t)N : 0);
         case GMM_OP_SORT_TOKENS:       // and the runs' counts of every expert
             return kWsStatusBytes + 4 * (size_t)gmm::sort_count_words(M, G);
+        case GMM_OP_BF16_LINEAR_BWD:   // and dpre, bf16 [M,N], and partial sums of db
+            return kWsStatusBytes + (M > 0 && N > 0 ? (size_t)M * 2 * (size_t)N : 0) +
+                   4 * (size_t)gmm::linear_part_words(M, N, G);
         default:
             return 0;
     }

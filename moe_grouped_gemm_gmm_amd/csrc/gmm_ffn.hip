@@ -1,7 +1,8 @@
-// Grouped products of the gated expert block for gfx950: its forward, and the
-// products of its backward pass.
+// Grouped products of the expert block for gfx950: its forward, gated or plain,
+// and the products of its backward pass.
 //
 //   kGated   P = x . w[g],  h = silu(P[:, :N]) * P[:, N:]   (reduce over K)
+//   kLinear  P = x . w[g] + b[g],  act(P) + residual        (reduce over K)
 //   kBwdX    dx = dP . w[g]^T                               (reduce over 2N)
 //   kBwdW    dw[g] = x_g^T dP_g                             (reduce over rows)
 //   kBwdWQ   the same with x from an 8-bit checkpoint
@@ -17,8 +18,9 @@
 //   ffn_kernel       128 x 128 or 128 x 256 tiles, every product
 //   ffn_bwd_kernel   both products of a small backward pass in one launch
 //   ffn_ws_kernel    160 x 256 tiles fed by load waves, forward and dX
-//   gated_few_kernel the forward for few rows per expert, K split over waves
+//   few_kernel       the forward for few rows per expert, K split over waves
 #include "gmm_launch.hpp"
+#include "gmm_linear.hpp"
 #include "gmm_mx8.hpp"
 #include "gmm_tile.hpp"
 
@@ -29,7 +31,7 @@ namespace gmm {
 
 namespace {
 
-enum FfnMode { kGated = 0, kBwdX = 1, kBwdW = 2, kBwdWQ = 3 };
+enum FfnMode { kGated = 0, kBwdX = 1, kBwdW = 2, kBwdWQ = 3, kLinear = 4 };
 enum Save { kSaveNone = 0, kSaveBf16 = 1, kSaveMx8 = 2 };
 
 struct FfnItem {
@@ -187,7 +189,7 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int block, int* s_inf
         it.hi = s_info[2];
         it.c0 = s_info[3] * (MODE == kGated ? TC / 2 : TC);
         it.red_lo = 0;
-        it.red_hi = MODE == kGated ? a.K : a.NN;
+        it.red_hi = MODE == kBwdX ? a.NN : a.K;
         return true;
     }
 }
@@ -196,11 +198,13 @@ __device__ __forceinline__ bool ffn_item(const FfnArgs& a, int block, int* s_inf
 template <int MODE, bool OUT_BF16, int SAVE, int TC, int NTHR>
 __device__ __forceinline__ void zero_tail(const FfnArgs& a, const FfnItem& it) {
     const int N = a.NN / 2;
-    const int ocols = MODE == kGated ? N : a.K;
+    const int ocols = MODE == kGated ? N : (MODE == kLinear ? a.NN : a.K);
     const int n = min(MODE == kGated ? TC / 2 : TC, ocols - it.c0);
     constexpr int kOut = OUT_BF16 ? 2 : 4;
     zero_block(a.out, (int64_t)ocols * kOut, it.lo, it.hi, (int64_t)it.c0 * kOut, n * kOut, NTHR);
-    if constexpr (SAVE == kSaveBf16) {
+    if constexpr (MODE == kLinear) {
+        if (a.gu != nullptr) zero_block(a.gu, (int64_t)ocols * 2, it.lo, it.hi, (int64_t)it.c0 * 2, n * 2, NTHR);
+    } else if constexpr (SAVE == kSaveBf16) {
         zero_block(a.gu, (int64_t)a.NN * 2, it.lo, it.hi, (int64_t)it.c0 * 2, n * 2, NTHR);
         zero_block(a.gu, (int64_t)a.NN * 2, it.lo, it.hi, (int64_t)(N + it.c0) * 2, n * 2, NTHR);
     }
@@ -307,6 +311,53 @@ __device__ __forceinline__ void gated_epilogue(const FfnArgs& a, const FfnItem& 
         if (it.c0 + c < N)
             store_out(reinterpret_cast<E*>(a.out) + (int64_t)(it.row0 + r) * N + it.c0 + c,
                       *reinterpret_cast<const uint4*>(om + r * P + c));
+    }
+}
+
+// Epilogue of the plain forward: each wave stages 32 rows x 64 columns of fp32
+// sums at a time and finishes whole row segments (128 bytes of bf16), eight
+// columns a lane, so the bias stays in registers and the residual, the kept
+// sums and the output cross the chip in full lines.
+template <bool OUT_BF16, int NJ>
+__device__ __forceinline__ void linear_epilogue(const FfnArgs& a, const FfnItem& it, const v4f (&acc)[4][NJ],
+                                                uint16_t* sm) {
+    constexpr int kRow = 64 + 4;   // fp32
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    const int wm = tid >> 7, wn = (tid >> 6) & 1, lr = lane & 15, lg = lane >> 4;
+    float* ep = reinterpret_cast<float*>(sm) + wave * 32 * kRow;
+    const int orow = lane >> 3, ocol = (lane & 7) * 8;
+#pragma unroll
+    for (int q = 0; q < NJ / 4; ++q) {
+        // fragments 4q .. 4q + 3 are 64 neighbouring columns
+        const int col = it.c0 + (NJ == 8 ? 16 * NJ * q + 64 * wn : 0) +
+                        (NJ == 8 ? ocol : (ocol >= 32 ? 64 : 0) + 32 * wn + ocol % 32);
+        const bool in = col < a.NN;
+        float bias[8];
+        linear_bias(a, it.g, in ? col : 0, bias);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<v4f*>(ep + (16 * i + lr) * kRow + 16 * j + 4 * lg) = acc[2 * half + i][4 * q + j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int r = 8 * p + orow, t = 32 * half + r;
+                const int row = it.row0 + 32 * (t >> 4) + 16 * wm + (t & 15);
+                if (row < it.hi && in) {
+                    float z[8];
+#pragma unroll
+                    for (int c = 0; c < 8; c += 4) {
+                        const v4f v = *reinterpret_cast<const v4f*>(ep + r * kRow + ocol + c);
+                        z[c] = v[0]; z[c + 1] = v[1]; z[c + 2] = v[2]; z[c + 3] = v[3];
+                    }
+                    linear_finish<OUT_BF16, 8>(a, row, col, bias, z);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
     }
 }
 
@@ -511,7 +562,7 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
     //      and NIB of B per wave and slice.  Rows and columns past the operand
     //      are clamped to its last ones (they only reach outputs that are not
     //      stored); a 16-row block of A without rows is not loaded.
-    const int lda = MODE == kGated ? K : NN;
+    const int lda = MODE == kBwdX ? NN : K;
     const uint16_t* wg = a.b + (kW ? 0 : (int64_t)g * K * NN);
     const int na = MODE == kBwdWQ ? 0 : (kW ? 2 : (wave < blocks) + (wave + 4 < blocks));
     int64_t a_off[2], b_off[NIB];
@@ -551,7 +602,7 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
             const uint16_t* pb;
             if constexpr (kW)
                 pb = a.b + (int64_t)min(r0 + b_row[i], red_hi - 1) * NN + b_off[i];
-            else if constexpr (MODE == kGated)
+            else if constexpr (MODE == kGated || MODE == kLinear)
                 pb = wg + (int64_t)(r0 + b_row[i]) * NN + b_off[i];
             else
                 pb = wg + b_off[i] + r0;
@@ -714,6 +765,9 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int block, uint16_t* 
 
     if constexpr (MODE == kGated) {
         gated_epilogue<OUT_BF16, SAVE, NJ>(a, it, acc, ring);
+    } else if constexpr (MODE == kLinear) {
+        static_assert(4 * 32 * 68 * 4 <= S * kSt * 2, "epilogue staging fits the ring");
+        linear_epilogue<OUT_BF16, NJ>(a, it, acc, ring);
     } else {
         // each wave stages 64 rows x 64 columns at a time and stores whole row
         // segments; widths are multiples of 64, so a wave's 64 columns are all
@@ -798,7 +852,8 @@ bool set_grid(FfnArgs& a) {
         a.ntiles_c = (a.NN + T::kTC - 1) / T::kTC;
         nblocks = (int64_t)a.G * a.ntiles_r * a.ntiles_c;
     } else {
-        const int cols = MODE == kGated ? a.NN / 2 : a.K, tc = MODE == kGated ? T::kTC / 2 : T::kTC;
+        const int cols = MODE == kGated ? a.NN / 2 : (MODE == kLinear ? a.NN : a.K);
+        const int tc = MODE == kGated ? T::kTC / 2 : T::kTC;
         a.ntiles_r = 0;
         a.ntiles_c = (cols + tc - 1) / tc;
         nblocks = max_work_items(a.M, a.G < a.M ? a.G : a.M, T::kTR) * a.ntiles_c;
@@ -1533,8 +1588,8 @@ __device__ __forceinline__ void few_slice(v8bf (&fa)[MB], v8bf (&fb)[NF], const 
     for (int i = 0; i < NF; ++i) fb[i] = __builtin_bit_cast(v8bf, u64x2{o[2 * i], o[2 * i + 1]});
 }
 
-template <bool OUT_BF16, int SAVE, int MB, int CT, int NW, int S>
-__global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) {
+template <int MODE, bool OUT_BF16, int SAVE, int MB, int CT, int NW, int S>
+__global__ __launch_bounds__(64 * NW, 1) void few_kernel(const FfnArgs a) {
     constexpr int TR = 16 * MB, NTHR = 64 * NW, NF = CT / 8, NI = CT / 8;
     constexpr int kA = TR * 32, kB = 64 * CT, kSt = kA + kB;   // elements
     constexpr int kRow = 2 * CT + 4;                           // fp32 staging row
@@ -1547,9 +1602,9 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     FfnItem it;
-    if (!ffn_item<kGated, TR, 2 * CT>(a, blockIdx.x, s_info, it)) return;
+    if (!ffn_item<MODE, TR, 2 * CT>(a, blockIdx.x, s_info, it)) return;
     if (it.g == a.G) {
-        zero_tail<kGated, OUT_BF16, SAVE, 2 * CT, NTHR>(a, it);
+        zero_tail<MODE, OUT_BF16, SAVE, 2 * CT, NTHR>(a, it);
         return;
     }
     const int K = a.K, NN = a.NN, N = NN / 2;
@@ -1565,7 +1620,7 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
     for (int i = 0; i < NI; ++i) {
         const int r = (64 / LPR) * i + lane / LPR, p = lane % LPR;
         const int col = 16 * ((p >> 1) ^ few_key<CT>(r)) + 8 * (p & 1);
-        b_off[i] = (int64_t)r * NN + it.c0 + (col < CT ? col : N + col - CT);
+        b_off[i] = (int64_t)r * NN + it.c0 + (MODE == kLinear || col < CT ? col : N + col - CT);
     }
     const uint16_t* wg = a.b + (int64_t)it.g * K * NN;
     auto issue = [&](int i, int stage) {
@@ -1632,6 +1687,21 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
         for (int j = 0; j < NF; ++j)
             *reinterpret_cast<v4f*>(part + (wave * TR + 16 * m + lr) * kRow + 16 * j + 4 * lg) = acc[m][j];
     __syncthreads();
+    if constexpr (MODE == kLinear) {
+        for (int e = tid; e < TR * (CT / 2); e += NTHR) {   // 4 columns a thread
+            const int r = e / (CT / 2), c = (e % (CT / 2)) * 4, row = it.row0 + r;
+            if (row >= it.hi) continue;
+            float z[4], bias[4];
+            linear_bias(a, it.g, it.c0 + c, bias);
+            v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) s += *reinterpret_cast<const v4f*>(part + (w * TR + r) * kRow + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = s[i];
+            linear_finish<OUT_BF16, 4>(a, row, it.c0 + c, bias, z);
+        }
+        return;
+    }
     // CT / 4 threads a row, 4 gate and 4 up columns each
     constexpr int TPR = CT / 4;
     for (int e = tid; e < TR * TPR; e += NTHR) {
@@ -1671,11 +1741,11 @@ __global__ __launch_bounds__(64 * NW, 1) void gated_few_kernel(const FfnArgs a) 
     }
 }
 
-template <bool OUT_BF16, int SAVE, int MB, int CT, int NW, int S>
+template <int MODE, bool OUT_BF16, int SAVE, int MB, int CT, int NW, int S>
 hipError_t launch_few(FfnArgs a, hipStream_t stream) {
-    a.ntiles_c = a.NN / 2 / CT;
+    a.ntiles_c = a.NN / 2 / CT;   // 2 CT columns of the second operand
     a.nblocks = (int)(max_work_items(a.M, a.G < a.M ? a.G : a.M, 16 * MB) * a.ntiles_c);
-    hipLaunchKernelGGL((gated_few_kernel<OUT_BF16, SAVE, MB, CT, NW, S>), dim3((unsigned)a.nblocks), dim3(64 * NW), 0,
+    hipLaunchKernelGGL((few_kernel<MODE, OUT_BF16, SAVE, MB, CT, NW, S>), dim3((unsigned)a.nblocks), dim3(64 * NW), 0,
                        stream, a);
     return hipGetLastError();
 }
@@ -1758,23 +1828,33 @@ int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean, bool 
 // experts (more workgroups than CUs) 29.4 against 20.7 us.
 constexpr int kFewMaxRows = 64;   // mean rows an expert: up to 4 blocks of 16
 
-template <bool OUT_BF16, int SAVE, int MB>
+template <int MODE, bool OUT_BF16, int SAVE, int MB>
 hipError_t launch_few_mb(const FfnArgs& a, const FfnChoice& c, hipStream_t stream) {
     if constexpr (SAVE != kSaveMx8)
-        if (c.cols == 32) return launch_few<OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
-    return launch_few<OUT_BF16, SAVE, MB, 32, 4, 3>(a, stream);
+        if (c.cols == 32) return launch_few<MODE, OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
+    return launch_few<MODE, OUT_BF16, SAVE, MB, 32, 4, 3>(a, stream);
+}
+template <int MODE, bool OUT_BF16, int SAVE>
+hipError_t launch_few_rows(const FfnArgs& a, const FfnChoice& c, hipStream_t stream) {
+    if (c.rows == 16) return launch_few_mb<MODE, OUT_BF16, SAVE, 1>(a, c, stream);
+    if (c.rows == 32) return launch_few_mb<MODE, OUT_BF16, SAVE, 2>(a, c, stream);
+    return launch_few_mb<MODE, OUT_BF16, SAVE, 4>(a, c, stream);
 }
 
 template <int SAVE, bool OUT_BF16>
 hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
     const FfnChoice c = gated_fwd_choice(a.M, a.K, a.NN, a.G, SAVE == kSaveMx8);
-    if (c.kernel == kFfnFewRows) {
-        if (c.rows == 16) return launch_few_mb<OUT_BF16, SAVE, 1>(a, c, stream);
-        if (c.rows == 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, c, stream);
-        return launch_few_mb<OUT_BF16, SAVE, 4>(a, c, stream);
-    }
+    if (c.kernel == kFfnFewRows) return launch_few_rows<kGated, OUT_BF16, SAVE>(a, c, stream);
     if (c.kernel == kFfnLoadWaves) return launch_ws<kGated, OUT_BF16, SAVE>(a, c.rows, stream);
     return c.cols == 256 ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream) : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
+}
+
+template <bool OUT_BF16>
+hipError_t launch_linear(const FfnArgs& a, hipStream_t stream) {
+    const FfnChoice c = linear_fwd_choice(a.M, a.K, a.NN, a.G);
+    if (c.kernel == kFfnFewRows) return launch_few_rows<kLinear, OUT_BF16, kSaveNone>(a, c, stream);
+    return c.cols == 256 ? launch<kLinear, OUT_BF16, kSaveNone, 8>(a, stream)
+                         : launch<kLinear, OUT_BF16, kSaveNone, 4>(a, stream);
 }
 
 template <int MODE>
@@ -1802,6 +1882,16 @@ FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8) {
     return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
 }
 
+FfnChoice linear_fwd_choice(int M, int K, int NN, int G) {
+    (void)K;
+    const int busy = G < M ? G : M, rows = (M + busy - 1) / busy;
+    if (rows <= kFewMaxRows && (int64_t)busy * (NN / 128) < device_cus()) {
+        const bool narrow = (int64_t)busy * (NN / 32) <= device_cus();
+        return {kFfnFewRows, narrow ? 8 : 4, rows <= 16 ? 16 : (rows <= 32 ? 32 : 64), narrow ? 32 : 64};
+    }
+    return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
+}
+
 FfnChoice ffn_dx_choice(int M, int K, int NN, int G) {
     const int cap = ws_cap(M, G, NN, (K + 255) / 256, 512, 48.0, true);
     if (cap > 0) return {kFfnLoadWaves, 12, cap, 256};
@@ -1823,6 +1913,10 @@ int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G) {
     return max_work_items(M, G < M ? G : M, 128) * ((N + 63) / 64);
 }
 
+int64_t linear_fwd_blocks(int64_t M, int64_t N, int64_t G) {
+    return max_work_items(M, G < M ? G : M, 128) * ((N + 127) / 128);
+}
+
 int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G) {
     return max_work_items(M, G < M ? G : M, 128) * ((K + 127) / 128);
 }
@@ -1833,6 +1927,10 @@ hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream)
     if (a.gu_q != nullptr) return out_bf16 ? launch_gated<kSaveMx8, true>(a, stream) : launch_gated<kSaveMx8, false>(a, stream);
     if (a.gu != nullptr) return out_bf16 ? launch_gated<kSaveBf16, true>(a, stream) : launch_gated<kSaveBf16, false>(a, stream);
     return out_bf16 ? launch_gated<kSaveNone, true>(a, stream) : launch_gated<kSaveNone, false>(a, stream);
+}
+
+hipError_t launch_linear_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream) {
+    return out_bf16 ? launch_linear<true>(a, stream) : launch_linear<false>(a, stream);
 }
 
 hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream) {

@@ -131,8 +131,12 @@ struct FfnArgs {
     uint8_t *gu_q, *gu_s;                 // the forward's P as a checkpoint, or NULL
     int ntiles_c, ntiles_r, nblocks, cap;   // set by the launcher (cap: rows of a load-wave item)
     int32_t* status;
+    // the plain product's epilogue (gmm_linear.hpp); its kept sums are gu
+    const void *bias, *residual;          // [G,NN] and [M,NN] of the output's type, or NULL
+    int bias_bf16, act;
 };
 hipError_t launch_gated_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream);
+hipError_t launch_linear_fwd(const FfnArgs& a, bool out_bf16, hipStream_t stream);
 hipError_t launch_ffn_dx(const FfnArgs& a, bool out_bf16, hipStream_t stream);
 hipError_t launch_ffn_dw(const FfnArgs& a, bool out_bf16, hipStream_t stream);
 // Both, in one launch where that pays.
@@ -144,6 +148,7 @@ struct FfnChoice {
     int kernel, waves, rows, cols;   // FfnKernel; waves of a workgroup; rows and columns of a tile
 };
 FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8);
+FfnChoice linear_fwd_choice(int M, int K, int NN, int G);
 FfnChoice ffn_dx_choice(int M, int K, int NN, int G);
 FfnChoice ffn_dw_choice(int K, int NN, int G);
 // dX's choice in a backward call for dX and dW: kFfnBoth when one launch computes both.
@@ -151,7 +156,15 @@ FfnChoice ffn_bwd_choice(int M, int K, int NN, int G);
 
 // Upper bounds of these launches' grids.
 int64_t gated_fwd_blocks(int64_t M, int64_t N, int64_t G);
+int64_t linear_fwd_blocks(int64_t M, int64_t N, int64_t G);
 int64_t ffn_dx_blocks(int64_t M, int64_t K, int64_t G);
 int64_t ffn_dw_blocks(int64_t K, int64_t NN, int64_t G);
+
+// Gradient of the plain product's epilogue: dpre = dout * act'(pre) (bf16, not
+// written where act is none: it is dout) and db [G,N], the column sums of dpre
+// in fp32.  dpre or db may be NULL; `part` holds linear_part_words(M, N, G) fp32.
+int64_t linear_part_words(int64_t M, int64_t N, int64_t G);
+hipError_t launch_linear_grad(const void* dout, const void* pre, int act, const int32_t* group_sizes, int M, int N, int G,
+                              void* dpre, void* db, bool db_bf16, float* part, int32_t* status, hipStream_t stream);
 
 }  // namespace gmm

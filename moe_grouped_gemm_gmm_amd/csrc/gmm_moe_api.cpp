@@ -50,6 +50,35 @@ gmm::MoveArgs move_args(const int32_t* row_of, const int32_t* slot_of, const flo
     return gmm::MoveArgs{row_of, slot_of, weights, T, M, (int)k, K};
 }
 
+// A launch holds fewer than 2^32 threads: workgroups of 256 in one grid.
+constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
+
+int check_grid(int64_t blocks) {
+    if (blocks > kMaxGrid) return fail(GMM_ERR_SHAPE, "grid too large");
+    return GMM_OK;
+}
+
+int check_linear(int64_t M, int64_t K, int64_t N, int64_t G, int act) {
+    GMM_TRY(check_groups(M, G));
+    GMM_TRY(check_mult(K, 64, "K"));
+    GMM_TRY(check_mult(N, 64, "N"));
+    if (act < GMM_ACT_NONE || act > GMM_ACT_GELU_TANH) return fail(GMM_ERR_DTYPE, "act %d is not a gmm_activation", act);
+    return GMM_OK;
+}
+
+gmm::FfnArgs linear_args(const int32_t* group_sizes, int64_t M, int64_t K, int64_t N, int64_t G, void* ws) {
+    gmm::FfnArgs a = {};
+    a.group_sizes = group_sizes;
+    a.M = (int)M;
+    a.K = (int)K;
+    a.NN = (int)N;
+    a.G = (int)G;
+    a.status = ws_status(ws);
+    return a;
+}
+
+const uint16_t* u16(const void* p) { return reinterpret_cast<const uint16_t*>(p); }
+
 }  // namespace
 
 extern "C" {
@@ -144,6 +173,77 @@ int gmm_combine_bwd(const void* dout, int dout_dtype, const void* y, int y_dtype
     return hip_status(gmm::launch_combine_bwd(move_args(row_of, slot_of, weights, T, k, M, K), dout,
                                               dout_dtype == GMM_BF16, y, y_dtype == GMM_BF16, dy, dweights,
                                               (hipStream_t)stream));
+}
+
+int gmm_bf16_linear(const void* lhs, const void* rhs, const int32_t* group_sizes, int64_t M, int64_t K, int64_t N,
+                    int64_t G, const void* bias, int bias_dtype, int act, const void* residual, void* out,
+                    int out_dtype, void* pre, void* ws, size_t ws_bytes, void* stream) {
+    GMM_TRY(check_out_dtype(out_dtype, "out"));
+    if (bias != nullptr) GMM_TRY(check_out_dtype(bias_dtype, "bias"));
+    GMM_TRY(check_linear(M, K, N, G, act));
+    GMM_TRY(check_rows_ptr(lhs, "lhs", M));
+    GMM_TRY(check_ptr(rhs, "rhs"));
+    GMM_TRY(check_ptr(group_sizes, "group_sizes"));
+    GMM_TRY(check_opt_ptr(bias, "bias"));
+    GMM_TRY(check_opt_ptr(residual, "residual"));
+    GMM_TRY(check_rows_ptr(out, "out", M));
+    GMM_TRY(check_opt_ptr(pre, "pre"));
+    GMM_TRY(check_grid(gmm::linear_fwd_blocks(M, N, G)));
+    GMM_TRY(check_ws(ws, ws_bytes, gmm_workspace_bytes(GMM_OP_BF16_LINEAR, M, K, N, G)));
+    if (M == 0) return GMM_OK;
+    gmm::FfnArgs a = linear_args(group_sizes, M, K, N, G, ws);
+    a.a = u16(lhs);
+    a.b = u16(rhs);
+    a.out = out;
+    a.gu = reinterpret_cast<uint16_t*>(pre);
+    a.bias = bias;
+    a.bias_bf16 = bias_dtype == GMM_BF16;
+    a.residual = residual;
+    a.act = act;
+    return hip_status(gmm::launch_linear_fwd(a, out_dtype == GMM_BF16, (hipStream_t)stream));
+}
+
+int gmm_bf16_linear_bwd(const void* dout, const void* rhs, const int32_t* group_sizes, const void* lhs,
+                        const void* pre, int act, int64_t M, int64_t K, int64_t N, int64_t G, void* dx, int dx_dtype,
+                        void* dw, int dw_dtype, void* db, int db_dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (dx != nullptr) GMM_TRY(check_out_dtype(dx_dtype, "dx"));
+    if (dw != nullptr) GMM_TRY(check_out_dtype(dw_dtype, "dw"));
+    if (db != nullptr) GMM_TRY(check_out_dtype(db_dtype, "db"));
+    GMM_TRY(check_linear(M, K, N, G, act));
+    GMM_TRY(check_rows_ptr(dout, "dout", M));
+    GMM_TRY(check_ptr(group_sizes, "group_sizes"));
+    if (act != GMM_ACT_NONE) GMM_TRY(check_rows_ptr(pre, "pre", M));
+    else GMM_TRY(check_opt_ptr(pre, "pre"));
+    if (dx != nullptr) GMM_TRY(check_ptr(rhs, "rhs"));
+    if (dw != nullptr) GMM_TRY(check_rows_ptr(lhs, "lhs", M));
+    if (dx == nullptr && dw == nullptr && db == nullptr && M > 0)
+        return fail(GMM_ERR_NULL, "dx, dw and db are all NULL");
+    GMM_TRY(check_opt_ptr(dx, "dx"));
+    GMM_TRY(check_opt_ptr(dw, "dw"));
+    GMM_TRY(check_opt_ptr(db, "db"));
+    GMM_TRY(check_grid(gmm::linear_part_words(M, N, G) / 64));
+    GMM_TRY(check_grid(gmm::ffn_dx_blocks(M, K, G)));
+    GMM_TRY(check_grid(gmm::ffn_dw_blocks(K, N, G)));
+    GMM_TRY(check_ws(ws, ws_bytes, gmm_workspace_bytes(GMM_OP_BF16_LINEAR_BWD, M, K, N, G)));
+    hipStream_t s = (hipStream_t)stream;
+    uint16_t* dpre = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsStatusBytes);
+    float* part = reinterpret_cast<float*>(dpre + M * N);
+    const bool products = dx != nullptr || dw != nullptr;
+    GMM_TRY(hip_status(gmm::launch_linear_grad(dout, pre, act, group_sizes, (int)M, (int)N, (int)G,
+                                               products ? dpre : nullptr, db, db_dtype == GMM_BF16, part, ws_status(ws), s)));
+    gmm::FfnArgs x = linear_args(group_sizes, M, K, N, G, ws), w = x;
+    x.a = act == GMM_ACT_NONE ? u16(dout) : dpre;
+    x.b = u16(rhs);
+    x.out = dx;
+    w.a = u16(lhs);
+    w.b = x.a;
+    w.out = dw;
+    const bool want_dx = dx != nullptr && M > 0;
+    if (want_dx && dw != nullptr)
+        return hip_status(gmm::launch_ffn_bwd(x, dx_dtype == GMM_BF16, w, dw_dtype == GMM_BF16, s));
+    if (want_dx) return hip_status(gmm::launch_ffn_dx(x, dx_dtype == GMM_BF16, s));
+    if (dw != nullptr) return hip_status(gmm::launch_ffn_dw(w, dw_dtype == GMM_BF16, s));
+    return GMM_OK;
 }
 
 }  // extern "C"

@@ -28,8 +28,10 @@ from . import _DT, ffn, load_library
 from .ffn import _BF16, _FLOAT, _INT32, _arg, _check, _stream
 
 OP_SORT_TOKENS, OP_BF16_LINEAR, OP_BF16_LINEAR_BWD = 32, 33, 34
-MOE_EXPORTS = ("gmm_route", "gmm_route_bwd", "gmm_sort_tokens", "gmm_dispatch", "gmm_combine", "gmm_combine_bwd")
+MOE_EXPORTS = ("gmm_route", "gmm_route_bwd", "gmm_sort_tokens", "gmm_dispatch", "gmm_combine", "gmm_combine_bwd",
+               "gmm_bf16_linear", "gmm_bf16_linear_bwd")
 SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 MAX_TOPK = 64
 
 _F32 = (torch.float32,)
@@ -181,6 +183,74 @@ def gmm_combine_bwd(dout: torch.Tensor, y: Optional[torch.Tensor], row_of: torch
     return dy, dweights
 
 
+def gmm_bf16_linear(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, activation: str = "none",
+                    residual: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                    out: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Grouped product with its epilogue: with pre = lhs [M,K] . rhs[g] [K,N] +
+    bias[g] per group, activation(pre) + residual, [M,N].  bias [G,N] bf16 or
+    fp32; activation "none", "relu", "silu", "gelu" or "gelu_tanh"; residual
+    [M,N] of the output's type (it may be out itself).  pre [M,N] bf16, if given,
+    receives pre for the backward pass."""
+    lib = load_library()
+    dev = lhs.device
+    M, K = lhs.shape
+    G, K2, N = rhs.shape
+    if K2 != K:
+        raise ValueError("lhs K=%d but rhs K=%d" % (K, K2))
+    act = _named(activation, ACTIVATIONS, "activation")
+    args = (_arg(lhs, None, _BF16, "lhs", dev), _arg(rhs, None, _BF16, "rhs", dev),
+            _arg(group_sizes, (G,), _INT32, "group_sizes", dev), M, K, N, G, _arg(bias, (G, N), _FLOAT, "bias", dev),
+            0 if bias is None else _DT[bias.dtype], act)
+    pp = _arg(pre, (M, N), _BF16, "pre", dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _check(lib, lib.gmm_bf16_linear(*args, _arg(residual, (M, N), (out.dtype,), "residual", dev),
+                                    _arg(out, (M, N), _FLOAT, "out", dev), _DT[out.dtype], pp, *ffn._status(ws, dev),
+                                    _stream(dev)))
+    return out
+
+
+def gmm_bf16_linear_bwd(dout: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Tensor,
+                        lhs: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+                        activation: str = "none", dx_dtype: torch.dtype = torch.bfloat16,
+                        dw_dtype: torch.dtype = torch.bfloat16, db_dtype: torch.dtype = torch.float32,
+                        dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                        db: Optional[torch.Tensor] = None, want_dx: bool = True, want_dw: bool = True,
+                        want_db: bool = True, ws: Optional[torch.Tensor] = None
+                        ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Backward of gmm_bf16_linear: (dx [M,K], dw [G,K,N], db [G,N]) from dout
+    [M,N] bf16, the layer's input lhs (for dw) and, unless activation is "none",
+    the kept pre.  want_dx / want_dw / want_db False leaves that gradient out
+    (None).  The residual's gradient is dout.  ws, if given
+    (workspace(OP_BF16_LINEAR_BWD, ...)), is used until the call's kernels have
+    finished: a call that may run at the same time on another stream needs
+    another one."""
+    lib = load_library()
+    dev = dout.device
+    M, N = dout.shape
+    G, K, N2 = rhs.shape
+    if N2 != N:
+        raise ValueError("dout N=%d but rhs N=%d" % (N, N2))
+    args = (_arg(dout, None, _BF16, "dout", dev), _arg(rhs, None, _BF16, "rhs", dev),
+            _arg(group_sizes, (G,), _INT32, "group_sizes", dev), _arg(lhs, (M, K), _BF16, "lhs", dev),
+            _arg(pre, (M, N), _BF16, "pre", dev), _named(activation, ACTIVATIONS, "activation"), M, K, N, G)
+    if dx is None and want_dx:
+        dx = torch.empty((M, K), dtype=dx_dtype, device=dev)
+    if dw is None and want_dw:
+        dw = torch.empty((G, K, N), dtype=dw_dtype, device=dev)
+    if db is None and want_db:
+        db = torch.empty((G, N), dtype=db_dtype, device=dev)
+    if ws is None:
+        ws = torch.empty(max(lib.gmm_workspace_bytes(OP_BF16_LINEAR_BWD, M, K, N, G), 16), dtype=torch.uint8, device=dev)
+    _check(lib, lib.gmm_bf16_linear_bwd(
+        *args, _arg(dx, (M, K), _FLOAT, "dx", dev), 0 if dx is None else _DT[dx.dtype],
+        _arg(dw, (G, K, N), _FLOAT, "dw", dev), 0 if dw is None else _DT[dw.dtype],
+        _arg(db, (G, N), _FLOAT, "db", dev), 0 if db is None else _DT[db.dtype], *ffn._status(ws, dev), _stream(dev)))
+    return dx, dw, db
+
+
 def _declare(lib) -> None:
     """ctypes signatures of this header's calls."""
     P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -190,5 +260,7 @@ def _declare(lib) -> None:
     lib.gmm_dispatch.argtypes = [P, I, P, P, I64, I64, I64, I64, P, P]
     lib.gmm_combine.argtypes = [P, I, P, P, P, I64, I64, I64, I64, P, I, P]
     lib.gmm_combine_bwd.argtypes = [P, I, P, I, P, P, P, I64, I64, I64, I64, P, P, P]
+    lib.gmm_bf16_linear.argtypes = [P, P, P, I64, I64, I64, I64, P, I, I, P, P, I, P, P, SZ, P]
+    lib.gmm_bf16_linear_bwd.argtypes = [P, P, P, P, P, I, I64, I64, I64, I64, P, I, P, I, P, I, P, SZ, P]
     for name in MOE_EXPORTS:
         getattr(lib, name).restype = I

@@ -132,7 +132,7 @@ def combine_bwd(dout, y, row_of, weights, M):
     return dy, dw, mag
 
 
-_erf = np.vectorize(math.erf)
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def act(name, z):
@@ -142,7 +142,7 @@ def act(name, z):
         if name == "relu":
             return np.maximum(z, 0), (z > 0).astype(np.float64)
         if name == "gelu":
-            cdf = 0.5 * (1 + _erf(z / math.sqrt(2))) if z.size else z
+            cdf = 0.5 * _erfc(-z / math.sqrt(2))
             return z * cdf, cdf + z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
         if name == "silu":
             u, du = z, 1.0
