@@ -99,7 +99,8 @@ GMM_API int gmm_route_bwd(const float *dweights, const void *logits, int logits_
  * row_of [T,k]: the slot's row, or -1.
  * slot_of [M]: the row's slot, or -1 behind the last one.
  * ws: gmm_workspace_bytes(GMM_OP_SORT_TOKENS, T k, 0, 0, G) bytes: the status
- *   block and counts; a call needs one of its own until it has finished.
+ *   block, and counts unless there are few slots and experts; with more than
+ *   256 bytes a call needs a workspace of its own until it has finished.
  * The result does not depend on the order in which anything runs.
  */
 GMM_API int gmm_sort_tokens(const int32_t *ids, int64_t T, int64_t k, int64_t first, int64_t G,

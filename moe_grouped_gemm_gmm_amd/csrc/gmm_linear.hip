@@ -15,7 +15,7 @@ namespace gmm {
 namespace {
 
 constexpr int kItemRows = 32;
-constexpr int kStripLanes = 64;   // lanes across a strip at most: 512 columns
+constexpr int kStripLanes = 16;   // lanes across a strip at most: 128 columns
 
 struct GradArgs {
     const uint16_t *dout, *pre;

@@ -3,16 +3,19 @@
 // W lanes of a wave take one token's logits, V consecutive experts a lane, so
 // the order of (lane, place in the lane) is the order of the experts: of
 // several equal keys the lowest lane's first one is the lowest index.  k
-// rounds each find the largest key left: V - 1 maxima in the lane, log2 W lane
-// moves, a ballot for the lowest lane that holds it.  Choice j stays in lane j
-// (k <= W always), where the weights are made.
+// rounds each find the largest key left: V / 2 three-way maxima in the lane,
+// log2 W lane moves, a ballot for the lowest lane that holds it.  Choice j
+// stays in lane j (k <= W always), where the weights are made.
 //
-// Keys are compared as integers in the order of the numbers they stand for,
-// 0 for an expert that is off or already taken.  Without a bias a key is the
-// logit itself (the scores are monotonic in it), exact.  With a bias it is
-// score + bias in 64 bits: scores that differ in the last bits of 32 would
-// change places with every change of the arithmetic.  The weights and their
-// gradient are in 32 bits.
+// Without a bias a key is the logit itself (the scores are monotonic in it),
+// exact.  With a bias it is score + bias in 64 bits: scores that differ in the
+// last bits of 32 would change places with every change of the arithmetic.
+// Such keys are first compared in 32 bits; only where two that follow each
+// other among the k + 1 largest are closer than twice their error is the
+// wave's choice made again in 64.  The weights and their gradient are in 32 bits.
+//
+// What bounds it: instructions, not memory.  At 65536 tokens of 256 experts, k
+// = 8, the forward reads 67 MB (14 us at a copy's 5 TB/s).
 #include "gmm_launch.hpp"
 #include "gmm_moe.hpp"
 #include "gmm_mx8.hpp"
@@ -50,17 +53,31 @@ __device__ __forceinline__ float sum_lanes(float x) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
+// Maxima of numbers (no NaN gets here).  In asm: fmaxf also has to quieten
+// signalling NaNs, an instruction more for each operand of unknown origin.
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
 template <int W>
 __device__ __forceinline__ float max_lanes(float x) {
     return __uint_as_float(over_lanes<W>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+        return __float_as_uint(max2(__uint_as_float(a), __uint_as_float(b)));
     }));
 }
-template <int W>
-__device__ __forceinline__ uint32_t max_key(uint32_t x) {
-    return over_lanes<W>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+template <int V>
+__device__ __forceinline__ float max_of(const float (&x)[V]) {
+    float m = x[0];
+#pragma unroll
+    for (int v = 1; v + 1 < V; v += 2) m = max3(m, x[v], x[v + 1]);
+    return V % 2 == 0 ? max2(m, x[V - 1]) : m;
 }
-
 // One exchange of 64-bit values between the lanes of a group: step s of log2 W.
 template <int S>
 __device__ __forceinline__ uint64_t exchange(uint64_t x) {
@@ -81,8 +98,15 @@ __device__ __forceinline__ uint64_t over_lanes64(uint64_t x, Op op) {
     return x;
 }
 template <int W>
-__device__ __forceinline__ uint64_t max_key(uint64_t x) {
+__device__ __forceinline__ uint64_t max_lanes(uint64_t x) {
     return over_lanes64<W>(x, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+}
+template <int V>
+__device__ __forceinline__ uint64_t max_of(const uint64_t (&x)[V]) {
+    uint64_t m = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = x[v] > m ? x[v] : m;
+    return m;
 }
 template <int W>
 __device__ __forceinline__ double sum_lanes(double x) {
@@ -91,22 +115,37 @@ __device__ __forceinline__ double sum_lanes(double x) {
     }));
 }
 
-// Integers in the order of the floating-point numbers; NaN is not given here.
-__device__ __forceinline__ uint32_t ordered(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float from_ordered(uint32_t u) {
-    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-}
+// An integer in the order of the floating-point numbers; NaN is not given here.
 __device__ __forceinline__ uint64_t ordered(double f) {
     const uint64_t u = (uint64_t)__double_as_longlong(f);
     return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
 }
 
-// A logit as the router takes it: kOff where the expert is off, +infinity as
-// the largest number, one zero.
-__device__ __forceinline__ float clean(float l) { return l > kOff ? fminf(l, FLT_MAX) + 0.0f : kOff; }
+// What a key that is off, or taken already, reads as.
+template <typename Key>
+__device__ __forceinline__ Key no_key();
+template <>
+__device__ __forceinline__ float no_key<float>() { return kOff; }
+template <>
+__device__ __forceinline__ uint64_t no_key<uint64_t>() { return 0; }
+
+// A lane's key as a scalar, and equality of scalars' bits (keys have one zero).
+__device__ __forceinline__ uint32_t lane_bits(uint32_t k, int lane) { return (uint32_t)lane_value((int)k, lane); }
+__device__ __forceinline__ uint32_t lane_bits(float k, int lane) { return lane_bits(__float_as_uint(k), lane); }
+__device__ __forceinline__ uint64_t lane_bits(uint64_t k, int lane) {
+    return (uint64_t)lane_bits((uint32_t)(k >> 32), lane) << 32 | lane_bits((uint32_t)k, lane);
+}
+
+// A logit as the router takes it: kOff where the expert is off (-infinity or
+// any NaN), +infinity as the largest number, one zero.
+__device__ __forceinline__ float clean(float l) {
+    return l > kOff ? __builtin_amdgcn_fmed3f(l, -FLT_MAX, FLT_MAX) + 0.0f : kOff;
+}
+
+// exp by the hardware's 2^x: the product's rounding moves it by |x| 2^-24 of
+// itself, as much as the rounding of the difference x that it is given; results
+// below the smallest normal number are 0.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 template <bool BF16>
 __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
@@ -114,18 +153,17 @@ __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
     else return reinterpret_cast<const float*>(p)[i];
 }
 
-// Experts e0 .. e0 + V - 1 of the row that starts at element `row`, kOff from E
-// on.  `vec`: E is a multiple of 4, so groups of four are aligned.
+// Values e0 .. e0 + V - 1 of the row of E that starts at element `row`, kOff from
+// E on.  `vec`: E is a multiple of 4, so groups of four are aligned.
 template <int V, bool BF16>
-__device__ __forceinline__ void load_logits(const void* p, int64_t row, int e0, int E, bool vec, float (&l)[V]) {
-    if (V >= 4 && vec) {
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int e0, int E, bool vec, float (&l)[V]) {
+    if constexpr (V >= 4) {
+        if (vec) {
 #pragma unroll
-        for (int v = 0; v < V; v += 4) {
-            if (e0 + v >= E) {
-#pragma unroll
-                for (int i = 0; i < 4 && v + i < V; ++i) l[v + i] = kOff;
-            } else if constexpr (V >= 4) {
-                if constexpr (BF16) {
+            for (int v = 0; v < V; v += 4) {
+                if (e0 + v >= E) {
+                    l[v] = l[v + 1] = l[v + 2] = l[v + 3] = kOff;
+                } else if constexpr (BF16) {
                     const uint2 d = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + row + e0 + v);
                     l[v] = bf16_lo(d.x);
                     l[v + 1] = bf16_hi(d.x);
@@ -139,27 +177,30 @@ __device__ __forceinline__ void load_logits(const void* p, int64_t row, int e0, 
                     l[v + 3] = d.w;
                 }
             }
+            return;
         }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? logit_at<BF16>(p, row + e0 + v) : kOff;
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? logit_at<BF16>(p, row + e0 + v) : kOff;
+}
+template <int V, bool BF16>
+__device__ __forceinline__ void load_logits(const void* p, int64_t row, int e0, int E, bool vec, float (&l)[V]) {
+    load_row<V, BF16>(p, row, e0, E, vec, l);
 #pragma unroll
     for (int v = 0; v < V; ++v) l[v] = clean(l[v]);
 }
 
-// Maximum (0 where every expert is off) and 1 / sum of exp(l - maximum) (0 there)
-// of a token.
+// exp(l - maximum) of a token's logits and 1 / their sum (0 where every expert is off).
 template <int W, int V>
-__device__ __forceinline__ void softmax_of(const float (&l)[V], float& top, float& inv) {
-    float m = l[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-    m = max_lanes<W>(m);
+__device__ __forceinline__ void softmax_of(const float (&l)[V], float (&e)[V], float& top, float& inv) {
+    const float m = max_lanes<W>(max_of<V>(l));
     top = m > kOff ? m : 0.0f;
     float s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) s += expf(l[v] - top);
+    for (int v = 0; v < V; ++v) {
+        e[v] = exp_of(l[v] - top);
+        s += e[v];
+    }
     s = sum_lanes<W>(s);
     inv = s > 0.0f ? 1.0f / s : 0.0f;
 }
@@ -174,101 +215,141 @@ __device__ __forceinline__ float chosen_share(float l, bool sigmoid_score) {
     const float top = max_lanes<W>(l), m = top > kOff ? top : 0.0f;
     float s;
     if (sigmoid_score) s = l >= 0.0f ? sigmoid(l) : expf(l - fminf(m, 0.0f)) / (1.0f + expf(l));
-    else s = expf(l - m);
+    else s = exp_of(l - m);
     const float sum = sum_lanes<W>(s);
     return sum > 0.0f ? s / sum : 0.0f;
 }
 
+// k rounds: the j-th largest key's expert and the key in lane j of the token's
+// W (-1 and no_key where none is left); returns the key of round k (`more`) or
+// no_key.  key is used up.
+template <int W, int V, typename Key>
+__device__ __forceinline__ Key choose(Key (&key)[V], int k, bool more, int& my_id, Key& my_key) {
+    const int lane = lane_id(), sub = lane % W;
+    const Key none = no_key<Key>();
+    my_id = -1;
+    my_key = none;
+    for (int j = 0; j < k; ++j) {
+        const Key best = max_of<V>(key), m = max_lanes<W>(best);
+        const unsigned long long held = __ballot(best == m);
+        int id = -1;
+        if constexpr (W == 64) {   // one token a wave: where the key is, and its removal, are scalar
+            if (lane_bits(m, 0) == lane_bits(none, 0)) return none;
+            const int owner = __ffsll((long long)held) - 1;
+            bool found = false;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (found || lane_bits(key[v], owner) != lane_bits(m, 0)) continue;
+                found = true;
+                id = owner * V + v;
+                key[v] = lane == owner ? none : key[v];
+            }
+        } else {
+            static_assert(W <= 16, "a token's lanes are in one half of the ballot");
+            const uint32_t half = lane < 32 ? (uint32_t)held : (uint32_t)(held >> 32);
+            const int owner = __ffs((int)(half >> (lane & 31 & ~(W - 1)) & ((1u << W) - 1u))) - 1;
+            int at = 0;
+            bool open = sub == owner;   // the first of the owner's equal keys
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool hit = open && key[v] == m;
+                at = hit ? v : at;
+                key[v] = hit ? none : key[v];
+                open = open && !hit;
+            }
+            if constexpr (V == 1) {
+                id = owner;
+            } else {
+                id = owner * V + __shfl(at, (lane & ~(W - 1)) + owner, 64);
+            }
+            if (m == none) id = -1;
+        }
+        my_id = sub == j ? id : my_id;
+        my_key = sub == j ? m : my_key;
+    }
+    return more ? max_lanes<W>(max_of<V>(key)) : none;
+}
+
+// The choice of token t by keys in 64 bits, 64 lanes of VX experts; choice j in
+// lane j.  top: the token's largest logit.
+template <int VX, bool BF16>
+__device__ __forceinline__ int exact_choice(const RouteArgs& a, int64_t t, float top) {
+    const int lane = lane_id(), E = a.E;
+    uint64_t key[VX];
+    double s[VX], sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < VX; ++v) {
+        const int e = lane * VX + v;
+        const float l = e < E ? clean(logit_at<BF16>(a.logits, t * E + e)) : kOff;
+        s[v] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : (l > kOff ? exp((double)l - (double)top) : 0.0);
+        key[v] = l > kOff;
+        sum += s[v];
+    }
+    sum = a.sigmoid ? 1.0 : sum_lanes<64>(sum);
+#pragma unroll
+    for (int v = 0; v < VX; ++v) {
+        const double z = s[v] / sum + (double)a.bias[min(lane * VX + v, E - 1)];
+        key[v] = key[v] != 0 && z > (double)kOff ? ordered(z + 0.0) : 0;
+    }
+    int id;
+    uint64_t unused;
+    choose<64, VX, uint64_t>(key, a.k, false, id, unused);
+    return id;
+}
+
 template <int W, int V, bool BF16, bool BIAS>
-__global__ __launch_bounds__(256) void route_kernel(const RouteArgs a, int32_t* __restrict__ ids,
+__global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kernel(const RouteArgs a, int32_t* __restrict__ ids,
                                                     float* __restrict__ weights) {
-    using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
     const int lane = lane_id(), sub = lane % W, E = a.E, k = a.k;
     const bool vec = E % 4 == 0;
     const int64_t stride = (int64_t)gridDim.x * (256 / W);
     // whole waves stay together: the last tokens' lanes without one repeat the last
     for (int64_t t0 = (int64_t)blockIdx.x * (256 / W) + (threadIdx.x / 64) * (64 / W); t0 < a.T; t0 += stride) {
         const int64_t t = min(t0 + lane / W, a.T - 1);
-        float l[V];
+        float l[V], s[V], top = 0.0f, inv = 0.0f;
         load_logits<V, BF16>(a.logits, t * E, sub * V, E, vec, l);
-        float top = 0.0f, inv = 0.0f;
-        if (!a.sigmoid && !a.normalize) softmax_of<W, V>(l, top, inv);
-        Key key[V];
-        if constexpr (BIAS) {
-            double s[V];
-            if (a.sigmoid) {
+        if (!a.sigmoid && (BIAS || !a.normalize)) softmax_of<W, V>(l, s, top, inv);
+        int my_id;
+        float my_l;
+        if constexpr (!BIAS) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) s[v] = 1.0 / (1.0 + exp(-(double)l[v]));
-            } else {
-                float m = l[0];
-#pragma unroll
-                for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-                m = max_lanes<W>(m);
-                double sum = 0.0;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s[v] = l[v] > kOff ? exp((double)l[v] - (double)m) : 0.0;
-                    sum += s[v];
-                }
-                sum = sum_lanes<W>(sum);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s[v] /= sum;
-            }
+            for (int v = 0; v < V; ++v) s[v] = l[v];
+            choose<W, V, float>(s, k, false, my_id, my_l);
+        } else {
+            float b[V];
+            load_row<V, false>(a.bias, 0, sub * V, E, vec, b);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int e = sub * V + v;
-                const double b = e < E ? s[v] + (double)a.bias[e] : 0.0;
-                key[v] = l[v] > kOff && b > (double)kOff ? ordered(b + 0.0) : 0;
+                const float x = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_of(-l[v])) : s[v] * inv;
+                const float z = x + b[v] + 0.0f;
+                s[v] = l[v] > kOff && z > kOff ? z : kOff;
             }
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) key[v] = l[v] > kOff ? ordered(l[v]) : 0;
-        }
-        int my_id = -1;
-        float my_l = kOff;
-        for (int j = 0; j < k; ++j) {
-            Key best = key[0];
-#pragma unroll
-            for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
-            const Key m = max_key<W>(best);
-            const unsigned long long held = __ballot(best == m);
-            int id, owner;
-            if constexpr (W == 64) {
-                owner = __ffsll((long long)held) - 1;
-            } else {
-                owner = __ffsll((long long)(held >> (lane - sub) & ((1ull << W) - 1ull))) - 1;
+            float my_key;
+            const float next = choose<W, V, float>(s, k, true, my_id, my_key);
+            // Twice the error of a key.  A sigmoid is off by less than 4 u of it (u = 2^-24: its exponential by (2 |l|
+            // + 2) u, of which s (1 - s) counts, the sum and the reciprocal); a softmax, d below the top, by (2 d + 80)
+            // u of it (the differences and products of d, a sum of at most 70 roundings), so by less than 2^-17 of
+            // the top's score, which is inv; score + bias by half a step.
+            const float after_lane = __shfl(my_key, (lane & ~(W - 1)) | ((sub + 1) & (W - 1)), 64);
+            const float after = sub + 1 < k ? after_lane : next;
+            const float tol = (a.sigmoid ? 0x1p-20f : 0x1p-16f * inv) + 0x1p-23f * (fabsf(my_key) + fabsf(after));
+            const bool close = sub < k && my_id >= 0 && after > kOff && !(my_key - after > tol);
+            constexpr unsigned long long kGroup = W == 64 ? ~0ull : (1ull << (W % 64)) - 1ull;
+            unsigned long long open = __ballot(close);
+            while (open != 0) {   // one token after the other, by the whole wave
+                const int base = (__ffsll((long long)open) - 1) & ~(W - 1);
+                open &= ~(kGroup << base);
+                const int id = exact_choice<(W * V + 63) / 64, BF16>(
+                    a, min(t0 + base / W, a.T - 1), __int_as_float(lane_value(__float_as_int(top), base)));
+                const int mine = __shfl(id, sub, 64);
+                my_id = (lane & ~(W - 1)) == base ? mine : my_id;
             }
-            int at = 0;
-            float lv = l[0];
-#pragma unroll
-            for (int v = V - 1; v >= 0; --v)
-                if (key[v] == m) {
-                    at = v;
-                    lv = l[v];
-                }
-            if constexpr (V > 1) {   // W == 64: the owner is the wave's
-                id = owner * V + lane_value(at, owner);
-            } else {
-                id = owner;
-            }
-            float lj;
-            if constexpr (!BIAS) lj = from_ordered((uint32_t)m);
-            else if constexpr (W == 64) lj = __int_as_float(lane_value(__float_as_int(lv), owner));
-            else lj = __shfl(lv, lane - sub + owner, 64);
-            if (sub == j && m != 0) {
-                my_id = id;
-                my_l = lj;
-            }
-            if (sub == owner) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (V == 1 || v == at) key[v] = 0;
-            }
+            my_l = my_id >= 0 ? clean(logit_at<BF16>(a.logits, t * E + my_id)) : kOff;
         }
         float w;
         if (a.normalize) w = chosen_share<W>(my_l, a.sigmoid);
         else if (a.sigmoid) w = sigmoid(my_l);
-        else w = expf(my_l - top) * inv;
+        else w = exp_of(my_l - top) * inv;
         if (sub < k && t0 + lane / W < a.T) {
             ids[t * k + sub] = my_id;
             weights[t * k + sub] = my_id >= 0 ? a.scale * w : 0.0f;
@@ -297,11 +378,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
         // what choice j adds at its expert: its part of the gradient itself, or
         // (dense) its weight's gradient
         const bool dense = !a.sigmoid && !a.normalize;
-        float g = dw, dot = 0.0f, l[V], top = 0.0f, inv = 0.0f;
+        float g = dw, dot = 0.0f, s[V], inv = 0.0f;
         if (dense) {
+            float l[V], top;
             load_logits<V, BF16>(a.logits, t * E, sub * V, E, vec, l);
-            softmax_of<W, V>(l, top, inv);
-            dot = sum_lanes<W>(on ? expf(lj - top) * inv * dw : 0.0f);
+            softmax_of<W, V>(l, s, top, inv);
+            dot = sum_lanes<W>(on ? exp_of(lj - top) * inv * dw : 0.0f);
         } else if (a.normalize) {
             const float q = chosen_share<W>(lj, a.sigmoid);
             g = a.scale * q * (dw - sum_lanes<W>(q * dw));
@@ -313,22 +395,23 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = 0.0f;
         for (int j = 0; j < k; ++j) {
-            int e;
-            float gj;
             if constexpr (W == 64) {
-                e = lane_value(id, j);
-                gj = __int_as_float(lane_value(__float_as_int(g), j));
-            } else {
-                e = __shfl(id, lane - sub + j, 64);
-                gj = __shfl(g, lane - sub + j, 64);
-            }
+                const int e = lane_value(id, j);
+                if (e < 0) continue;
+                const float gj = lane == e / V ? __int_as_float(lane_value(__float_as_int(g), j)) : 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (e == sub * V + v) d[v] += gj;
+                for (int v = 0; v < V; ++v)
+                    if (e % V == v) d[v] += gj;   // a scalar condition
+            } else {
+                const int e = __shfl(id, lane - sub + j, 64);
+                const float gj = __shfl(g, lane - sub + j, 64);
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] += e == sub * V + v ? gj : 0.0f;
+            }
         }
         if (dense) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) d[v] = a.scale * (expf(l[v] - top) * inv) * (d[v] - dot);
+            for (int v = 0; v < V; ++v) d[v] = a.scale * (s[v] * inv) * (d[v] - dot);
         }
         if (!mine) continue;
         const int64_t o = t * E + sub * V;
@@ -354,18 +437,23 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
     }
 }
 
-// Lanes and experts a lane for E experts.
+// Lanes and experts a lane for E experts.  16 lanes a token (four tokens a
+// wave) share the lane moves and ballots of a round between four tokens; 64
+// give the shortest rounds and the most waves.
 template <typename F>
-hipError_t with_lanes(int E, F f) {
+hipError_t with_lanes(int E, int k, bool many, F f) {
     using std::integral_constant;
-    if (E <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    if (E <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-    if (E <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    if (E <= 64) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    if (E <= 256) return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-    if (E <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
-    return f(integral_constant<int, 64>{}, integral_constant<int, 64>{});
+    constexpr integral_constant<int, 16> w16;
+    constexpr integral_constant<int, 64> w64;
+    if (E <= 16) return f(w16, integral_constant<int, 1>{});
+    if (E <= 64) return k <= 16 ? f(w16, integral_constant<int, 4>{}) : f(w64, integral_constant<int, 1>{});
+    if (E <= 256) return k <= 16 && many ? f(w16, integral_constant<int, 16>{}) : f(w64, integral_constant<int, 4>{});
+    if (E <= 512) return f(w64, integral_constant<int, 8>{});
+    if (E <= 1024) return f(w64, integral_constant<int, 16>{});
+    return f(w64, integral_constant<int, 64>{});
 }
+
+constexpr int64_t kManyTokens = 8192;
 
 dim3 token_grid(int64_t T, int W) {
     const int64_t blocks = (T + 256 / W - 1) / (256 / W);
@@ -375,7 +463,7 @@ dim3 token_grid(int64_t T, int W) {
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, bool logits_bf16, int32_t* ids, float* weights, hipStream_t stream) {
-    return with_lanes(a.E, [&](auto w, auto v) {
+    return with_lanes(a.E, a.k, a.T >= kManyTokens, [&](auto w, auto v) {
         constexpr int W = decltype(w)::value, V = decltype(v)::value;
         const dim3 grid = token_grid(a.T, W), block(256);
         if (a.bias != nullptr) {
@@ -391,7 +479,7 @@ hipError_t launch_route(const RouteArgs& a, bool logits_bf16, int32_t* ids, floa
 
 hipError_t launch_route_bwd(const RouteArgs& a, bool logits_bf16, const float* dweights, const int32_t* ids,
                             void* dlogits, bool out_bf16, hipStream_t stream) {
-    return with_lanes(a.E, [&](auto w, auto v) {
+    return with_lanes(a.E, a.k, false, [&](auto w, auto v) {
         constexpr int W = decltype(w)::value, V = decltype(v)::value;
         const dim3 grid = token_grid(a.T, W), block(256);
         if (logits_bf16) {

@@ -20,6 +20,7 @@ and backward:
     dlogits = gmm_route_bwd(dweights, logits, ids)
 """
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -35,6 +36,34 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 MAX_TOPK = 64
 
 _F32 = (torch.float32,)
+
+
+# A serving step's calls take a few microseconds on the device: outputs made
+# here are not checked, and sizes of workspaces are asked for once.
+
+def _out(t: Optional[torch.Tensor], shape, dtype: torch.dtype, dtypes: tuple, name: str, dev: torch.device):
+    """(t, its address), t allocated unless given."""
+    if t is None:
+        if dtype not in dtypes:
+            raise TypeError("%s has dtype %s" % (name, dtype))
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _arg(t, shape, dtypes, name, dev)
+
+
+@functools.lru_cache(maxsize=512)
+def _ws_bytes(op: int, M: int, K: int, N: int, G: int) -> int:
+    return int(load_library().gmm_workspace_bytes(op, M, K, N, G))
+
+
+def _work(ws: Optional[torch.Tensor], dev: torch.device, op: int, M: int, K: int, N: int, G: int):
+    """(ws, its address, its bytes), ws allocated unless given or only the status block."""
+    if ws is None:
+        need = _ws_bytes(op, M, K, N, G)
+        if need > 256:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            return ws, ws.data_ptr(), need
+    return (ws,) + ffn._status(ws, dev)
 
 
 def _named(value: str, table: dict, what: str) -> int:
@@ -56,13 +85,10 @@ def gmm_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
     dev = logits.device
     T, E = logits.shape
     lp, bp = _arg(logits, None, _FLOAT, "logits", dev), _arg(bias, (E,), _F32, "bias", dev)
-    if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _check(lib, lib.gmm_route(lp, _DT[logits.dtype], bp, T, E, k, _named(score, SCORES, "score"), int(normalize), scale,
-                              _arg(ids, (T, k), _INT32, "ids", dev), _arg(weights, (T, k), _F32, "weights", dev),
-                              _stream(dev)))
+    kind = _named(score, SCORES, "score")
+    ids, ip = _out(ids, (T, k), torch.int32, _INT32, "ids", dev)
+    weights, wp = _out(weights, (T, k), torch.float32, _F32, "weights", dev)
+    _check(lib, lib.gmm_route(lp, _DT[logits.dtype], bp, T, E, k, kind, int(normalize), scale, ip, wp, _stream(dev)))
     return ids, weights
 
 
@@ -81,9 +107,8 @@ def gmm_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tenso
     args = (_arg(dweights, (T, k), _F32, "dweights", dev), _arg(logits, None, _FLOAT, "logits", dev),
             _DT[logits.dtype], _arg(ids, None, _INT32, "ids", dev), T, E, k, _named(score, SCORES, "score"),
             int(normalize), scale)
-    if out is None:
-        out = torch.empty((T, E), dtype=out_dtype or logits.dtype, device=dev)
-    _check(lib, lib.gmm_route_bwd(*args, _arg(out, (T, E), _FLOAT, "out", dev), _DT[out.dtype], _stream(dev)))
+    out, op = _out(out, (T, E), out_dtype or logits.dtype, _FLOAT, "out", dev)
+    _check(lib, lib.gmm_route_bwd(*args, op, _DT[out.dtype], _stream(dev)))
     return out
 
 
@@ -101,18 +126,11 @@ def gmm_sort_tokens(ids: torch.Tensor, G: int, first: int = 0, rows: Optional[in
     T, k = ids.shape
     M = T * k if rows is None else rows
     ip = _arg(ids, None, _INT32, "ids", dev)
-    if group_sizes is None:
-        group_sizes = torch.empty(G, dtype=torch.int32, device=dev)
-    if row_of is None:
-        row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if slot_of is None:
-        slot_of = torch.empty(max(M, 0), dtype=torch.int32, device=dev)
-    if ws is None:
-        ws = torch.empty(max(lib.gmm_workspace_bytes(OP_SORT_TOKENS, T * k, 0, 0, G), 16), dtype=torch.uint8, device=dev)
-    _check(lib, lib.gmm_sort_tokens(ip, T, k, first, G, M, _arg(group_sizes, (G,), _INT32, "group_sizes", dev),
-                                    _arg(row_of, (T, k), _INT32, "row_of", dev),
-                                    _arg(slot_of, (max(M, 0),), _INT32, "slot_of", dev), *ffn._status(ws, dev),
-                                    _stream(dev)))
+    group_sizes, gp = _out(group_sizes, (max(G, 0),), torch.int32, _INT32, "group_sizes", dev)
+    row_of, rp = _out(row_of, (T, k), torch.int32, _INT32, "row_of", dev)
+    slot_of, sp = _out(slot_of, (max(M, 0),), torch.int32, _INT32, "slot_of", dev)
+    ws, wp, wb = _work(ws, dev, OP_SORT_TOKENS, T * k, 0, 0, G)
+    _check(lib, lib.gmm_sort_tokens(ip, T, k, first, G, M, gp, rp, sp, wp, wb, _stream(dev)))
     return group_sizes, row_of, slot_of
 
 
@@ -129,9 +147,8 @@ def gmm_dispatch(x: torch.Tensor, row_of: torch.Tensor, slot_of: torch.Tensor, o
     M = slot_of.numel()
     args = (_arg(x, None, _FLOAT, "x", dev), _DT[x.dtype], _arg(row_of, None, _INT32, "row_of", dev),
             _arg(slot_of, (M,), _INT32, "slot_of", dev), T, k, M, K)
-    if out is None:
-        out = torch.empty((M, K), dtype=x.dtype, device=dev)
-    _check(lib, lib.gmm_dispatch(*args, _arg(out, (M, K), (x.dtype,), "out", dev), _stream(dev)))
+    out, op = _out(out, (M, K), x.dtype, (x.dtype,), "out", dev)
+    _check(lib, lib.gmm_dispatch(*args, op, _stream(dev)))
     return out
 
 
@@ -145,12 +162,11 @@ def gmm_combine(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[torch.T
     dev = y.device
     M, K = y.shape
     T, k = row_of.shape
-    if out is None:
-        out = torch.empty((T, K), dtype=out_dtype or y.dtype, device=dev)
-    _check(lib, lib.gmm_combine(_arg(y, None, _FLOAT, "y", dev), _DT[y.dtype], _arg(row_of, None, _INT32, "row_of", dev),
-                                _arg(weights, (T, k), _F32, "weights", dev),
-                                _arg(residual, (T, K), (out.dtype,), "residual", dev), T, k, M, K,
-                                _arg(out, (T, K), _FLOAT, "out", dev), _DT[out.dtype], _stream(dev)))
+    args = (_arg(y, None, _FLOAT, "y", dev), _DT[y.dtype], _arg(row_of, None, _INT32, "row_of", dev),
+            _arg(weights, (T, k), _F32, "weights", dev))
+    out, op = _out(out, (T, K), out_dtype or y.dtype, _FLOAT, "out", dev)
+    _check(lib, lib.gmm_combine(*args, _arg(residual, (T, K), (out.dtype,), "residual", dev), T, k, M, K, op,
+                                _DT[out.dtype], _stream(dev)))
     return out
 
 
@@ -174,12 +190,12 @@ def gmm_combine_bwd(dout: torch.Tensor, y: Optional[torch.Tensor], row_of: torch
     args = (_arg(dout, None, _FLOAT, "dout", dev), _DT[dout.dtype], _arg(y, (M, K), _FLOAT, "y", dev), _DT.get(dt, -1),
             _arg(row_of, None, _INT32, "row_of", dev), _arg(slot_of, (M,), _INT32, "slot_of", dev),
             _arg(weights, (T, k), _F32, "weights", dev), T, k, M, K)
-    if dy is None and want_dy:
-        dy = torch.empty((M, K), dtype=dt, device=dev)
-    if dweights is None and want_dweights:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _check(lib, lib.gmm_combine_bwd(*args, _arg(dy, (M, K), (dt,), "dy", dev),
-                                    _arg(dweights, (T, k), _F32, "dweights", dev), _stream(dev)))
+    yp = wp = None
+    if dy is not None or want_dy:
+        dy, yp = _out(dy, (M, K), dt, (dt,), "dy", dev)
+    if dweights is not None or want_dweights:
+        dweights, wp = _out(dweights, (T, k), torch.float32, _F32, "dweights", dev)
+    _check(lib, lib.gmm_combine_bwd(*args, yp, wp, _stream(dev)))
     return dy, dweights
 
 
@@ -204,11 +220,9 @@ def gmm_bf16_linear(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Ten
             _arg(group_sizes, (G,), _INT32, "group_sizes", dev), M, K, N, G, _arg(bias, (G, N), _FLOAT, "bias", dev),
             0 if bias is None else _DT[bias.dtype], act)
     pp = _arg(pre, (M, N), _BF16, "pre", dev)
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    _check(lib, lib.gmm_bf16_linear(*args, _arg(residual, (M, N), (out.dtype,), "residual", dev),
-                                    _arg(out, (M, N), _FLOAT, "out", dev), _DT[out.dtype], pp, *ffn._status(ws, dev),
-                                    _stream(dev)))
+    out, op = _out(out, (M, N), out_dtype, _FLOAT, "out", dev)
+    _check(lib, lib.gmm_bf16_linear(*args, _arg(residual, (M, N), (out.dtype,), "residual", dev), op, _DT[out.dtype],
+                                    pp, *ffn._status(ws, dev), _stream(dev)))
     return out
 
 
@@ -236,18 +250,17 @@ def gmm_bf16_linear_bwd(dout: torch.Tensor, rhs: torch.Tensor, group_sizes: torc
     args = (_arg(dout, None, _BF16, "dout", dev), _arg(rhs, None, _BF16, "rhs", dev),
             _arg(group_sizes, (G,), _INT32, "group_sizes", dev), _arg(lhs, (M, K), _BF16, "lhs", dev),
             _arg(pre, (M, N), _BF16, "pre", dev), _named(activation, ACTIVATIONS, "activation"), M, K, N, G)
-    if dx is None and want_dx:
-        dx = torch.empty((M, K), dtype=dx_dtype, device=dev)
-    if dw is None and want_dw:
-        dw = torch.empty((G, K, N), dtype=dw_dtype, device=dev)
-    if db is None and want_db:
-        db = torch.empty((G, N), dtype=db_dtype, device=dev)
-    if ws is None:
-        ws = torch.empty(max(lib.gmm_workspace_bytes(OP_BF16_LINEAR_BWD, M, K, N, G), 16), dtype=torch.uint8, device=dev)
+    xp = wp = bp = None
+    if dx is not None or want_dx:
+        dx, xp = _out(dx, (M, K), dx_dtype, _FLOAT, "dx", dev)
+    if dw is not None or want_dw:
+        dw, wp = _out(dw, (G, K, N), dw_dtype, _FLOAT, "dw", dev)
+    if db is not None or want_db:
+        db, bp = _out(db, (G, N), db_dtype, _FLOAT, "db", dev)
+    ws, sp, sb = _work(ws, dev, OP_BF16_LINEAR_BWD, M, K, N, G)
     _check(lib, lib.gmm_bf16_linear_bwd(
-        *args, _arg(dx, (M, K), _FLOAT, "dx", dev), 0 if dx is None else _DT[dx.dtype],
-        _arg(dw, (G, K, N), _FLOAT, "dw", dev), 0 if dw is None else _DT[dw.dtype],
-        _arg(db, (G, N), _FLOAT, "db", dev), 0 if db is None else _DT[db.dtype], *ffn._status(ws, dev), _stream(dev)))
+        *args, xp, 0 if dx is None else _DT[dx.dtype], wp, 0 if dw is None else _DT[dw.dtype], bp,
+        0 if db is None else _DT[db.dtype], sp, sb, _stream(dev)))
     return dx, dw, db
 
 

@@ -38,12 +38,13 @@ def test_exports(lib):
 def test_workspace_of_the_order(lib):
     def w(n, G):
         return lib.gmm_workspace_bytes(gmm.OP_SORT_TOKENS, n, 0, 0, G)
-    # the status block, and counts of every run of slots and their totals
-    assert w(8, 256) == 256 + 4 * 2 * 256
+    # the status block, and where one workgroup does not take all slots counts of every run of them and their totals
+    assert w(8, 256) == 256 and w(4096, 1024) == 256
+    assert w(4097, 256) == 256 + 4 * 6 * 256
     assert w(0, 4096) == 256 + 4 * 2 * 4096
-    assert w(65536, 256) == 256 + 4 * 33 * 256
+    assert w(65536, 256) == 256 + 4 * 65 * 256
     assert w((1 << 31) - 1024, 4096) <= 256 + 4 * 1025 * 4096      # bounded however many slots
-    assert w(-5, 16) == w(0, 16) and w(100, 0) == 256
+    assert w(-5, 2000) == w(0, 2000) and w(100, 0) == 256
 
 
 def route(lib, l=A, dt=0, b=0, T=10, E=64, k=4, score=0, ids=A, w=A):
@@ -85,7 +86,8 @@ def sort(lib, ids=A, T=10, k=4, first=0, G=16, M=40, gs=A, row=A, slot=A, ws=A, 
     (dict(gs=MIS), ALIGN), (dict(row=MIS), ALIGN), (dict(slot=MIS), ALIGN), (dict(ws=MIS), ALIGN),
     (dict(G=0), SHAPE), (dict(G=4097), SHAPE), (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(first=-1), SHAPE),
     (dict(first=1 << 31), SHAPE), (dict(T=-1), SHAPE), (dict(k=0), SHAPE), (dict(k=65), SHAPE),
-    (dict(T=1 << 30, k=2), SHAPE), (dict(ws=0), WORKSPACE), (dict(wsb=256 + 4 * 2 * 16 - 1), WORKSPACE),
+    (dict(T=1 << 30, k=2), SHAPE), (dict(ws=0), WORKSPACE), (dict(wsb=255), WORKSPACE),
+    (dict(T=2000, wsb=256 + 4 * 9 * 16 - 1), WORKSPACE),
 ])
 def test_order_refusals(lib, kw, status):
     assert sort(lib, **kw) == status
