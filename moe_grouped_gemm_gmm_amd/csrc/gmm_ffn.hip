@@ -17,7 +17,7 @@
 // fp32.  In the order they stand here:
 //   ffn_kernel       128 x 128 or 128 x 256 tiles, every product
 //   ffn_bwd_kernel   both products of a small backward pass in one launch
-//   ffn_ws_kernel    160 x 256 tiles fed by load waves, forward and dX
+//   ffn_ws_kernel    160 x 256 tiles fed by load waves, forward and dX (linear_ws_kernel: the plain forward)
 //   few_kernel       the forward for few rows per expert, K split over waves
 #include "gmm_launch.hpp"
 #include "gmm_linear.hpp"
@@ -317,47 +317,60 @@ __device__ __forceinline__ void gated_epilogue(const FfnArgs& a, const FfnItem& 
 // Epilogue of the plain forward: each wave stages 32 rows x 64 columns of fp32
 // sums at a time and finishes whole row segments (128 bytes of bf16), eight
 // columns a lane, so the bias stays in registers and the residual, the kept
-// sums and the output cross the chip in full lines.
+// sums and the output cross the chip in full lines.  The residual of a step is
+// read while the step before is finished.
 template <bool OUT_BF16, int NJ>
 __device__ __forceinline__ void linear_epilogue(const FfnArgs& a, const FfnItem& it, const v4f (&acc)[4][NJ],
                                                 uint16_t* sm) {
-    constexpr int kRow = 64 + 4;   // fp32
+    constexpr int kRow = 64 + 4, kSteps = NJ / 4 * 2;   // fp32; halves of 64 columns
     const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
     const int wm = tid >> 7, wn = (tid >> 6) & 1, lr = lane & 15, lg = lane >> 4;
     float* ep = reinterpret_cast<float*>(sm) + wave * 32 * kRow;
     const int orow = lane >> 3, ocol = (lane & 7) * 8;
+    // fragments 4q .. 4q + 3 are 64 neighbouring columns (NJ == 4: twice 32)
+    auto col_of = [&](int step) {
+        const int q = step >> 1;
+        return it.c0 + (NJ == 8 ? 16 * NJ * q + 64 * wn + ocol : (ocol >= 32 ? 64 : 0) + 32 * wn + ocol % 32);
+    };
+    auto row_of = [&](int step, int p) {
+        const int t = 32 * (step & 1) + 8 * p + orow;
+        return it.row0 + 32 * (t >> 4) + 16 * wm + (t & 15);
+    };
+    ResidualVec<OUT_BF16> res[4];
+    auto fetch = [&](int step, int p) {
+        const int row = row_of(step, p), col = col_of(step);
+        if (a.residual != nullptr && row < it.hi && col < a.NN) res[p].load(a.residual, (int64_t)row * a.NN + col);
+    };
 #pragma unroll
-    for (int q = 0; q < NJ / 4; ++q) {
-        // fragments 4q .. 4q + 3 are 64 neighbouring columns
-        const int col = it.c0 + (NJ == 8 ? 16 * NJ * q + 64 * wn : 0) +
-                        (NJ == 8 ? ocol : (ocol >= 32 ? 64 : 0) + 32 * wn + ocol % 32);
+    for (int p = 0; p < 4; ++p) fetch(0, p);
+    float bias[8];
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step) {
+        const int q = step >> 1, half = step & 1, col = col_of(step);
         const bool in = col < a.NN;
-        float bias[8];
-        linear_bias(a, it.g, in ? col : 0, bias);
+        if (half == 0) linear_bias(a, it.g, in ? col : 0, bias);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<v4f*>(ep + (16 * i + lr) * kRow + 16 * j + 4 * lg) = acc[2 * half + i][4 * q + j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<v4f*>(ep + (16 * i + lr) * kRow + 16 * j + 4 * lg) = acc[2 * half + i][4 * q + j];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int p = 0; p < 4; ++p) {
+            const int row = row_of(step, p);
+            if (row < it.hi && in) {
+                float z[8], r[8];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int r = 8 * p + orow, t = 32 * half + r;
-                const int row = it.row0 + 32 * (t >> 4) + 16 * wm + (t & 15);
-                if (row < it.hi && in) {
-                    float z[8];
-#pragma unroll
-                    for (int c = 0; c < 8; c += 4) {
-                        const v4f v = *reinterpret_cast<const v4f*>(ep + r * kRow + ocol + c);
-                        z[c] = v[0]; z[c + 1] = v[1]; z[c + 2] = v[2]; z[c + 3] = v[3];
-                    }
-                    linear_finish<OUT_BF16, 8>(a, row, col, bias, z);
+                for (int c = 0; c < 8; c += 4) {
+                    const v4f v = *reinterpret_cast<const v4f*>(ep + (8 * p + orow) * kRow + ocol + c);
+                    z[c] = v[0]; z[c + 1] = v[1]; z[c + 2] = v[2]; z[c + 3] = v[3];
                 }
+                res[p].get(r);
+                linear_finish<OUT_BF16, 8>(a, row, col, bias, r, z);
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (step + 1 < kSteps) fetch(step + 1, p);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -1213,21 +1226,86 @@ __device__ __forceinline__ void ws_store(int tid, E* out, int64_t ld, int row0, 
     }
 }
 
+// End of an item of the plain forward: two halves of 128 columns, the fp32 sums
+// of up to 96 rows staged at a time, finished eight columns a thread. A thread
+// keeps its columns over a half's rounds, so the bias is read once; a bf16
+// residual is read a round ahead, so that no round waits for memory (one in
+// fp32 would need registers that the sums take: it is read where it is used).
+constexpr int kLinRounds = 2 * WsRounds<float, 128>::kRounds;
+template <bool OUT_BF16>
+__device__ __forceinline__ void linear_ws_end(const FfnArgs& a, int tid, int g, int row0, int rows, int c0,
+                                              const v16f (&acc)[3][2], uint16_t* sm) {
+    using R = WsRounds<float, 128>;
+    constexpr int P = R::P, RB = R::RB, kRounds = R::kRounds;
+    const int lane = tid & 63, wm = __builtin_amdgcn_readfirstlane(tid >> 8), wn = (tid >> 6) & 3;
+    const int c = (tid & 15) * 8, r0 = tid >> 4;   // 32 rows a pass
+    float* s = reinterpret_cast<float*>(sm);
+    ResidualVec<OUT_BF16> res[RB];
+    auto fetch = [&](int p, int k, int i) {
+        const int r = 32 * (RB * k + i) + r0, col = c0 + 128 * p + c;
+        if (OUT_BF16 && a.residual != nullptr && r < rows && col < a.NN) res[i].load(a.residual, (int64_t)(row0 + r) * a.NN + col);
+    };
+#pragma unroll
+    for (int i = 0; i < RB; ++i) fetch(0, 0, i);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int col = c0 + 128 * p + c;
+        const bool in = col < a.NN;
+        float bias[8];
+        linear_bias(a, g, in ? col : 0, bias);
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+            const int step = p * kRounds + k;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int blk = 2 * i + wm - k * RB;
+                if (blk < 0 || blk >= RB || 2 * i + wm >= 5) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4*>(s + (32 * blk + (lane & 31)) * P + 32 * wn + 8 * q + 4 * (lane >> 5)) =
+                        make_float4(acc[i][p][4 * q], acc[i][p][4 * q + 1], acc[i][p][4 * q + 2], acc[i][p][4 * q + 3]);
+            }
+            stage_barrier();
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const int r = 32 * (RB * k + i) + r0;
+                if (r < rows && in) {
+                    float z[8];
+                    [[maybe_unused]] float v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; q += 4) {
+                        const float4 d = *reinterpret_cast<const float4*>(s + (32 * i + r0) * P + c + q);
+                        z[q] = d.x; z[q + 1] = d.y; z[q + 2] = d.z; z[q + 3] = d.w;
+                    }
+                    if constexpr (OUT_BF16) {
+                        res[i].get(v);
+                        linear_finish<OUT_BF16, 8>(a, row0 + r, col, bias, v, z);
+                    } else {
+                        linear_finish<OUT_BF16, 8>(a, row0 + r, col, bias, z);
+                    }
+                }
+                if (step + 1 < 2 * kRounds) fetch((step + 1) / kRounds, (step + 1) % kRounds, i);
+            }
+            stage_barrier();
+        }
+    }
+}
+
 template <int MODE, bool OUT_BF16, int SAVE>
-__global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) {
-    static_assert(MODE == kGated || MODE == kBwdX, "forward and dX");
+__device__ __forceinline__ void ws_body(const FfnArgs& a) {
+    static_assert(MODE == kGated || MODE == kBwdX || MODE == kLinear, "forward and dX");
     constexpr int S = kWsStages, kSt = kWsStage;
-    constexpr bool kBTr = MODE == kGated;
+    constexpr bool kBTr = MODE != kBwdX;
     using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
     // barriers of an item's end
-    constexpr int kEndBarriers = 2 * WsRounds<E, MODE == kGated ? 128 : 256>::kRounds +
+    constexpr int kEndBarriers = MODE == kLinear ? 2 * kLinRounds : 2 * WsRounds<E, MODE == kGated ? 128 : 256>::kRounds +
                                  (SAVE == kSaveBf16 ? 4 * WsRounds<uint16_t, 128>::kRounds : SAVE == kSaveMx8 ? 2 : 0);
     __shared__ __attribute__((aligned(1024))) uint16_t ring[S * kSt];
     __shared__ __attribute__((aligned(16))) int s_info[8][4];   // items of the last rounds: g, first row, end, column tile
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.K, NN = a.NN, N = NN / 2;
-    const int nsl = (MODE == kGated ? K : NN) >> 6;
+    const int nsl = (MODE == kBwdX ? NN : K) >> 6;
     constexpr int kItemCols = MODE == kGated ? kWsCols / 2 : kWsCols;
     if (wave == 1 && blockIdx.x == 0) {   // the call's device status word
         const int st = group_status(a.group_sizes, a.G, a.M);
@@ -1241,7 +1319,7 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
         //      of one item after the other, with one slot after each item for its
         //      results; loading runs two slots ahead of the barriers, into the
         //      next item where this one ends.
-        const int p = wave - 8, lda = MODE == kGated ? K : NN;
+        const int p = wave - 8, lda = MODE == kBwdX ? NN : K;
         EvenItems items;
         items.init(a.group_sizes, a.G, a.M, a.cap);
         const int64_t bstep = kBTr ? 64 * (int64_t)NN : 64;
@@ -1281,7 +1359,8 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
                 if constexpr (kBTr) {
                     const int r = 2 * j + (lane >> 5), c = (lane & 31) >> 1;   // row r of 64: slice r / 32
                     const int tc = 16 * (c ^ (2 * (r & 3))) + 8 * (lane & 1);
-                    const int cc = tc < 128 ? min(c0 + tc, N - 8) : N + min(c0 + tc - 128, N - 8);
+                    const int cc = MODE == kLinear ? min(c0 + tc, NN - 8)
+                                   : tc < 128 ? min(c0 + tc, N - 8) : N + min(c0 + tc - 128, N - 8);
                     pb[i] = wg + (int64_t)r * NN + cc;
                 } else {
                     const DmaLane d = dma_direct<64, 8, 8>(j, lane);
@@ -1479,6 +1558,8 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) v[k] = acc[i][0][4 * q + k];
                                 });
+        } else if constexpr (MODE == kLinear) {
+            linear_ws_end<OUT_BF16>(a, fresh_tid(), g, row0, rows, c0, acc, sm);
         } else {
             ws_store<E, 256, 2>(tid, reinterpret_cast<E*>(a.out), K, row0, rows, c0, K, 64 * wn, sm,
                                 [&](int i, int b, int q, float (&v)[4]) {
@@ -1490,15 +1571,28 @@ __global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) 
 }
 
 template <int MODE, bool OUT_BF16, int SAVE>
+__global__ __launch_bounds__(kWsThreads, 3) void ffn_ws_kernel(const FfnArgs a) {
+    ws_body<MODE, OUT_BF16, SAVE>(a);
+}
+template <bool OUT_BF16>
+__global__ __launch_bounds__(kWsThreads, 3) void linear_ws_kernel(const FfnArgs a) {
+    ws_body<kLinear, OUT_BF16, kSaveNone>(a);
+}
+
+template <int MODE, bool OUT_BF16, int SAVE>
 hipError_t launch_ws(FfnArgs a, int cap, hipStream_t stream) {
-    const int cols = MODE == kGated ? a.NN / 2 : a.K, tc = MODE == kGated ? kWsCols / 2 : kWsCols;
+    const int cols = MODE == kGated ? a.NN / 2 : (MODE == kLinear ? a.NN : a.K);
+    const int tc = MODE == kGated ? kWsCols / 2 : kWsCols;
     a.cap = cap;
     a.ntiles_r = 0;
     a.ntiles_c = (cols + tc - 1) / tc;
     a.nblocks = (int)(max_work_items(a.M, a.G < a.M ? a.G : a.M, cap) * a.ntiles_c);
     // one workgroup per CU, a multiple of the XCDs (the items' XCD placement counts on it)
     const int grid = (a.nblocks < device_cus() ? a.nblocks + kNumXcd - 1 : device_cus()) / kNumXcd * kNumXcd;
-    hipLaunchKernelGGL((ffn_ws_kernel<MODE, OUT_BF16, SAVE>), dim3((unsigned)grid), dim3(kWsThreads), 0, stream, a);
+    if constexpr (MODE == kLinear)
+        hipLaunchKernelGGL((linear_ws_kernel<OUT_BF16>), dim3((unsigned)grid), dim3(kWsThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL((ffn_ws_kernel<MODE, OUT_BF16, SAVE>), dim3((unsigned)grid), dim3(kWsThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -1853,6 +1947,7 @@ template <bool OUT_BF16>
 hipError_t launch_linear(const FfnArgs& a, hipStream_t stream) {
     const FfnChoice c = linear_fwd_choice(a.M, a.K, a.NN, a.G);
     if (c.kernel == kFfnFewRows) return launch_few_rows<kLinear, OUT_BF16, kSaveNone>(a, c, stream);
+    if (c.kernel == kFfnLoadWaves) return launch_ws<kLinear, OUT_BF16, kSaveNone>(a, c.rows, stream);
     return c.cols == 256 ? launch<kLinear, OUT_BF16, kSaveNone, 8>(a, stream)
                          : launch<kLinear, OUT_BF16, kSaveNone, 4>(a, stream);
 }
@@ -1882,14 +1977,49 @@ FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8) {
     return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
 }
 
+// The plain forward.  Measured (us; rows, experts, K, N, R: with a residual):
+//   few rows (32 rows x 64 columns, K split over four waves) / 128 x 128 tiles /
+//   load waves, up to three workgroups a CU: 1000, 8, 1024, 512 8.3 / 21.8 /
+//   18.5; 1777, 13, 1088, 704 13.9 / 21.5 / 17.5; 500, 4, 2048, 1024 15.2 / 34.1 /
+//   28.2; 700, 3, 704, 64 7.4 / 17.4 / 13.6; four: 2000, 16, 512, 1024 13.1 /
+//   12.9 / 11.8; 1000, 8, 2048, 2048 43.8 / 36.5 / 30.4.  64 rows an item are no
+//   better where a group has more (9.4 for the first, 17.4 for the second).
+//   load waves / the better of 128 and 256 columns, one round of the chip at
+//   least three quarters full, K from 768 on: 8192, 32, 2048, 512 30.7 / 37.7;
+//   8192, 32, 2048, 1024 49.9 / 56.8; 4096, 32, 1024, 1024 23.8 / 28.1; 6000, 20,
+//   2048, 1280 39.4 / 48.4; 5000, 12, 2048, 1024 35.7 / 42.5; shorter: 3000, 8,
+//   512, 2048 16.4 / 15.3
+//   more rounds where rows of x lie a multiple of 4 KB apart and a group is at
+//   most three items: 24000, 64, 2048, 1024 135 / 154; 65536, 256, 2048, 512 216 /
+//   232; not: 16384, 1, 4096, 1024 145 / 123; 12000, 60, 1024, 1024 41.0 / 32.9;
+//   and where a group is two items of eight column tiles or more: 8192, 32, 512,
+//   2048 30.9 / 34.4, R 36.0 / 39.4; 65536, 256, 512, 2048 240 / 238, R 284 / 322
+//   128 / 256 columns, K up to 256: 60000, 256, 64, 2048 80 / 82, R 156 / 199;
+//   30000, 100, 256, 512 R 25.4 / 32.4; above: 16000, 64, 384, 768 R 29.1 / 25.5
 FfnChoice linear_fwd_choice(int M, int K, int NN, int G) {
-    (void)K;
     const int busy = G < M ? G : M, rows = (M + busy - 1) / busy;
-    if (rows <= kFewMaxRows && (int64_t)busy * (NN / 128) < device_cus()) {
-        const bool narrow = (int64_t)busy * (NN / 32) <= device_cus();
-        return {kFfnFewRows, narrow ? 8 : 4, rows <= 16 ? 16 : (rows <= 32 ? 32 : 64), narrow ? 32 : 64};
+    const int64_t cus = device_cus(), tiles = (NN + 255) / 256;
+    const int few = rows <= 16 ? 16 : 32;
+    if (max_work_items(M, busy, few) * (NN / 64) <= 3 * cus) {
+        const bool narrow = (int64_t)busy * (NN / 32) <= cus && rows <= 16;
+        return {kFfnFewRows, narrow ? 8 : 4, few, narrow ? 32 : 64};
     }
-    return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
+    // rows an item may have: the rows of evenly routed groups, most of them
+    const double mean = (double)M / (double)busy, high = mean + sqrt(mean);
+    int cap = 0;
+    double cost = 0.0;
+    for (int c = 64; c <= kWsRows && mean >= 96.0 && K >= 512; c += 32) {
+        const int64_t n = (int64_t)ceil(high / c), wgs = busy * n * tiles, r = (wgs + cus - 1) / cus;
+        const bool fits = (r == 1 && K >= 768) || (K % 2048 == 0 && n <= 3) || (tiles >= 8 && n <= 2);
+        if (!fits || 4 * wgs < 3 * r * cus) continue;
+        const double t = (double)r * (2.0 + mean / (double)n / 160.0);
+        if (cap == 0 || t < cost) {
+            cap = c;
+            cost = t;
+        }
+    }
+    if (cap > 0) return {kFfnLoadWaves, 12, cap, 256};
+    return {kFfnTiles, 4, 128, K > 256 && wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
 }
 
 FfnChoice ffn_dx_choice(int M, int K, int NN, int G) {

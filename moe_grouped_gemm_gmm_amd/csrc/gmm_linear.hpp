@@ -2,10 +2,18 @@
 // + residual, and the activations' slopes (device side).  Everything is in
 // fp32; out is rounded once, and pre, where it is kept, once to bf16.
 //
-// The activations are written so that small results keep their digits: z times
-// a sigmoid for SiLU and the tanh form of GELU (1 + tanh(u) = 2 / (1 +
-// exp(-2u))), z erfc(-z / sqrt 2) / 2 for GELU, whose 1 + erf would cancel for
-// z below -3.  An exponential that overflows gives 0.
+// The activations are written so that small results keep their digits, from
+// the hardware's 2^x and 1/x: an epilogue runs them on every output, and with
+// library exponentials and divisions SiLU alone cost the 128 x 128 tiles a third
+// of their time (3000 rows, 8 experts, K = 512, N = 2048: 19.5 us, 16.2 so; no activation 15.3).
+//   SiLU, tanh form of GELU: z / (1 + exp(-u)), since 1 + tanh(v) = 2 / (1 +
+//     exp(-2v)).  An exponential that overflows gives 0.
+//   GELU: with h = erfc(|z| / sqrt 2) / 2 it is z h for z < 0 and z (1 - h)
+//     above; 1 + erf would cancel below -3.  h = exp(-z^2 / 2) q(t), t = 1 / (1 +
+//     |z| / (2 sqrt 2)): q is a polynomial of degree 9, fitted to erfc(x)
+//     exp(x^2) / 2 on 0 <= x <= 14 by least squares on relative errors,
+//     reweighted until they are level; off by 3.3e-7 of the value at most,
+//     evaluated in fp32.
 #pragma once
 
 #include "gmm_launch.hpp"
@@ -17,18 +25,41 @@ namespace gmm {
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kLog2E = 1.44269504088896341f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 1.5957691216057308f;    // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
-__device__ __forceinline__ float logistic(float u) { return 1.0f / (1.0f + expf(-u)); }
+__device__ __forceinline__ float logistic(float u) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * u));
+}
+
+// exp(-z^2 / 2), and erfc(|z| / sqrt 2) / 2 over it.
+__device__ __forceinline__ float gauss(float z) { return __builtin_amdgcn_exp2f(-0.5f * kLog2E * (z * z)); }
+__device__ __forceinline__ float half_erfcx(float z) {
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.35355339059327376f, 1.0f));
+    float q = -2.940962091e-02f;
+    q = __builtin_fmaf(q, t, 1.416352689e-01f);
+    q = __builtin_fmaf(q, t, -2.421303689e-01f);
+    q = __builtin_fmaf(q, t, 1.371632516e-01f);
+    q = __builtin_fmaf(q, t, -1.183455344e-02f);
+    q = __builtin_fmaf(q, t, 1.005925909e-01f);
+    q = __builtin_fmaf(q, t, 1.217964739e-01f);
+    q = __builtin_fmaf(q, t, 1.411384493e-01f);
+    q = __builtin_fmaf(q, t, 1.410487443e-01f);
+    return __builtin_fmaf(q, t, -2.655870617e-07f);
+}
+// P(x <= z) of a standard normal, given gauss(z).
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+    const float h = e * half_erfcx(z);
+    return z < 0.0f ? h : 1.0f - h;
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == kActRelu) return z > 0.0f ? z : 0.0f;
     else if constexpr (ACT == kActSilu) return z * logistic(z);
-    else if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-z * kSqrtHalf);
+    else if constexpr (ACT == kActGelu) return z * normal_cdf(z, gauss(z));
     else if constexpr (ACT == kActGeluTanh) return z * logistic(kTanhScale * (z + kTanhCubic * z * z * z));
     else return z;
 }
@@ -40,7 +71,8 @@ __device__ __forceinline__ float act_slope(float z) {
         const float s = logistic(z);
         return s + z * s * (1.0f - s);
     } else if constexpr (ACT == kActGelu) {
-        return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+        const float e = gauss(z);
+        return normal_cdf(z, e) + z * kInvSqrt2Pi * e;
     } else if constexpr (ACT == kActGeluTanh) {
         const float s = logistic(kTanhScale * (z + kTanhCubic * z * z * z));
         return s + z * s * (1.0f - s) * (kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z));
@@ -109,12 +141,12 @@ __device__ __forceinline__ void store_n(void* p, int64_t e, const float (&v)[N])
     }
 }
 
-// From the sums z of N columns of a row to everything the call writes there.
+// From the sums z of N columns of a row to everything the call writes there; r:
+// the residual's values, if there is one.
 template <bool OUT_BF16, int N>
-__device__ __forceinline__ void linear_finish(const FfnArgs& a, int row, int col, const float (&bias)[N], float (&z)[N]) {
+__device__ __forceinline__ void linear_finish(const FfnArgs& a, int row, int col, const float (&bias)[N],
+                                              const float (&r)[N], float (&z)[N]) {
     const int64_t e = (int64_t)row * a.NN + col;
-    float r[N];
-    if (a.residual != nullptr) load_n<N>(a.residual, OUT_BF16, e, r);
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] += bias[i];
     if (a.gu != nullptr) store_n<true, N>(a.gu, e, z);
@@ -128,5 +160,38 @@ __device__ __forceinline__ void linear_finish(const FfnArgs& a, int row, int col
     }
     store_n<OUT_BF16, N>(a.out, e, z);
 }
+
+// The same with the residual read here.
+template <bool OUT_BF16, int N>
+__device__ __forceinline__ void linear_finish(const FfnArgs& a, int row, int col, const float (&bias)[N], float (&z)[N]) {
+    float r[N];
+    if (a.residual != nullptr) load_n<N>(a.residual, OUT_BF16, (int64_t)row * a.NN + col, r);
+    linear_finish<OUT_BF16, N>(a, row, col, bias, r, z);
+}
+
+// Eight values of the residual as they are stored, and as fp32.
+template <bool BF16>
+struct ResidualVec {
+    uint4 d[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void* p, int64_t e) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + e * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) d[i] = q[i];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (BF16) {
+            v[0] = bf16_lo(d[0].x); v[1] = bf16_hi(d[0].x); v[2] = bf16_lo(d[0].y); v[3] = bf16_hi(d[0].y);
+            v[4] = bf16_lo(d[0].z); v[5] = bf16_hi(d[0].z); v[6] = bf16_lo(d[0].w); v[7] = bf16_hi(d[0].w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(d[i].x);
+                v[4 * i + 1] = __uint_as_float(d[i].y);
+                v[4 * i + 2] = __uint_as_float(d[i].z);
+                v[4 * i + 3] = __uint_as_float(d[i].w);
+            }
+        }
+    }
+};
 
 }  // namespace gmm
