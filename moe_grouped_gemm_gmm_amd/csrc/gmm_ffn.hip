@@ -1977,49 +1977,60 @@ FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8) {
     return {kFfnTiles, 4, 128, wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
 }
 
-// The plain forward.  Measured (us; rows, experts, K, N, R: with a residual):
+// The plain forward.  Measured (us; rows, experts, K, N; R: with a residual, Z:
+// Zipf routing, which the host does not see):
 //   few rows (32 rows x 64 columns, K split over four waves) / 128 x 128 tiles /
-//   load waves, up to three workgroups a CU: 1000, 8, 1024, 512 8.3 / 21.8 /
-//   18.5; 1777, 13, 1088, 704 13.9 / 21.5 / 17.5; 500, 4, 2048, 1024 15.2 / 34.1 /
-//   28.2; 700, 3, 704, 64 7.4 / 17.4 / 13.6; four: 2000, 16, 512, 1024 13.1 /
-//   12.9 / 11.8; 1000, 8, 2048, 2048 43.8 / 36.5 / 30.4.  64 rows an item are no
-//   better where a group has more (9.4 for the first, 17.4 for the second).
+//   load waves, up to four workgroups a CU: 1000, 8, 1024, 512 8.3 / 21.8 / 18.5;
+//   1777, 13, 1088, 704 R 13.2 / 20.2 / 16.3; 500, 4, 2048, 1024 15.2 / 34.1 /
+//   28.2; 1100, 4, 4096, 1024 34.7 / 57.5 / 41.6; 1500, 12, 2048, 1024 26.1 / 33.0
+//   / 25.9; five: 2000, 16, 512, 1024 13.1 / 12.9 / 11.8; 1000, 8, 2048, 2048 43.8
+//   / 36.5 / 30.4.  64 rows an item are no better where a group has more (9.4 for
+//   the first).
 //   load waves / the better of 128 and 256 columns, one round of the chip at
-//   least three quarters full, K from 768 on: 8192, 32, 2048, 512 30.7 / 37.7;
-//   8192, 32, 2048, 1024 49.9 / 56.8; 4096, 32, 1024, 1024 23.8 / 28.1; 6000, 20,
-//   2048, 1280 39.4 / 48.4; 5000, 12, 2048, 1024 35.7 / 42.5; shorter: 3000, 8,
-//   512, 2048 16.4 / 15.3
+//   least three quarters full, K from 768 on: 8192, 32, 2048, 512 30.7 / 37.7 (Z
+//   32.1 / 39.1); 8192, 32, 2048, 1024 49.9 / 56.8; 4096, 32, 1024, 1024 23.8 /
+//   28.1; 6000, 20, 2048, 1280 39.4 / 48.4; 5000, 12, 2048, 1024 35.7 / 42.5;
+//   shorter: 3000, 8, 512, 2048 16.4 / 15.3
 //   more rounds where rows of x lie a multiple of 4 KB apart and a group is at
-//   most three items: 24000, 64, 2048, 1024 135 / 154; 65536, 256, 2048, 512 216 /
-//   232; not: 16384, 1, 4096, 1024 145 / 123; 12000, 60, 1024, 1024 41.0 / 32.9;
-//   and where a group is two items of eight column tiles or more: 8192, 32, 512,
-//   2048 30.9 / 34.4, R 36.0 / 39.4; 65536, 256, 512, 2048 240 / 238, R 284 / 322
+//   most three items: 24000, 64, 2048, 1024 R 135 / 154 (Z 138 / 159); 65536,
+//   256, 2048, 512 216 / 232; not: 16384, 1, 4096, 1024 145 / 123; 12000, 60,
+//   1024, 1024 41.0 / 32.9
+//   more than two rounds where a group is two items of eight column tiles or
+//   more, with a cap of 128 rows (160): 65536, 256, 512, 2048 R 288 (280) / 320, RZ
+//   290 (313) / 318, without R 250 (243) / 237; two rounds: 8192, 32, 512, 2048 R
+//   (36.0) / 39.4, RZ (48.0) / 38.4
 //   128 / 256 columns, K up to 256: 60000, 256, 64, 2048 80 / 82, R 156 / 199;
-//   30000, 100, 256, 512 R 25.4 / 32.4; above: 16000, 64, 384, 768 R 29.1 / 25.5
+//   30000, 100, 256, 512 R 25.4 / 32.4; up to 512: 16000, 64, 384, 768 R 29.1 /
+//   25.5; 8192, 32, 512, 2048 R 39.4 / 44.3; 65536, 256, 512, 2048 284 / 238
 FfnChoice linear_fwd_choice(int M, int K, int NN, int G) {
     const int busy = G < M ? G : M, rows = (M + busy - 1) / busy;
     const int64_t cus = device_cus(), tiles = (NN + 255) / 256;
     const int few = rows <= 16 ? 16 : 32;
-    if (max_work_items(M, busy, few) * (NN / 64) <= 3 * cus) {
+    if (max_work_items(M, busy, few) * (NN / 64) <= 4 * cus) {
         const bool narrow = (int64_t)busy * (NN / 32) <= cus && rows <= 16;
         return {kFfnFewRows, narrow ? 8 : 4, few, narrow ? 32 : 64};
     }
     // rows an item may have: the rows of evenly routed groups, most of them
     const double mean = (double)M / (double)busy, high = mean + sqrt(mean);
     int cap = 0;
+    int64_t rounds = 0;
     double cost = 0.0;
     for (int c = 64; c <= kWsRows && mean >= 96.0 && K >= 512; c += 32) {
         const int64_t n = (int64_t)ceil(high / c), wgs = busy * n * tiles, r = (wgs + cus - 1) / cus;
-        const bool fits = (r == 1 && K >= 768) || (K % 2048 == 0 && n <= 3) || (tiles >= 8 && n <= 2);
+        const bool fits = (r == 1 && K >= 768) || (K % 2048 == 0 && n <= 3) || (r > 2 && tiles >= 8 && n <= 2);
         if (!fits || 4 * wgs < 3 * r * cus) continue;
         const double t = (double)r * (2.0 + mean / (double)n / 160.0);
         if (cap == 0 || t < cost) {
             cap = c;
+            rounds = r;
             cost = t;
         }
     }
+    if (rounds > 2 && K < 2048) cap = 128;
     if (cap > 0) return {kFfnLoadWaves, 12, cap, 256};
-    return {kFfnTiles, 4, 128, K > 256 && wide_tiles(max_work_items(M, busy, 128), NN) ? 256 : 128};
+    const int64_t row_tiles = max_work_items(M, busy, 128);
+    const bool wide = K > 512 || (K > 256 && (tiles < 8 || row_tiles * (NN / 128) > 8 * cus));
+    return {kFfnTiles, 4, 128, wide && wide_tiles(row_tiles, NN) ? 256 : 128};
 }
 
 FfnChoice ffn_dx_choice(int M, int K, int NN, int G) {

@@ -2,11 +2,12 @@
 // the operand of the two products that follow, and db[g], the column sums of
 // dpre over the rows of group g.
 //
-// One pass over dout and pre.  A workgroup takes up to kItemRows rows of one
-// group and a strip of columns, eight a lane; a lane adds its rows' dpre in
-// fp32 before they are rounded, the lanes of a column meet in LDS, and the
-// item's sums go to a row of `part`.  A second launch adds each group's items.
-// No atomics: the order of every sum is that of the rows and items.
+// One pass over dout and pre, bound by memory.  A workgroup takes an item, up to
+// 32 or 128 rows of one group, and a strip of columns, eight a lane; a lane adds
+// its rows' dpre in fp32 before they are rounded, the lanes of a column meet in
+// LDS, and the item's sums go to a row of `part`.  A second launch adds each
+// group's items.  No atomics: the order of every sum is that of the rows and
+// items.
 #include "gmm_launch.hpp"
 #include "gmm_linear.hpp"
 
@@ -14,13 +15,17 @@ namespace gmm {
 
 namespace {
 
-constexpr int kItemRows = 32;
 constexpr int kStripLanes = 16;   // lanes across a strip at most: 128 columns
+
+// Rows of an item: 32 to fill the chip, 128 once that gives enough workgroups
+// (fewer partial sums to write and add: 65536 rows, 256 groups, N = 2048, no
+// activation 82 -> 56 us).
+int item_rows(int64_t M, int64_t N) { return M * N >= (int64_t(1) << 25) ? 128 : 32; }
 
 struct GradArgs {
     const uint16_t *dout, *pre;
     const int32_t* group_sizes;
-    int M, N, G, act, strips, lanes;   // lanes across a strip
+    int M, N, G, act, strips, lanes, item_rows;   // lanes across a strip
     uint16_t* dpre;
     float* part;                       // [item, N], or NULL: db is not wanted
     int32_t* status;
@@ -36,7 +41,7 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(const GradArgs a) {
         if (lane == 0) a.status[0] = st;
     }
     if (wave == 0) {
-        const WorkItem it = find_work_item<true>(a.group_sizes, a.G, a.M, kItemRows, w);
+        const WorkItem it = find_work_item<true>(a.group_sizes, a.G, a.M, a.item_rows, w);
         if (lane == 0) { s_info[0] = it.g; s_info[1] = it.lo; s_info[2] = it.hi; }
     }
     __syncthreads();
@@ -80,42 +85,47 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(const GradArgs a) {
     }
 }
 
-// db[g, 4 columns a thread]: the sum of the group's items.
+// db[g, 64 columns]: the sum of the group's items, sixteen threads to four
+// columns, each every sixteenth item (20000 rows of one group, N = 1024, both
+// launches: 179 us with a thread adding all items, 17.5 so).
 template <bool OUT_BF16>
 __global__ __launch_bounds__(256) void linear_db_kernel(const int32_t* __restrict__ group_sizes, int M, int N, int G,
-                                                        const float* __restrict__ part, void* __restrict__ db) {
+                                                        int item_rows, const float* __restrict__ part,
+                                                        void* __restrict__ db) {
     __shared__ int s_first, s_count;
-    const int g = blockIdx.y;
+    __shared__ v4f sums[16][16];
+    const int g = blockIdx.y, across = threadIdx.x & 15, down = threadIdx.x >> 4;
     if (threadIdx.x < 64) {   // items of earlier groups, and of this one
         int carry = 0, items = 0;
         for (int base = 0; base <= g; base += 64) {
             const GroupChunk ch = group_chunk(group_sizes, G, M, base, carry);
             carry = ch.next_carry;
-            const int c = group_items<true>(ch.lo, ch.hi, kItemRows), incl = wave_incl_scan(c);
-            if (g < base + 64) {
-                if (lane_id() == g - base) { s_first = items + incl - c; s_count = c; }
-                break;
-            }
+            const int c = group_items<true>(ch.lo, ch.hi, item_rows), incl = wave_incl_scan(c);
+            if (g < base + 64 && lane_id() == g - base) { s_first = items + incl - c; s_count = c; }
             items += lane_value(incl, 63);
         }
     }
     __syncthreads();
-    const int col = (blockIdx.x * 256 + threadIdx.x) * 4;
-    if (col >= N) return;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int col = blockIdx.x * 64 + 4 * across;   // N is a multiple of 64
     const float* p = part + (int64_t)s_first * N + col;
-    for (int i = 0; i < s_count; ++i, p += N) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
-    }
-    store_n<OUT_BF16, 4>(db, (int64_t)g * N + col, s);
+    const int n = s_count;
+    v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int i = down; i < n; i += 16) s += *reinterpret_cast<const v4f*>(p + (int64_t)i * N);
+    sums[down][across] = s;
+    __syncthreads();
+    if (down != 0) return;
+#pragma unroll
+    for (int d = 1; d < 16; ++d) s += sums[d][across];
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    store_n<OUT_BF16, 4>(db, (int64_t)g * N + col, v);
 }
 
-int64_t grad_items(int64_t M, int64_t G) { return max_work_items(M, G < M ? G : M, kItemRows); }
+int64_t grad_items(int64_t M, int64_t N, int64_t G) { return max_work_items(M, G < M ? G : M, item_rows(M, N)); }
 
 }  // namespace
 
-int64_t linear_part_words(int64_t M, int64_t N, int64_t G) { return M > 0 && N > 0 && G > 0 ? grad_items(M, G) * N : 0; }
+int64_t linear_part_words(int64_t M, int64_t N, int64_t G) { return M > 0 && N > 0 && G > 0 ? grad_items(M, N, G) * N : 0; }
 
 hipError_t launch_linear_grad(const void* dout, const void* pre, int act, const int32_t* group_sizes, int M, int N, int G,
                               void* dpre, void* db, bool db_bf16, float* part, int32_t* status, hipStream_t stream) {
@@ -130,21 +140,23 @@ hipError_t launch_linear_grad(const void* dout, const void* pre, int act, const 
         a.act = act;
         a.strips = (N / 8 + kStripLanes - 1) / kStripLanes;
         a.lanes = (N / 8 + a.strips - 1) / a.strips;
+        a.item_rows = item_rows(M, N);
         a.dpre = static_cast<uint16_t*>(dpre);
         a.part = db != nullptr ? part : nullptr;
         a.status = status;
-        const int64_t blocks = grad_items(M, G) * a.strips;
+        const int64_t blocks = grad_items(M, N, G) * a.strips;
         if (blocks >= int64_t(1) << 24) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL(linear_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (db == nullptr) return hipSuccess;
-    const dim3 grid((unsigned)((N / 4 + 255) / 256), (unsigned)G);
+    const dim3 grid((unsigned)(N / 64), (unsigned)G);
+    const int rows = item_rows(M, N);
     if (db_bf16)
-        hipLaunchKernelGGL((linear_db_kernel<true>), grid, dim3(256), 0, stream, group_sizes, M, N, G, part, db);
+        hipLaunchKernelGGL((linear_db_kernel<true>), grid, dim3(256), 0, stream, group_sizes, M, N, G, rows, part, db);
     else
-        hipLaunchKernelGGL((linear_db_kernel<false>), grid, dim3(256), 0, stream, group_sizes, M, N, G, part, db);
+        hipLaunchKernelGGL((linear_db_kernel<false>), grid, dim3(256), 0, stream, group_sizes, M, N, G, rows, part, db);
     return hipGetLastError();
 }
 

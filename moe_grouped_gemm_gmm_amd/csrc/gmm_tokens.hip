@@ -283,7 +283,8 @@ __device__ __forceinline__ Choices choices_of(const MoveArgs& a, int64_t t) {
 constexpr int kTailRows = 16;   // rows a unit behind the tokens' looks at
 
 // Zeros in the rows r0 .. r0 + 15 of out that no slot owns (row_bytes a
-// multiple of 16), by 256 threads.
+// multiple of 16), by TPT threads.
+template <int TPT>
 __device__ __forceinline__ void zero_unowned(const MoveArgs& a, int64_t r0, void* out, int64_t row_bytes) {
     const int lane = lane_id();
     const int64_t r = r0 + lane, slots = a.T * a.k;
@@ -294,24 +295,33 @@ __device__ __forceinline__ void zero_unowned(const MoveArgs& a, int64_t r0, void
     }
     for (unsigned long long m = __ballot(none); m != 0; m &= m - 1) {
         char* p = static_cast<char*>(out) + (r0 + __ffsll((long long)m) - 1) * row_bytes;
-        for (int64_t b = 16 * (int64_t)threadIdx.x; b < row_bytes; b += 16 * 256)
+        for (int64_t b = 16 * (int64_t)(threadIdx.x % TPT); b < row_bytes; b += 16 * TPT)
             *reinterpret_cast<u32x4*>(p + b) = u32x4{0u, 0u, 0u, 0u};
     }
 }
 
 // A unit is a token, or 16 rows of the sorted buffer to look for unowned ones.
+// TPT threads take one: the workgroup, or (rows of up to 2 KB) each of its waves
+// another.
 __device__ __forceinline__ int64_t move_units(const MoveArgs& a) { return a.T + (a.M + kTailRows - 1) / kTailRows; }
+template <int TPT>
+__device__ __forceinline__ int64_t first_unit() {
+    return (int64_t)blockIdx.x * (256 / TPT) + __builtin_amdgcn_readfirstlane(threadIdx.x / TPT);
+}
+template <int TPT>
+__device__ __forceinline__ int64_t unit_step() { return (int64_t)gridDim.x * (256 / TPT); }
 
+template <int TPT>
 __global__ __launch_bounds__(256) void dispatch_kernel(const MoveArgs a, const char* __restrict__ x, int64_t row_bytes,
                                                        char* __restrict__ out) {
-    for (int64_t u = blockIdx.x; u < move_units(a); u += gridDim.x) {
+    for (int64_t u = first_unit<TPT>(); u < move_units(a); u += unit_step<TPT>()) {
         if (u >= a.T) {
-            zero_unowned(a, (u - a.T) * kTailRows, out, row_bytes);
+            zero_unowned<TPT>(a, (u - a.T) * kTailRows, out, row_bytes);
             continue;
         }
         const Choices c = choices_of(a, u);
         if (c.mask == 0) continue;
-        for (int64_t b = 16 * (int64_t)threadIdx.x; b < row_bytes; b += 16 * 256) {
+        for (int64_t b = 16 * (int64_t)(threadIdx.x % TPT); b < row_bytes; b += 16 * TPT) {
             const u32x4 v = *reinterpret_cast<const u32x4*>(x + u * row_bytes + b);
             for (unsigned long long m = c.mask; m != 0; m &= m - 1)
                 *reinterpret_cast<u32x4*>(out + (int64_t)lane_value(c.row, __ffsll((long long)m) - 1) * row_bytes + b) = v;
@@ -324,118 +334,155 @@ __device__ __forceinline__ u32x4 row_vec(const void* p, int64_t row, int64_t pit
     return *reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + row * pitch + b);
 }
 
-// The next at most B choices of `mask` (removed from it): their rows and
-// weights, all wave-uniform; returns how many.
-template <int B>
-__device__ __forceinline__ int next_choices(const Choices& c, unsigned long long& mask, int (&j)[B]) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-        j[i] = 0;
-        if (mask != 0) {
-            j[i] = __ffsll((long long)mask) - 1;
-            mask &= mask - 1;
-            n = i + 1;
-        }
-    }
-    return n;
-}
-
-// Rows are loaded eight at a time before any is used: one after the other, each
-// waits for the one before (8192 tokens of 8 rows of 2048 bf16: 86 us, 62 so).
-constexpr int kBatch = 8;
-
-template <bool Y_BF16, bool OUT_BF16>
-__global__ __launch_bounds__(256) void combine_kernel(const MoveArgs a, const void* __restrict__ y, const void* residual,
-                                                      void* out) {
-    constexpr int N = Vec<Y_BF16>::N, kBytes = Y_BF16 ? 2 : 4;
-    const int64_t pitch = a.K * kBytes;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const Choices c = choices_of(a, t);
-        for (int64_t e = N * (int64_t)threadIdx.x; e < a.K; e += N * 256) {
-            float s[N];
-            if (residual != nullptr) {
-                get_n<OUT_BF16, N>(residual, t * a.K + e, s);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) s[i] = 0.0f;
-            }
-            unsigned long long mask = c.mask;
-            while (mask != 0) {
-                int j[kBatch];
-                const int n = next_choices<kBatch>(c, mask, j);
-                u32x4 d[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (i < n) d[i] = row_vec(y, lane_value(c.row, j[i]), pitch, e * kBytes);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (i < n) {
-                        const float w = __int_as_float(lane_value(__float_as_int(c.w), j[i]));
-                        float v[N];
-                        Vec<Y_BF16>::get(d[i], v);
-#pragma unroll
-                        for (int q = 0; q < N; ++q) s[q] = __builtin_fmaf(w, v[q], s[q]);
-                    }
-            }
-            put_n<OUT_BF16, N>(out, t * a.K + e, s);
-        }
-    }
-}
-
 __device__ __forceinline__ float wave_sum_f(float x) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
     return x;
 }
 
-template <bool D_BF16, bool Y_BF16>
-__global__ __launch_bounds__(256) void combine_bwd_kernel(const MoveArgs a, const void* __restrict__ dout,
-                                                          const void* __restrict__ y, void* __restrict__ dy,
-                                                          float* __restrict__ dweights) {
+// The first B choices of the mask, taken off it.  Their rows are loaded before
+// any is used.
+template <int B>
+__device__ __forceinline__ void take_choices(unsigned long long& mask, int (&j)[B]) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        j[i] = __ffsll((long long)mask) - 1;
+        mask &= mask - 1;
+    }
+}
+
+// s += weights * rows of B choices.
+template <bool Y_BF16, int B>
+__device__ __forceinline__ void add_rows(const Choices& c, unsigned long long& mask, const void* y, int64_t pitch,
+                                         int64_t b, float (&s)[Vec<Y_BF16>::N]) {
     constexpr int N = Vec<Y_BF16>::N;
-    __shared__ float part[4];
-    const int64_t units = dy != nullptr ? move_units(a) : a.T;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        if (u >= a.T) {
-            zero_unowned(a, (u - a.T) * kTailRows, dy, a.K * (Y_BF16 ? 2 : 4));
-            continue;
-        }
-        const Choices c = choices_of(a, u);
-        for (int j = 0; j < a.k; ++j) {
-            float dot = 0.0f;
-            if (c.mask >> j & 1) {
-                const int64_t row = lane_value(c.row, j);
-                const float w = __int_as_float(lane_value(__float_as_int(c.w), j));
-                for (int64_t e = N * (int64_t)threadIdx.x; e < a.K; e += N * 256) {
-                    float d[N];
-                    get_n<D_BF16, N>(dout, u * a.K + e, d);
-                    if (dweights != nullptr) {
-                        float v[N];
-                        get_n<Y_BF16, N>(y, row * a.K + e, v);
+    int j[B];
+    take_choices<B>(mask, j);
+    u32x4 d[B];
 #pragma unroll
-                        for (int i = 0; i < N; ++i) dot = __builtin_fmaf(d[i], v[i], dot);
-                    }
-                    if (dy != nullptr) {
+    for (int i = 0; i < B; ++i) d[i] = row_vec(y, lane_value(c.row, j[i]), pitch, b);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) d[i] *= w;
-                        put_n<Y_BF16, N>(dy, row * a.K + e, d);
-                    }
-                }
-            }
-            if (dweights == nullptr) continue;
-            dot = wave_sum_f(dot);
-            __syncthreads();
-            if (lane_id() == 0) part[threadIdx.x >> 6] = dot;
-            __syncthreads();
-            if (threadIdx.x == 0) dweights[u * a.k + j] = ((part[0] + part[1]) + part[2]) + part[3];
+    for (int i = 0; i < B; ++i) {
+        const float w = __int_as_float(lane_value(__float_as_int(c.w), j[i]));
+        float v[N];
+        Vec<Y_BF16>::get(d[i], v);
+#pragma unroll
+        for (int q = 0; q < N; ++q) s[q] = __builtin_fmaf(w, v[q], s[q]);
+    }
+}
+
+template <int TPT, bool Y_BF16, bool OUT_BF16, bool RES>
+__global__ __launch_bounds__(256) void combine_kernel(const MoveArgs a, const void* __restrict__ y, const void* residual,
+                                                      void* out) {
+    constexpr int N = Vec<Y_BF16>::N, kBytes = Y_BF16 ? 2 : 4;
+    const int64_t pitch = a.K * kBytes;
+    for (int64_t t = first_unit<TPT>(); t < a.T; t += unit_step<TPT>()) {
+        const Choices c = choices_of(a, t);
+        const int n = __popcll(c.mask);
+        for (int64_t e = N * (int64_t)(threadIdx.x % TPT); e < a.K; e += N * TPT) {
+            float s[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = 0.0f;
+            if constexpr (RES) get_n<OUT_BF16, N>(residual, t * a.K + e, s);
+            unsigned long long mask = c.mask;
+            for (int i = n >> 3; i > 0; --i) add_rows<Y_BF16, 8>(c, mask, y, pitch, e * kBytes, s);
+            if (n & 4) add_rows<Y_BF16, 4>(c, mask, y, pitch, e * kBytes, s);
+            if (n & 2) add_rows<Y_BF16, 2>(c, mask, y, pitch, e * kBytes, s);
+            if (n & 1) add_rows<Y_BF16, 1>(c, mask, y, pitch, e * kBytes, s);
+            put_n<OUT_BF16, N>(out, t * a.K + e, s);
         }
     }
 }
 
-dim3 unit_grid(int64_t units) {
-    return dim3((unsigned)(units < 1 ? 1 : (units < (1 << 20) ? units : 1 << 20)));
+// dy rows and, where wanted, partial dot products of B choices: acc[i] of the
+// thread's columns.
+template <int TPT, bool D_BF16, bool Y_BF16, int B>
+__device__ __forceinline__ void grad_rows(const MoveArgs& a, const Choices& c, unsigned long long& mask, int64_t t,
+                                          const void* dout, const void* y, void* dy, bool dots, float* part,
+                                          float* dweights) {
+    constexpr int N = Vec<Y_BF16>::N, kBytes = Y_BF16 ? 2 : 4;
+    int j[B];
+    take_choices<B>(mask, j);
+    float acc[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) acc[i] = 0.0f;
+    for (int64_t e = N * (int64_t)(threadIdx.x % TPT); e < a.K; e += N * TPT) {
+        float d[N];
+        get_n<D_BF16, N>(dout, t * a.K + e, d);
+        u32x4 r[B];
+        if (dots) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) r[i] = row_vec(y, lane_value(c.row, j[i]), a.K * kBytes, e * kBytes);
+        }
+        if (dy != nullptr) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const float w = __int_as_float(lane_value(__float_as_int(c.w), j[i]));
+                float v[N];
+#pragma unroll
+                for (int q = 0; q < N; ++q) v[q] = w * d[q];
+                put_n<Y_BF16, N>(dy, (int64_t)lane_value(c.row, j[i]) * a.K + e, v);
+            }
+        }
+        if (dots) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                float v[N];
+                Vec<Y_BF16>::get(r[i], v);
+#pragma unroll
+                for (int q = 0; q < N; ++q) acc[i] = __builtin_fmaf(d[q], v[q], acc[i]);
+            }
+        }
+    }
+    if (!dots) return;
+#pragma unroll
+    for (int i = 0; i < B; ++i) acc[i] = wave_sum_f(acc[i]);
+    if constexpr (TPT == 64) {
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (lane_id() == 0) dweights[t * a.k + j[i]] = acc[i];
+    } else {   // the four waves' parts, in their order
+        __syncthreads();
+        if (lane_id() == 0) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) part[(threadIdx.x >> 6) * 8 + i] = acc[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (threadIdx.x == i) dweights[t * a.k + j[i]] = ((part[i] + part[8 + i]) + part[16 + i]) + part[24 + i];
+    }
 }
+
+template <int TPT, bool D_BF16, bool Y_BF16>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(const MoveArgs a, const void* __restrict__ dout, const void* y,
+                                                          void* dy, float* __restrict__ dweights) {
+    __shared__ float part[32];
+    const int64_t units = dy != nullptr ? move_units(a) : a.T;
+    const bool dots = dweights != nullptr;
+    for (int64_t u = first_unit<TPT>(); u < units; u += unit_step<TPT>()) {
+        if (u >= a.T) {
+            zero_unowned<TPT>(a, (u - a.T) * kTailRows, dy, a.K * (Y_BF16 ? 2 : 4));
+            continue;
+        }
+        const Choices c = choices_of(a, u);
+        const int lane = threadIdx.x % TPT, n = __popcll(c.mask);
+        if (dots && lane < a.k && !(c.mask >> lane & 1)) dweights[u * a.k + lane] = 0.0f;
+        unsigned long long mask = c.mask;
+        for (int i = n >> 3; i > 0; --i) grad_rows<TPT, D_BF16, Y_BF16, 8>(a, c, mask, u, dout, y, dy, dots, part, dweights);
+        if (n & 4) grad_rows<TPT, D_BF16, Y_BF16, 4>(a, c, mask, u, dout, y, dy, dots, part, dweights);
+        if (n & 2) grad_rows<TPT, D_BF16, Y_BF16, 2>(a, c, mask, u, dout, y, dy, dots, part, dweights);
+        if (n & 1) grad_rows<TPT, D_BF16, Y_BF16, 1>(a, c, mask, u, dout, y, dy, dots, part, dweights);
+    }
+}
+
+dim3 unit_grid(int64_t units, int tpt) {
+    const int64_t blocks = (units + 256 / tpt - 1) / (256 / tpt);
+    return dim3((unsigned)(blocks < 1 ? 1 : (blocks < (1 << 20) ? blocks : 1 << 20)));
+}
+
+// Threads a token takes for rows of `bytes` bytes.
+bool wave_a_token(int64_t bytes) { return bytes <= 2048; }
 
 template <int NW, int GMAX, int BEFORE>
 hipError_t place(const int32_t* ids, int n, int first, int G, int M, Runs r, const int32_t* counts, int32_t* group_sizes,
@@ -481,37 +528,57 @@ hipError_t launch_sort_tokens(const int32_t* ids, int n, int first, int G, int M
 }
 
 hipError_t launch_dispatch(const MoveArgs& a, const void* x, bool bf16, void* out, hipStream_t stream) {
-    const int64_t units = a.T + (a.M + kTailRows - 1) / kTailRows;
-    hipLaunchKernelGGL(dispatch_kernel, unit_grid(units), dim3(256), 0, stream, a, static_cast<const char*>(x),
-                       a.K * (bf16 ? 2 : 4), static_cast<char*>(out));
+    const int64_t units = a.T + (a.M + kTailRows - 1) / kTailRows, bytes = a.K * (bf16 ? 2 : 4);
+    if (wave_a_token(bytes))
+        hipLaunchKernelGGL((dispatch_kernel<64>), unit_grid(units, 64), dim3(256), 0, stream, a,
+                           static_cast<const char*>(x), bytes, static_cast<char*>(out));
+    else
+        hipLaunchKernelGGL((dispatch_kernel<256>), unit_grid(units, 256), dim3(256), 0, stream, a,
+                           static_cast<const char*>(x), bytes, static_cast<char*>(out));
     return hipGetLastError();
 }
 
+namespace {
+
+// f(TPT, first type is bf16, second type is bf16)
+template <typename F>
+hipError_t with_types(bool wave, bool p, bool q, F f) {
+    using std::integral_constant;
+    auto types = [&](auto tpt) {
+        constexpr integral_constant<bool, true> yes;
+        constexpr integral_constant<bool, false> no;
+        if (p) return q ? f(tpt, yes, yes) : f(tpt, yes, no);
+        return q ? f(tpt, no, yes) : f(tpt, no, no);
+    };
+    return wave ? types(integral_constant<int, 64>{}) : types(integral_constant<int, 256>{});
+}
+
+}  // namespace
+
 hipError_t launch_combine(const MoveArgs& a, const void* y, bool y_bf16, const void* residual, void* out, bool out_bf16,
                           hipStream_t stream) {
-    const dim3 grid = unit_grid(a.T), block(256);
-    if (y_bf16) {
-        if (out_bf16) hipLaunchKernelGGL((combine_kernel<true, true>), grid, block, 0, stream, a, y, residual, out);
-        else hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, stream, a, y, residual, out);
-    } else {
-        if (out_bf16) hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, stream, a, y, residual, out);
-        else hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, stream, a, y, residual, out);
-    }
-    return hipGetLastError();
+    return with_types(wave_a_token(a.K * (y_bf16 ? 2 : 4)), y_bf16, out_bf16, [&](auto tpt, auto yb, auto ob) {
+        constexpr int TPT = decltype(tpt)::value;
+        constexpr bool YB = decltype(yb)::value, OB = decltype(ob)::value;
+        const dim3 grid = unit_grid(a.T, TPT), block(256);
+        if (residual != nullptr)
+            hipLaunchKernelGGL((combine_kernel<TPT, YB, OB, true>), grid, block, 0, stream, a, y, residual, out);
+        else
+            hipLaunchKernelGGL((combine_kernel<TPT, YB, OB, false>), grid, block, 0, stream, a, y, residual, out);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_combine_bwd(const MoveArgs& a, const void* dout, bool dout_bf16, const void* y, bool y_bf16, void* dy,
                               float* dweights, hipStream_t stream) {
     const int64_t units = a.T + (dy != nullptr ? (a.M + kTailRows - 1) / kTailRows : 0);
-    const dim3 grid = unit_grid(units), block(256);
-    if (dout_bf16) {
-        if (y_bf16) hipLaunchKernelGGL((combine_bwd_kernel<true, true>), grid, block, 0, stream, a, dout, y, dy, dweights);
-        else hipLaunchKernelGGL((combine_bwd_kernel<true, false>), grid, block, 0, stream, a, dout, y, dy, dweights);
-    } else {
-        if (y_bf16) hipLaunchKernelGGL((combine_bwd_kernel<false, true>), grid, block, 0, stream, a, dout, y, dy, dweights);
-        else hipLaunchKernelGGL((combine_bwd_kernel<false, false>), grid, block, 0, stream, a, dout, y, dy, dweights);
-    }
-    return hipGetLastError();
+    return with_types(wave_a_token(a.K * (y_bf16 ? 2 : 4)), dout_bf16, y_bf16, [&](auto tpt, auto db, auto yb) {
+        constexpr int TPT = decltype(tpt)::value;
+        constexpr bool DB = decltype(db)::value, YB = decltype(yb)::value;
+        hipLaunchKernelGGL((combine_bwd_kernel<TPT, DB, YB>), unit_grid(units, TPT), dim3(256), 0, stream, a, dout, y, dy,
+                           dweights);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace gmm
