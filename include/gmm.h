@@ -29,7 +29,8 @@
  *    gmm_device_status after the call.  Where the workspace is the 256 bytes of
  *    that status block, calls that share one and may run at the same time race
  *    on the status word only (the results are unaffected).  A larger workspace
- *    holds data of the call (gmm_bf16_swiglu_bwd of gmm_ffn.h keeps dP there):
+ *    holds data of the call (gmm_bf16_swiglu_bwd of gmm_ffn.h keeps dP there,
+ *    gmm_bf16_linear_bwd and gmm_sort_tokens of gmm_moe.h dpre and counts):
  *    such a call needs a workspace of its own until it has finished, or both
  *    calls' results are wrong.  A missing or too small workspace is
  *    GMM_ERR_WORKSPACE.
@@ -101,7 +102,8 @@ GMM_API const char *gmm_last_error(void);
 /*
  * gmm_workspace_bytes -- bytes of workspace the grouped call `op` (a gmm_op)
  *   needs for this shape: 256, the status block, and for gmm_bf16_swiglu_bwd
- *   4 M N more; 0 for an unknown op.  Sizes are not checked here.
+ *   4 M N more, for gmm_bf16_linear_bwd and gmm_sort_tokens what they keep; 0
+ *   for an unknown op.  Sizes are not checked here.
  */
 GMM_API size_t gmm_workspace_bytes(int op, int64_t M, int64_t K, int64_t N, int64_t G);
 

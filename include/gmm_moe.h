@@ -8,6 +8,8 @@
  *  - With T = 0 (or M = 0) the tensors of T (or M) rows may be NULL.
  *  - Indices are read on the device.  One outside its range stands for "none"
  *    and never makes a kernel read or write outside the caller's buffers.
+ *  - An output overlaps no other tensor of the call, unless a call says that it
+ *    may be one of them.
  *
  * A layer, forward:
  *     gmm_route           scores of the experts -> ids and weights [T,k]
@@ -33,6 +35,13 @@ typedef enum {
     GMM_OP_BF16_LINEAR = 33,     /* gmm_bf16_linear */
     GMM_OP_BF16_LINEAR_BWD = 34  /* gmm_bf16_linear_bwd */
 } gmm_moe_op;
+
+/*
+ * gmm_get_tile_config of the two products tells which kernel a call runs, in
+ * the words of gmm_ffn.h (kernels 1 to 3 for GMM_OP_BF16_LINEAR; for
+ * GMM_OP_BF16_LINEAR_BWD dX's, in a call for both gradients: 2 to 4, the weight
+ * gradient, unless in that launch, as GMM_OP_TGMM_MX8 of N columns).
+ */
 
 /* What an expert's score is made of a logit. */
 typedef enum {
@@ -81,7 +90,8 @@ GMM_API int gmm_route(const void *logits, int logits_dtype, const float *bias, i
  *   Experts that are off, and choices that are -1, take no part.  An expert
  *   named by several choices of a token gets the sum of their gradients.
  * dweights: [T,k] fp32.  logits, ids: as given to and made by gmm_route.
- * dlogits: [T,E], GMM_F32 or GMM_BF16.
+ * dlogits: [T,E], GMM_F32 or GMM_BF16; of the logits' dtype it may be logits
+ *   itself.
  */
 GMM_API int gmm_route_bwd(const float *dweights, const void *logits, int logits_dtype,
                           const int32_t *ids, int64_t T, int64_t E, int64_t k, int score,
@@ -137,7 +147,8 @@ GMM_API int gmm_combine(const void *y, int y_dtype, const int32_t *row_of, const
  *   0 for a slot without a row; rows of dy that no slot owns are zeros.
  * dout: [T,K], dout_dtype GMM_BF16 or GMM_F32.  y (needed for dweights) and dy:
  *   [M,K], y_dtype GMM_BF16 or GMM_F32.  weights: [T,k] fp32 (needed for dy).
- * dy, dweights [T,k] fp32: NULL where not wanted (both: GMM_ERR_NULL).
+ * dy, dweights [T,k] fp32: NULL where not wanted (both: GMM_ERR_NULL).  dy may
+ *   be y itself.
  * row_of and slot_of: made by gmm_sort_tokens.  K a multiple of 8.
  */
 GMM_API int gmm_combine_bwd(const void *dout, int dout_dtype, const void *y, int y_dtype,

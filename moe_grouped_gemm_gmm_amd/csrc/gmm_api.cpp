@@ -64,7 +64,7 @@ gmm_tile_config to_public(const gmm::TileConfig& c) {
     return o;
 }
 
-// gmm_get_tile_config of the calls of gmm_ffn.h.
+// gmm_get_tile_config of the calls of gmm_ffn.h and of gmm_moe.h's products.
 int ffn_tile_config(int op, int64_t M, int64_t K, int64_t N, int64_t G, int out_dtype, gmm_tile_config* cfg) {
     if (cfg == nullptr) return fail(GMM_ERR_NULL, "cfg is NULL");
     GMM_TRY(check_out_dtype(out_dtype, "out"));
@@ -73,9 +73,14 @@ int ffn_tile_config(int op, int64_t M, int64_t K, int64_t N, int64_t G, int out_
     GMM_TRY(check_mult(N, 64, "N"));
     if (M < 1 || N > kMaxDim / 2) return fail(GMM_ERR_SHAPE, "M=%lld, N=%lld out of range", (long long)M, (long long)N);
     const int m = (int)M, k = (int)K, n = (int)N, g = (int)G;
-    const gmm::FfnChoice c = op == GMM_OP_BF16_SWIGLU       ? gmm::gated_fwd_choice(m, k, 2 * n, g, false)
-                             : op == GMM_OP_BF16_SWIGLU_BWD ? gmm::ffn_bwd_choice(m, k, 2 * n, g)
-                                                            : gmm::ffn_dw_choice(k, n, g);
+    gmm::FfnChoice c;
+    switch (op) {
+        case GMM_OP_BF16_SWIGLU: c = gmm::gated_fwd_choice(m, k, 2 * n, g, false); break;
+        case GMM_OP_BF16_SWIGLU_BWD: c = gmm::ffn_bwd_choice(m, k, 2 * n, g); break;
+        case GMM_OP_BF16_LINEAR: c = gmm::linear_fwd_choice(m, k, n, g); break;
+        case GMM_OP_BF16_LINEAR_BWD: c = gmm::ffn_bwd_choice(m, k, n, g); break;
+        default: c = gmm::ffn_dw_choice(k, n, g); break;
+    }
     *cfg = gmm_tile_config{};
     cfg->kernel = c.kernel;
     cfg->waves = c.waves;
@@ -154,7 +159,8 @@ int gmm_set_tile_config(int op, const gmm_tile_config* cfg) {
 
 int gmm_get_tile_config(int op, int64_t M, int64_t K, int64_t N, int64_t G, int lhs_dtype,
                         int out_dtype, gmm_tile_config* cfg) {
-    if (op >= GMM_OP_BF16_SWIGLU && op <= GMM_OP_TGMM_MX8) return ffn_tile_config(op, M, K, N, G, out_dtype, cfg);
+    if ((op >= GMM_OP_BF16_SWIGLU && op <= GMM_OP_TGMM_MX8) || op == GMM_OP_BF16_LINEAR || op == GMM_OP_BF16_LINEAR_BWD)
+        return ffn_tile_config(op, M, K, N, G, out_dtype, cfg);
     if (op < GMM_OP_FP8_FWD || op > GMM_OP_FP8_INT4_FWD)
         return fail(GMM_ERR_SHAPE, "op %d has no tile configuration", op);
     if (cfg == nullptr) return fail(GMM_ERR_NULL, "cfg is NULL");

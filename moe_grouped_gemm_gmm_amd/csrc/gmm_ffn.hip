@@ -1922,23 +1922,21 @@ int ws_cap(int M, int G, int red, int tiles, int min_red, double min_mean, bool 
 // experts (more workgroups than CUs) 29.4 against 20.7 us.
 constexpr int kFewMaxRows = 64;   // mean rows an expert: up to 4 blocks of 16
 
-template <int MODE, bool OUT_BF16, int SAVE, int MB>
+template <bool OUT_BF16, int SAVE, int MB>
 hipError_t launch_few_mb(const FfnArgs& a, const FfnChoice& c, hipStream_t stream) {
     if constexpr (SAVE != kSaveMx8)
-        if (c.cols == 32) return launch_few<MODE, OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
-    return launch_few<MODE, OUT_BF16, SAVE, MB, 32, 4, 3>(a, stream);
-}
-template <int MODE, bool OUT_BF16, int SAVE>
-hipError_t launch_few_rows(const FfnArgs& a, const FfnChoice& c, hipStream_t stream) {
-    if (c.rows == 16) return launch_few_mb<MODE, OUT_BF16, SAVE, 1>(a, c, stream);
-    if (c.rows == 32) return launch_few_mb<MODE, OUT_BF16, SAVE, 2>(a, c, stream);
-    return launch_few_mb<MODE, OUT_BF16, SAVE, 4>(a, c, stream);
+        if (c.cols == 32) return launch_few<kGated, OUT_BF16, SAVE, MB, 16, 8, MB == 4 ? 3 : 4>(a, stream);
+    return launch_few<kGated, OUT_BF16, SAVE, MB, 32, 4, 3>(a, stream);
 }
 
 template <int SAVE, bool OUT_BF16>
 hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
     const FfnChoice c = gated_fwd_choice(a.M, a.K, a.NN, a.G, SAVE == kSaveMx8);
-    if (c.kernel == kFfnFewRows) return launch_few_rows<kGated, OUT_BF16, SAVE>(a, c, stream);
+    if (c.kernel == kFfnFewRows) {
+        if (c.rows == 16) return launch_few_mb<OUT_BF16, SAVE, 1>(a, c, stream);
+        if (c.rows == 32) return launch_few_mb<OUT_BF16, SAVE, 2>(a, c, stream);
+        return launch_few_mb<OUT_BF16, SAVE, 4>(a, c, stream);
+    }
     if (c.kernel == kFfnLoadWaves) return launch_ws<kGated, OUT_BF16, SAVE>(a, c.rows, stream);
     return c.cols == 256 ? launch<kGated, OUT_BF16, SAVE, 8>(a, stream) : launch<kGated, OUT_BF16, SAVE, 4>(a, stream);
 }
@@ -1946,7 +1944,11 @@ hipError_t launch_gated(const FfnArgs& a, hipStream_t stream) {
 template <bool OUT_BF16>
 hipError_t launch_linear(const FfnArgs& a, hipStream_t stream) {
     const FfnChoice c = linear_fwd_choice(a.M, a.K, a.NN, a.G);
-    if (c.kernel == kFfnFewRows) return launch_few_rows<kLinear, OUT_BF16, kSaveNone>(a, c, stream);
+    if (c.kernel == kFfnFewRows) {
+        if (c.rows == 32) return launch_few<kLinear, OUT_BF16, kSaveNone, 2, 32, 4, 3>(a, stream);
+        if (c.cols == 64) return launch_few<kLinear, OUT_BF16, kSaveNone, 1, 32, 4, 3>(a, stream);
+        return launch_few<kLinear, OUT_BF16, kSaveNone, 1, 16, 8, 4>(a, stream);
+    }
     if (c.kernel == kFfnLoadWaves) return launch_ws<kLinear, OUT_BF16, kSaveNone>(a, c.rows, stream);
     return c.cols == 256 ? launch<kLinear, OUT_BF16, kSaveNone, 8>(a, stream)
                          : launch<kLinear, OUT_BF16, kSaveNone, 4>(a, stream);

@@ -359,7 +359,7 @@ __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kerne
 
 template <int W, int V, bool BF16, bool OUT_BF16>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const float* __restrict__ dweights,
-                                                        const int32_t* __restrict__ ids, void* __restrict__ dlogits) {
+                                                        const int32_t* __restrict__ ids, void* dlogits) {
     const int lane = lane_id(), sub = lane % W, E = a.E, k = a.k;
     const bool vec = E % 4 == 0;
     const int64_t stride = (int64_t)gridDim.x * (256 / W);

@@ -51,6 +51,20 @@ def _out(t: Optional[torch.Tensor], shape, dtype: torch.dtype, dtypes: tuple, na
     return t, _arg(t, shape, dtypes, name, dev)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(lib, fn, dev: torch.device, *args) -> None:
+    """fn(*args, torch's current stream of dev), with dev as the current device."""
+    stream = _stream(dev)
+    if dev.index is None or _current_device() == dev.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    _check(lib, rc)
+
+
 @functools.lru_cache(maxsize=512)
 def _ws_bytes(op: int, M: int, K: int, N: int, G: int) -> int:
     return int(load_library().gmm_workspace_bytes(op, M, K, N, G))
@@ -88,7 +102,7 @@ def gmm_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
     kind = _named(score, SCORES, "score")
     ids, ip = _out(ids, (T, k), torch.int32, _INT32, "ids", dev)
     weights, wp = _out(weights, (T, k), torch.float32, _F32, "weights", dev)
-    _check(lib, lib.gmm_route(lp, _DT[logits.dtype], bp, T, E, k, kind, int(normalize), scale, ip, wp, _stream(dev)))
+    _call(lib, lib.gmm_route, dev, lp, _DT[logits.dtype], bp, T, E, k, kind, int(normalize), scale, ip, wp)
     return ids, weights
 
 
@@ -108,7 +122,7 @@ def gmm_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tenso
             _DT[logits.dtype], _arg(ids, None, _INT32, "ids", dev), T, E, k, _named(score, SCORES, "score"),
             int(normalize), scale)
     out, op = _out(out, (T, E), out_dtype or logits.dtype, _FLOAT, "out", dev)
-    _check(lib, lib.gmm_route_bwd(*args, op, _DT[out.dtype], _stream(dev)))
+    _call(lib, lib.gmm_route_bwd, dev, *args, op, _DT[out.dtype])
     return out
 
 
@@ -130,7 +144,7 @@ def gmm_sort_tokens(ids: torch.Tensor, G: int, first: int = 0, rows: Optional[in
     row_of, rp = _out(row_of, (T, k), torch.int32, _INT32, "row_of", dev)
     slot_of, sp = _out(slot_of, (max(M, 0),), torch.int32, _INT32, "slot_of", dev)
     ws, wp, wb = _work(ws, dev, OP_SORT_TOKENS, T * k, 0, 0, G)
-    _check(lib, lib.gmm_sort_tokens(ip, T, k, first, G, M, gp, rp, sp, wp, wb, _stream(dev)))
+    _call(lib, lib.gmm_sort_tokens, dev, ip, T, k, first, G, M, gp, rp, sp, wp, wb)
     return group_sizes, row_of, slot_of
 
 
@@ -148,7 +162,7 @@ def gmm_dispatch(x: torch.Tensor, row_of: torch.Tensor, slot_of: torch.Tensor, o
     args = (_arg(x, None, _FLOAT, "x", dev), _DT[x.dtype], _arg(row_of, None, _INT32, "row_of", dev),
             _arg(slot_of, (M,), _INT32, "slot_of", dev), T, k, M, K)
     out, op = _out(out, (M, K), x.dtype, (x.dtype,), "out", dev)
-    _check(lib, lib.gmm_dispatch(*args, op, _stream(dev)))
+    _call(lib, lib.gmm_dispatch, dev, *args, op)
     return out
 
 
@@ -165,8 +179,8 @@ def gmm_combine(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[torch.T
     args = (_arg(y, None, _FLOAT, "y", dev), _DT[y.dtype], _arg(row_of, None, _INT32, "row_of", dev),
             _arg(weights, (T, k), _F32, "weights", dev))
     out, op = _out(out, (T, K), out_dtype or y.dtype, _FLOAT, "out", dev)
-    _check(lib, lib.gmm_combine(*args, _arg(residual, (T, K), (out.dtype,), "residual", dev), T, k, M, K, op,
-                                _DT[out.dtype], _stream(dev)))
+    _call(lib, lib.gmm_combine, dev, *args, _arg(residual, (T, K), (out.dtype,), "residual", dev), T, k, M, K, op,
+          _DT[out.dtype])
     return out
 
 
@@ -195,7 +209,7 @@ def gmm_combine_bwd(dout: torch.Tensor, y: Optional[torch.Tensor], row_of: torch
         dy, yp = _out(dy, (M, K), dt, (dt,), "dy", dev)
     if dweights is not None or want_dweights:
         dweights, wp = _out(dweights, (T, k), torch.float32, _F32, "dweights", dev)
-    _check(lib, lib.gmm_combine_bwd(*args, yp, wp, _stream(dev)))
+    _call(lib, lib.gmm_combine_bwd, dev, *args, yp, wp)
     return dy, dweights
 
 
@@ -221,8 +235,8 @@ def gmm_bf16_linear(lhs: torch.Tensor, rhs: torch.Tensor, group_sizes: torch.Ten
             0 if bias is None else _DT[bias.dtype], act)
     pp = _arg(pre, (M, N), _BF16, "pre", dev)
     out, op = _out(out, (M, N), out_dtype, _FLOAT, "out", dev)
-    _check(lib, lib.gmm_bf16_linear(*args, _arg(residual, (M, N), (out.dtype,), "residual", dev), op, _DT[out.dtype],
-                                    pp, *ffn._status(ws, dev), _stream(dev)))
+    _call(lib, lib.gmm_bf16_linear, dev, *args, _arg(residual, (M, N), (out.dtype,), "residual", dev), op,
+          _DT[out.dtype], pp, *ffn._status(ws, dev))
     return out
 
 
@@ -258,9 +272,8 @@ def gmm_bf16_linear_bwd(dout: torch.Tensor, rhs: torch.Tensor, group_sizes: torc
     if db is not None or want_db:
         db, bp = _out(db, (G, N), db_dtype, _FLOAT, "db", dev)
     ws, sp, sb = _work(ws, dev, OP_BF16_LINEAR_BWD, M, K, N, G)
-    _check(lib, lib.gmm_bf16_linear_bwd(
-        *args, xp, 0 if dx is None else _DT[dx.dtype], wp, 0 if dw is None else _DT[dw.dtype], bp,
-        0 if db is None else _DT[db.dtype], sp, sb, _stream(dev)))
+    _call(lib, lib.gmm_bf16_linear_bwd, dev, *args, xp, 0 if dx is None else _DT[dx.dtype], wp,
+          0 if dw is None else _DT[dw.dtype], bp, 0 if db is None else _DT[db.dtype], sp, sb)
     return dx, dw, db
 
 

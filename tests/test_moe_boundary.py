@@ -137,6 +137,63 @@ def test_combine_bwd_refusals(lib, kw, status):
     assert combine_bwd(lib, **kw) == status
 
 
+def linear(lib, x=A, w=A, gs=A, M=100, K=128, N=192, G=4, b=A, bt=1, act=3, res=A, out=A, ot=1, pre=A, ws=A, wsb=256):
+    return lib.gmm_bf16_linear(P(x), P(w), P(gs), M, K, N, G, P(b), bt, act, P(res), P(out), ot, P(pre), P(ws), wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=0), NULL), (dict(w=0), NULL), (dict(gs=0), NULL), (dict(out=0), NULL),
+    (dict(x=MIS), ALIGN), (dict(w=MIS), ALIGN), (dict(b=MIS), ALIGN), (dict(res=MIS), ALIGN), (dict(out=MIS), ALIGN),
+    (dict(pre=MIS), ALIGN), (dict(ws=MIS), ALIGN), (dict(bt=2), DTYPE), (dict(ot=2), DTYPE), (dict(act=5), DTYPE),
+    (dict(act=-1), DTYPE), (dict(K=96), SHAPE), (dict(K=0), SHAPE), (dict(N=96), SHAPE), (dict(N=-64), SHAPE),
+    (dict(M=-1), SHAPE), (dict(G=0), SHAPE), (dict(G=4097), SHAPE), (dict(M=(1 << 31) - 1), SHAPE),
+    (dict(M=(1 << 31) - 2048, N=1 << 29), SHAPE),                # grid
+    (dict(ws=0), WORKSPACE), (dict(wsb=255), WORKSPACE),
+    (dict(M=0, x=0, out=0, b=0, res=0, pre=0), OK), (dict(M=0, ws=0), WORKSPACE), (dict(M=0, w=0), NULL),
+])
+def test_linear_refusals(lib, kw, status):
+    assert linear(lib, **kw) == status
+    if status:
+        assert lib.gmm_last_error()
+
+
+def linear_bwd(lib, d=A, w=A, gs=A, x=A, pre=A, act=3, M=100, K=128, N=192, G=4, dx=A, dxt=1, dw=A, dwt=1, db=A, dbt=0,
+               ws=A, wsb=BIG):
+    return lib.gmm_bf16_linear_bwd(P(d), P(w), P(gs), P(x), P(pre), act, M, K, N, G, P(dx), dxt, P(dw), dwt, P(db), dbt,
+                                   P(ws), wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(d=0), NULL), (dict(w=0), NULL), (dict(gs=0), NULL), (dict(x=0), NULL), (dict(pre=0), NULL),
+    (dict(dx=0, dw=0, db=0), NULL), (dict(d=MIS), ALIGN), (dict(w=MIS), ALIGN), (dict(x=MIS), ALIGN),
+    (dict(pre=MIS), ALIGN), (dict(pre=MIS, act=0), ALIGN), (dict(dx=MIS), ALIGN), (dict(dw=MIS), ALIGN),
+    (dict(db=MIS), ALIGN), (dict(ws=MIS), ALIGN), (dict(dxt=2), DTYPE), (dict(dwt=2), DTYPE), (dict(dbt=2), DTYPE),
+    (dict(act=9), DTYPE), (dict(K=32), SHAPE), (dict(N=100), SHAPE), (dict(G=0), SHAPE), (dict(M=-5), SHAPE),
+    (dict(G=4096, K=1 << 24, N=1 << 24), SHAPE), (dict(M=1 << 30, N=1 << 13), SHAPE),      # grids
+    (dict(ws=0), WORKSPACE), (dict(wsb=256 + 100 * 192 * 2 + 4 * 9 * 192 - 1), WORKSPACE),
+])
+def test_linear_bwd_refusals(lib, kw, status):
+    assert linear_bwd(lib, **kw) == status
+
+
+def test_workspaces_of_the_product(lib):
+    w = lib.gmm_workspace_bytes
+    assert w(gmm.OP_BF16_LINEAR, 1000, 256, 128, 4) == 256
+    # dpre, and partial sums of up to ceil(M / 32) + G + 1 items (128 rows an item from 2^25 values on)
+    assert w(gmm.OP_BF16_LINEAR_BWD, 100, 128, 192, 4) == 256 + 100 * 192 * 2 + 4 * 9 * 192
+    assert w(gmm.OP_BF16_LINEAR_BWD, 1 << 16, 512, 2048, 256) == 256 + (1 << 28) + 4 * (512 + 256 + 1) * 2048
+    assert w(gmm.OP_BF16_LINEAR_BWD, 0, 128, 192, 4) == 256
+
+
+def test_header_says_which_workspaces_hold_data(lib):
+    read = lambda f: re.sub(r"[\s*]+", " ", open(os.path.join(ROOT, "include", f)).read())
+    moe_h, gmm_h = read("gmm_moe.h"), read("gmm.h")
+    rule = re.search(r"- Workspace:.*?- `stream`", gmm_h).group()
+    for call, op in (("gmm_sort_tokens", gmm.OP_SORT_TOKENS), ("gmm_bf16_linear_bwd", gmm.OP_BF16_LINEAR_BWD)):
+        assert lib.gmm_workspace_bytes(op, 100000, 256, 128, 4) > 256
+        assert call in rule and "of its own until it has finished" in re.search(call + r" -- .*?GMM_API", moe_h).group()
+
+
 # ------------------------------------------------------------- the binding --
 
 class Lib:
@@ -160,7 +217,7 @@ def t(shape, dt, dev="cpu"):
     return torch.zeros(shape, dtype=dt, device=dev)
 
 
-T, E, k, K, M, G = 6, 32, 4, 64, 24, 8
+T, E, k, K, M, G, N = 6, 32, 4, 64, 24, 8, 128
 CALLS = {
     "gmm_route": dict(logits=(T, E, F32), k=k, bias=(E, F32), ids=(T, k, I32), weights=(T, k, F32)),
     "gmm_route_bwd": dict(dweights=(T, k, F32), logits=(T, E, BF), ids=(T, k, I32), out=(T, E, F32)),
@@ -169,9 +226,13 @@ CALLS = {
     "gmm_combine": dict(y=(M, K, BF), row_of=(T, k, I32), weights=(T, k, F32), residual=(T, K, F32), out=(T, K, F32)),
     "gmm_combine_bwd": dict(dout=(T, K, BF), y=(M, K, F32), row_of=(T, k, I32), slot_of=(M, I32), weights=(T, k, F32),
                             dy=(M, K, F32), dweights=(T, k, F32)),
+    "gmm_bf16_linear": dict(lhs=(M, K, BF), rhs=(G, K, N, BF), group_sizes=(G, I32), bias=(G, N, F32), residual=(M, N, BF),
+                            out=(M, N, BF), pre=(M, N, BF), ws=(256, U8)),
+    "gmm_bf16_linear_bwd": dict(dout=(M, N, BF), rhs=(G, K, N, BF), group_sizes=(G, I32), lhs=(M, K, BF), pre=(M, N, BF),
+                                dx=(M, K, F32), dw=(G, K, N, BF), db=(G, N, BF), ws=(1 << 16, U8)),
 }
 FIRST = dict(gmm_route="logits", gmm_route_bwd="logits", gmm_sort_tokens="ids", gmm_dispatch="x", gmm_combine="y",
-             gmm_combine_bwd="dout")
+             gmm_combine_bwd="dout", gmm_bf16_linear="lhs", gmm_bf16_linear_bwd="dout")
 
 
 def args_of(call):
@@ -219,8 +280,35 @@ def test_other_shapes_are_refused(no_launch, call, name):
         getattr(gmm, call)(**a)
 
 
+def test_the_tensors_device_is_the_current_one_of_a_call(monkeypatch):
+    """A call on tensors of a device that is not the current one switches to it for the launch."""
+    seen = []
+    now = [0]
+
+    class Switch:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.dev.index
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+    monkeypatch.setattr(moe, "_stream", lambda dev: 77)
+    monkeypatch.setattr(moe, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    fn = lambda *args: seen.append((now[0], args)) or 0
+    moe._call(None, fn, torch.device("cuda", 0), 1, 2)
+    moe._call(None, fn, torch.device("cuda", 1), 3)
+    assert seen == [(0, (1, 2, 77)), (1, (3, 77))] and now == [0]
+
+
 def test_names_are_checked(no_launch):
     with pytest.raises(ValueError, match="softplus"):
         gmm.gmm_route(t((T, E), F32), k, score="softplus")
+    with pytest.raises(ValueError, match="swish"):
+        gmm.gmm_bf16_linear(t((M, K), BF), t((G, K, N), BF), t((G,), I32), activation="swish")
+    with pytest.raises(TypeError, match="float16"):
+        gmm.gmm_bf16_linear(t((M, K), BF), t((G, K, N), BF), t((G,), I32), out_dtype=torch.float16)
     with pytest.raises(ValueError, match="tanh"):
         gmm.gmm_route_bwd(t((T, k), F32), t((T, E), F32), t((T, k), I32), score="tanh")
