@@ -14,8 +14,10 @@
 // other among the k + 1 largest are closer than twice their error is the
 // wave's choice made again in 64.  The weights and their gradient are in 32 bits.
 //
-// What bounds it: instructions, not memory.  At 65536 tokens of 256 experts, k
-// = 8, the forward reads 67 MB (14 us at a copy's 5 TB/s).
+// What bounds it: the forward's instructions (65536 tokens of 256 experts, k =
+// 8: 20 us for 71 MB, which a copy's 5 TB/s moves in 14; one wave a token took
+// 54), the gradient's memory (28.6 us for 138 MB, the copy 28; 44 with a wave a
+// token, which spent as many instructions on its lane moves).
 #include "gmm_launch.hpp"
 #include "gmm_moe.hpp"
 #include "gmm_mx8.hpp"
@@ -70,6 +72,11 @@ __device__ __forceinline__ float max_lanes(float x) {
     return __uint_as_float(over_lanes<W>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
         return __float_as_uint(max2(__uint_as_float(a), __uint_as_float(b)));
     }));
+}
+__device__ __forceinline__ float min2(float a, float b) {
+    float r;
+    asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
 template <int V>
 __device__ __forceinline__ float max_of(const float (&x)[V]) {
@@ -202,7 +209,7 @@ __device__ __forceinline__ void softmax_of(const float (&l)[V], float (&e)[V], f
         s += e[v];
     }
     s = sum_lanes<W>(s);
-    inv = s > 0.0f ? 1.0f / s : 0.0f;
+    inv = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
@@ -270,6 +277,95 @@ __device__ __forceinline__ Key choose(Key (&key)[V], int k, bool more, int& my_i
     return more ? max_lanes<W>(max_of<V>(key)) : none;
 }
 
+// Batcher's odd-even merge sort of V numbers: the pairs that are compared.
+template <int V>
+struct SortPairs {
+    int a[V * V], b[V * V], n;
+    constexpr SortPairs() : a(), b(), n(0) {
+        for (int p = 1; p < V; p *= 2)
+            for (int q = p; q >= 1; q /= 2)
+                for (int j = q % p; j + q < V; j += 2 * q)
+                    for (int i = 0; i < q && i + j + q < V; ++i)
+                        if ((i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                            a[n] = i + j;
+                            b[n] = i + j + q;
+                            ++n;
+                        }
+    }
+};
+
+// choose<W, V, float> for many rounds: each lane sorts its keys first (63
+// comparisons of two instructions for 16), so that a round looks at one key a
+// lane and the owner's others move up.  The places that sorting forgets are
+// found again at the end: lane j reads its choice's owner's keys from `row`
+// (W V words of LDS of the token's own) and takes the first that is equal, or
+// the next one where the choice before it is the same key of the same lane.
+template <int W, int V>
+__device__ __forceinline__ float choose_sorted(const float (&key)[V], int k, bool more, float* row, int& my_id,
+                                               float& my_key) {
+    static_assert(W == 16 && V % 4 == 0, "a token's lanes are a row of 16");
+    constexpr SortPairs<V> pairs;
+    const int lane = lane_id(), sub = lane % W;
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = key[v];
+#pragma unroll
+    for (int c = 0; c < pairs.n; ++c) {
+        const float hi = max2(s[pairs.a[c]], s[pairs.b[c]]), lo = min2(s[pairs.a[c]], s[pairs.b[c]]);
+        s[pairs.a[c]] = hi;
+        s[pairs.b[c]] = lo;
+    }
+    my_key = kOff;
+    int my_owner = 0;
+    for (int j = 0; j < k; ++j) {
+        const float m = max_lanes<W>(s[0]);
+        const unsigned long long held = __ballot(s[0] == m);
+        const uint32_t half = lane < 32 ? (uint32_t)held : (uint32_t)(held >> 32);
+        const int owner = __ffs((int)(half >> (lane & 16) & 0xffffu)) - 1;
+        const bool pop = sub == owner;
+#pragma unroll
+        for (int v = 0; v < V / 2 - 1; ++v) s[v] = pop ? s[v + 1] : s[v];
+        if (k > V / 2) {   // further keys only matter with more rounds than V / 2
+#pragma unroll
+            for (int v = V / 2 - 1; v < V - 1; ++v) s[v] = pop ? s[v + 1] : s[v];
+            s[V - 1] = pop ? kOff : s[V - 1];
+        }
+        my_key = sub == j ? m : my_key;
+        my_owner = sub == j ? owner : my_owner;
+    }
+    auto sync = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+    sync();   // the last token's reads
+#pragma unroll
+    for (int v = 0; v < V; v += 4)
+        *reinterpret_cast<float4*>(row + V * sub + v) = make_float4(key[v], key[v + 1], key[v + 2], key[v + 3]);
+    sync();
+    // how many choices just before this one are the same key of the same lane
+    int skip = 0;
+    const float key_before = __shfl_up(my_key, 1, W);   // by every lane: an idle one would give nothing
+    const int owner_before = __shfl_up(my_owner, 1, W);
+    const bool same = sub > 0 && sub < k && key_before == my_key && owner_before == my_owner;
+    unsigned long long run = __ballot(same);
+    if (run != 0) {
+        const uint32_t half = lane < 32 ? (uint32_t)run : (uint32_t)(run >> 32);
+        const uint32_t mine = half >> (lane & 16) & 0xffffu;        // bit j: choice j repeats choice j - 1
+        skip = __clz((int)~(mine << (31 - sub)));                   // ones from bit sub down
+    }
+    int at = -1;
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(row + V * my_owner + v);
+        const float x[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool hit = x[i] == my_key;
+            at = hit && skip == 0 ? v + i : at;
+            skip -= hit ? 1 : 0;
+        }
+    }
+    my_id = my_key > kOff ? V * my_owner + at : -1;
+    return more ? max_lanes<W>(s[0]) : kOff;
+}
+
 // The choice of token t by keys in 64 bits, 64 lanes of VX experts; choice j in
 // lane j.  top: the token's largest logit.
 template <int VX, bool BF16>
@@ -300,9 +396,19 @@ __device__ __forceinline__ int exact_choice(const RouteArgs& a, int64_t t, float
 template <int W, int V, bool BF16, bool BIAS>
 __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kernel(const RouteArgs a, int32_t* __restrict__ ids,
                                                     float* __restrict__ weights) {
+    // Sorting a lane's keys pays from five rounds on (65536 tokens, 256 experts,
+    // scores of a softmax, us by rounds alone / sorted: k 4 17.9 / 18.1, 5 19.9 /
+    // 18.6, 8 24.8 / 19.9, 16 39.0 / 27.8).
+    constexpr bool kSorts = W == 16 && V >= 8;
+    __shared__ __attribute__((aligned(16))) float rows[kSorts ? 256 / W : 1][kSorts ? W * V : 4];
     const int lane = lane_id(), sub = lane % W, E = a.E, k = a.k;
     const bool vec = E % 4 == 0;
     const int64_t stride = (int64_t)gridDim.x * (256 / W);
+    auto pick = [&](float (&key)[V], bool more, int& my_id, float& my_key) {
+        if constexpr (kSorts)
+            if (k >= 5) return choose_sorted<W, V>(key, k, more, rows[threadIdx.x / W], my_id, my_key);
+        return choose<W, V, float>(key, k, more, my_id, my_key);
+    };
     // whole waves stay together: the last tokens' lanes without one repeat the last
     for (int64_t t0 = (int64_t)blockIdx.x * (256 / W) + (threadIdx.x / 64) * (64 / W); t0 < a.T; t0 += stride) {
         const int64_t t = min(t0 + lane / W, a.T - 1);
@@ -314,7 +420,7 @@ __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kerne
         if constexpr (!BIAS) {
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] = l[v];
-            choose<W, V, float>(s, k, false, my_id, my_l);
+            pick(s, false, my_id, my_l);
         } else {
             float b[V];
             load_row<V, false>(a.bias, 0, sub * V, E, vec, b);
@@ -325,7 +431,7 @@ __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kerne
                 s[v] = l[v] > kOff && z > kOff ? z : kOff;
             }
             float my_key;
-            const float next = choose<W, V, float>(s, k, true, my_id, my_key);
+            const float next = pick(s, true, my_id, my_key);
             // Twice the error of a key.  A sigmoid is off by less than 4 u of it (u = 2^-24: its exponential by (2 |l|
             // + 2) u, of which s (1 - s) counts, the sum and the reciprocal); a softmax, d below the top, by (2 d + 80)
             // u of it (the differences and products of d, a sum of at most 70 roundings), so by less than 2^-17 of
@@ -357,9 +463,60 @@ __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kerne
     }
 }
 
+// Where the gradient's lanes have their experts: place v of lane `sub` (the
+// order does not matter here, so a group's lanes read and write whole lines).
+template <int W, int V>
+__device__ __forceinline__ int expert_at(int sub, int v) { return V < 4 ? sub * V + v : 4 * W * (v / 4) + 4 * sub + v % 4; }
+
+// The choices' values added up at their experts: x[v] of expert_at(v) from g of
+// the expert id (or -1) in lane j < k, by way of `row` in LDS, W V words of the
+// token's own.  Ids that a router made differ, and one write each does; where
+// some are equal (found by writing the lane and reading it back) the lanes add
+// one after the other.
+template <int W, int V>
+__device__ __forceinline__ void scatter_choices(int id, float g, int k, float* row, float (&x)[V]) {
+    const int sub = lane_id() % W;
+    int* owner = reinterpret_cast<int*>(row);
+    auto sync = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+    sync();   // the last token's reads
+#pragma unroll
+    for (int v = 0; v < V; v += V < 4 ? 1 : 4) {
+        if constexpr (V < 4) row[expert_at<W, V>(sub, v)] = 0.0f;
+        else *reinterpret_cast<float4*>(row + expert_at<W, V>(sub, v)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    sync();
+    if (id >= 0) owner[id] = sub;
+    sync();
+    const bool shared = id >= 0 && owner[id] != sub;
+    sync();
+    if (__ballot(shared) == 0) {
+        if (id >= 0) row[id] = g;
+    } else {
+        if (id >= 0) row[id] = 0.0f;
+        for (int j = 0; j < k; ++j) {
+            sync();
+            if (sub == j && id >= 0) row[id] += g;
+        }
+    }
+    sync();
+#pragma unroll
+    for (int v = 0; v < V; v += V < 4 ? 1 : 4) {
+        if constexpr (V < 4) {
+            x[v] = row[expert_at<W, V>(sub, v)];
+        } else {
+            const float4 d = *reinterpret_cast<const float4*>(row + expert_at<W, V>(sub, v));
+            x[v] = d.x;
+            x[v + 1] = d.y;
+            x[v + 2] = d.z;
+            x[v + 3] = d.w;
+        }
+    }
+}
+
 template <int W, int V, bool BF16, bool OUT_BF16>
 __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const float* __restrict__ dweights,
                                                         const int32_t* __restrict__ ids, void* dlogits) {
+    __shared__ __attribute__((aligned(16))) float rows[256 / W][W * V];
     const int lane = lane_id(), sub = lane % W, E = a.E, k = a.k;
     const bool vec = E % 4 == 0;
     const int64_t stride = (int64_t)gridDim.x * (256 / W);
@@ -378,12 +535,20 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
         // what choice j adds at its expert: its part of the gradient itself, or
         // (dense) its weight's gradient
         const bool dense = !a.sigmoid && !a.normalize;
-        float g = dw, dot = 0.0f, s[V], inv = 0.0f;
+        float g = dw, dot = 0.0f, s[V], d[V];
         if (dense) {
-            float l[V], top;
-            load_logits<V, BF16>(a.logits, t * E, sub * V, E, vec, l);
+            float l[V], top, inv;
+#pragma unroll
+            for (int v = 0; v < V; v += V < 4 ? 1 : 4) {
+                const int e = expert_at<W, V>(sub, v);
+                if constexpr (V < 4) load_logits<1, BF16>(a.logits, t * E, e, E, vec, reinterpret_cast<float(&)[1]>(l[v]));
+                else load_logits<4, BF16>(a.logits, t * E, e, E, vec, reinterpret_cast<float(&)[4]>(l[v]));
+            }
             softmax_of<W, V>(l, s, top, inv);
             dot = sum_lanes<W>(on ? exp_of(lj - top) * inv * dw : 0.0f);
+            const float c = a.scale * inv;
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] *= c;
         } else if (a.normalize) {
             const float q = chosen_share<W>(lj, a.sigmoid);
             g = a.scale * q * (dw - sum_lanes<W>(q * dw));
@@ -391,47 +556,33 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
         } else {
             g = on ? a.scale * dw * sigmoid(lj) * (1.0f / (1.0f + expf(lj))) : 0.0f;
         }
-        float d[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) d[v] = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            if constexpr (W == 64) {
-                const int e = lane_value(id, j);
-                if (e < 0) continue;
-                const float gj = lane == e / V ? __int_as_float(lane_value(__float_as_int(g), j)) : 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (e % V == v) d[v] += gj;   // a scalar condition
-            } else {
-                const int e = __shfl(id, lane - sub + j, 64);
-                const float gj = __shfl(g, lane - sub + j, 64);
-#pragma unroll
-                for (int v = 0; v < V; ++v) d[v] += e == sub * V + v ? gj : 0.0f;
-            }
-        }
+        scatter_choices<W, V>(id, g, k, rows[threadIdx.x / W], d);
         if (dense) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) d[v] = a.scale * (s[v] * inv) * (d[v] - dot);
+            for (int v = 0; v < V; ++v) d[v] = s[v] * (d[v] - dot);
         }
         if (!mine) continue;
-        const int64_t o = t * E + sub * V;
-        if (V >= 4 && vec) {
+        const int64_t o = t * E;
 #pragma unroll
-            for (int v = 0; v + 3 < V; v += 4) {
-                if (sub * V + v >= E) break;
-                if constexpr (OUT_BF16)
-                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(dlogits) + o + v) =
-                        make_uint2(pack_rne(d[v], d[v + 1]), pack_rne(d[v + 2], d[v + 3]));
-                else
-                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(dlogits) + o + v) =
-                        make_float4(d[v], d[v + 1], d[v + 2], d[v + 3]);
-            }
-        } else {
+        for (int v = 0; v < V; v += V < 4 ? 1 : 4) {
+            const int e = expert_at<W, V>(sub, v);
+            if (e >= E) break;
+            if (V >= 4 && vec) {
+                if constexpr (V >= 4) {
+                    if constexpr (OUT_BF16)
+                        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(dlogits) + o + e) =
+                            make_uint2(pack_rne(d[v], d[v + 1]), pack_rne(d[v + 2], d[v + 3]));
+                    else
+                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(dlogits) + o + e) =
+                            make_float4(d[v], d[v + 1], d[v + 2], d[v + 3]);
+                }
+            } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (sub * V + v >= E) break;
-                if constexpr (OUT_BF16) reinterpret_cast<uint16_t*>(dlogits)[o + v] = (uint16_t)pack_rne(d[v], d[v]);
-                else reinterpret_cast<float*>(dlogits)[o + v] = d[v];
+                for (int i = 0; i < (V < 4 ? 1 : 4); ++i) {
+                    if (e + i >= E) break;
+                    if constexpr (OUT_BF16) reinterpret_cast<uint16_t*>(dlogits)[o + e + i] = (uint16_t)pack_rne(d[v + i], d[v + i]);
+                    else reinterpret_cast<float*>(dlogits)[o + e + i] = d[v + i];
+                }
             }
         }
     }
@@ -439,7 +590,9 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
 
 // Lanes and experts a lane for E experts.  16 lanes a token (four tokens a
 // wave) share the lane moves and ballots of a round between four tokens; 64
-// give the shortest rounds and the most waves.
+// give the shortest rounds and the most waves, which few tokens need (below 8192
+// tokens of 256 experts both take the time of a launch, 65536 47.2 / 25.3 us
+// before a lane's keys were sorted).
 template <typename F>
 hipError_t with_lanes(int E, int k, bool many, F f) {
     using std::integral_constant;
@@ -447,6 +600,7 @@ hipError_t with_lanes(int E, int k, bool many, F f) {
     constexpr integral_constant<int, 64> w64;
     if (E <= 16) return f(w16, integral_constant<int, 1>{});
     if (E <= 64) return k <= 16 ? f(w16, integral_constant<int, 4>{}) : f(w64, integral_constant<int, 1>{});
+    if (E <= 128 && k <= 16 && many) return f(w16, integral_constant<int, 8>{});
     if (E <= 256) return k <= 16 && many ? f(w16, integral_constant<int, 16>{}) : f(w64, integral_constant<int, 4>{});
     if (E <= 512) return f(w64, integral_constant<int, 8>{});
     if (E <= 1024) return f(w64, integral_constant<int, 16>{});
@@ -479,7 +633,7 @@ hipError_t launch_route(const RouteArgs& a, bool logits_bf16, int32_t* ids, floa
 
 hipError_t launch_route_bwd(const RouteArgs& a, bool logits_bf16, const float* dweights, const int32_t* ids,
                             void* dlogits, bool out_bf16, hipStream_t stream) {
-    return with_lanes(a.E, a.k, false, [&](auto w, auto v) {
+    return with_lanes(a.E, a.k, a.T >= kManyTokens, [&](auto w, auto v) {
         constexpr int W = decltype(w)::value, V = decltype(v)::value;
         const dim3 grid = token_grid(a.T, W), block(256);
         if (logits_bf16) {

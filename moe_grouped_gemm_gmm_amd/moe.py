@@ -46,11 +46,12 @@ def _out(t: Optional[torch.Tensor], shape, dtype: torch.dtype, dtypes: tuple, na
     if t is None:
         if dtype not in dtypes:
             raise TypeError("%s has dtype %s" % (name, dtype))
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = _empty(*shape, dtype=dtype, device=dev)   # sizes one by one: parsed faster than a tuple (1.3 us, 1.6)
         return t, t.data_ptr()
     return t, _arg(t, shape, dtypes, name, dev)
 
 
+_empty = torch.empty
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -62,7 +63,8 @@ def _call(lib, fn, dev: torch.device, *args) -> None:
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, stream)
-    _check(lib, rc)
+    if rc:
+        _check(lib, rc)
 
 
 @functools.lru_cache(maxsize=512)
@@ -75,15 +77,16 @@ def _work(ws: Optional[torch.Tensor], dev: torch.device, op: int, M: int, K: int
     if ws is None:
         need = _ws_bytes(op, M, K, N, G)
         if need > 256:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = _empty(need, dtype=torch.uint8, device=dev)
             return ws, ws.data_ptr(), need
     return (ws,) + ffn._status(ws, dev)
 
 
 def _named(value: str, table: dict, what: str) -> int:
-    if value not in table:
+    code = table.get(value)
+    if code is None:
         raise ValueError("%s %r is not one of %s" % (what, value, ", ".join(sorted(table))))
-    return table[value]
+    return code
 
 
 def gmm_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",

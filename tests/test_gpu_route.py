@@ -80,6 +80,39 @@ def test_choice_weights_and_gradient(T, E, k, dt, bias):
         check_bwd(l, ids, score, normalize, scale, None if i < 2 else (BF if dt == F32 else F32))
 
 
+# many tokens: four a wave, and from five choices on by sorted lanes
+@pytest.mark.parametrize("T,E,k", [(8192, 256, 8), (8195, 250, 16), (8193, 128, 6), (8200, 97, 4), (8192, 130, 5), (8199, 256, 17),
+                                   (8192, 65, 9), (9001, 60, 12), (8194, 20, 1)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_many_tokens(T, E, k, bias):
+    for i, (score, normalize) in enumerate(FORMS):
+        l, b = inputs(T, E, [F32, BF][i % 2], T + 7 * E + i)     # bf16: many equal logits
+        l[::7, E // 2] = float("-inf")
+        l[5] = float("-inf")
+        ids = check_fwd(l, k, b if bias else None, score, normalize, 1.0)
+        if T < 8200:
+            check_bwd(l[:300], ids[:300].clone(), score, normalize, 1.0, None)
+        # the gradient of many tokens is that of few
+        dw = torch.randn(T, k, device=DEV)
+        whole = gmm.gmm_route_bwd(dw, l.to(DEV), ids, score=score, normalize=normalize, out_dtype=F32)
+        part = gmm.gmm_route_bwd(dw[-1000:].clone(), l[-1000:].to(DEV), ids[-1000:].clone(), score=score, normalize=normalize,
+                                 out_dtype=F32)
+        tol = (8 * span(l.double().numpy()) + 600) * U * dw[-1000:].abs().max()
+        assert ((whole[-1000:] - part).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(8192, 256, 8), (8192, 128, 7), (8192, 256, 16), (70, 256, 8)])
+@pytest.mark.parametrize("levels", [1, 2, 5])
+def test_equal_keys_of_many_tokens(T, E, k, levels):
+    """Few different logits: most choices are the same key, many of the same lane."""
+    l = torch.randint(0, levels, (T, E), generator=torch.Generator().manual_seed(E + levels)).float()
+    check_fwd(l, k, None, "softmax", True, 1.0)
+    check_fwd(l.to(BF), k, torch.zeros(E), "sigmoid", True, 1.0)
+    l[:, 3:] = float("-inf")
+    ids = check_fwd(l, k, None, "softmax", True, 1.0)
+    assert (ids[:, 3:] == -1).all()
+
+
 @pytest.mark.parametrize("score,normalize", FORMS)
 @pytest.mark.parametrize("E", [8, 60, 256, 700])
 def test_equal_keys_go_to_the_lower_index(score, normalize, E):
@@ -171,6 +204,14 @@ def test_gradient_of_bad_and_repeated_ids():
         dw = torch.randn(6, 3, device=DEV)
         a = gmm.gmm_route_bwd(dw, l.to(DEV), ids.to(DEV), score=score)
         assert torch.equal(a, gmm.gmm_route_bwd(dw, l.to(DEV), clean_ids.to(DEV), score=score))
+        for E, many in ((8, 1), (40, 1), (200, 1), (200, 2000), (600, 1), (2000, 1)):
+            # the same few experts at every width, for few tokens and for many
+            wide = torch.cat([l, torch.full((6, 2000), float("-inf"))], 1)[:, :E].repeat(many, 1)
+            i = torch.where(clean_ids < E, clean_ids, torch.full_like(ids, -1)).repeat(many, 1)
+            check_bwd(wide[:12], i[:12], score, False, 1.0, None)
+            d = dw.repeat(many, 1)
+            g = gmm.gmm_route_bwd(d, wide.to(DEV), i.to(DEV), score=score)
+            assert torch.equal(g[:6], g[-6:]) and torch.equal(g, gmm.gmm_route_bwd(d, wide.to(DEV), i.to(DEV), score=score))
 
 
 @pytest.mark.parametrize("score,normalize", FORMS)
