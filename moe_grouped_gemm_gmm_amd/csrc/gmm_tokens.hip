@@ -28,7 +28,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRun = 1024;        // slots of a run, the least
 constexpr int kMaxRuns = 1024;
-constexpr int kSumRuns = 64;      // up to here every workgroup adds up the runs before its own
+constexpr int kSumRuns = 64;      // up to here (and 256 experts) every workgroup adds up the runs before its own
 constexpr int kOneRun = 4096;     // up to here (and 1024 experts) one workgroup does everything
 
 struct Runs {
@@ -65,33 +65,31 @@ __global__ __launch_bounds__(256) void count_kernel(const int32_t* __restrict__ 
 }
 
 // counts[run, g] -> slots of expert g in earlier runs, and totals[g] behind
-// them: 64 experts a workgroup, each of 16 waves a sixteenth of the runs.
+// them: 16 experts a workgroup, each of 64 threads a sixty-fourth of the runs,
+// so that 512 runs (524288 slots) are one batch of loads a thread and stay in
+// registers (4.4 us; with a quarter of the workgroups and two passes 7).
 __global__ __launch_bounds__(1024) void scan_kernel(int32_t* __restrict__ counts, int runs, int G) {
-    __shared__ int part[16][64];
-    const int lane = lane_id(), wave = threadIdx.x >> 6, g = blockIdx.x * 64 + lane;
-    const int per = (runs + 15) / 16, lo = min(runs, wave * per), hi = min(runs, lo + per);
-    int sum = 0;
-    if (g < G) {
-#pragma unroll 8
-        for (int r = lo; r < hi; ++r) sum += counts[(int64_t)r * G + g];
+    __shared__ int part[64][16];
+    const int across = threadIdx.x & 15, seg = threadIdx.x >> 4, g = blockIdx.x * 16 + across;
+    const int per = (runs + 63) / 64, lo = min(runs, seg * per), hi = min(runs, lo + per);
+    const bool mine = g < G && lo < hi;
+    constexpr int kHeld = kMaxRuns / 64;
+    int c[kHeld], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        c[i] = mine && lo + i < hi ? counts[(int64_t)(lo + i) * G + g] : 0;
+        sum += c[i];
     }
-    part[wave][lane] = sum;
+    part[seg][across] = sum;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < wave; ++w) before += part[w][lane];
-    if (g >= G) return;
-    for (int r = lo; r < hi; r += 8) {
-        int c[8];
+    for (int w = 0; w < seg; ++w) before += part[w][across];
+    if (g < G && seg == 63) counts[(int64_t)runs * G + g] = before + sum;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = counts[(int64_t)min(r + i, hi - 1) * G + g];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (r + i < hi) {
-                counts[(int64_t)(r + i) * G + g] = before;
-                before += c[i];
-            }
+    for (int i = 0; i < kHeld; ++i) {
+        if (mine && lo + i < hi) counts[(int64_t)(lo + i) * G + g] = before;
+        before += c[i];
     }
-    if (wave == 15) counts[(int64_t)runs * G + g] = before;
 }
 
 enum Before { kAlone = 0, kSum = 1, kScanned = 2 };   // one run; runs added up here; runs added up by scan_kernel
@@ -119,7 +117,8 @@ __global__ __launch_bounds__(64 * NW) void place_kernel(const int32_t* __restric
     }
     __syncthreads();
     // the runs before and all runs of every expert, PARTS threads an expert
-    constexpr int PARTS = BEFORE == kSum && NT > GMAX ? NT / GMAX : 1;
+    constexpr int PARTS = BEFORE == kSum ? NT / GMAX : 1;
+    static_assert(BEFORE != kSum || PARTS > 1, "several threads an expert");
     __shared__ int part_before[PARTS][PARTS > 1 ? GMAX : 1], part_total[PARTS][PARTS > 1 ? GMAX : 1];
     if constexpr (PARTS > 1) {
         const int g = tid % GMAX, q = tid / GMAX;
@@ -150,12 +149,6 @@ __global__ __launch_bounds__(64 * NW) void place_kernel(const int32_t* __restric
                 for (int q = 0; q < PARTS; ++q) {
                     before[i] += part_before[q][g];
                     total[i] += part_total[q][g];
-                }
-            } else if constexpr (BEFORE == kSum) {
-                for (int r = 0; r < runs; ++r) {
-                    const int c = counts[(int64_t)r * G + g];
-                    total[i] += c;
-                    before[i] += r < (int)blockIdx.x ? c : 0;
                 }
             } else {
                 before[i] = counts[(int64_t)blockIdx.x * G + g];
@@ -514,16 +507,15 @@ hipError_t launch_sort_tokens(const int32_t* ids, int n, int first, int G, int M
         hipLaunchKernelGGL((count_kernel<4096>), dim3((unsigned)r.count), dim3(256), 0, stream, ids, n, first, G, r.slots, counts);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (r.count <= kSumRuns) {
-        if (G <= 256)
-            return place<16, 256, kSum>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
-        return place<4, 4096, kSum>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
-    }
-    hipLaunchKernelGGL(scan_kernel, dim3((unsigned)((G + 63) / 64)), dim3(1024), 0, stream, counts, r.count, G);
+    if (r.count <= kSumRuns && G <= 256)
+        return place<16, 256, kSum>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
+    hipLaunchKernelGGL(scan_kernel, dim3((unsigned)((G + 15) / 16)), dim3(1024), 0, stream, counts, r.count, G);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (G <= 256)
         return place<16, 256, kScanned>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
+    if (G <= 1024)
+        return place<16, 1024, kScanned>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
     return place<4, 4096, kScanned>(ids, n, first, G, M, r, counts, group_sizes, row_of, slot_of, status, stream);
 }
 
