@@ -56,7 +56,9 @@ __device__ __forceinline__ float sum_lanes(float x) {
     }));
 }
 // Maxima of numbers (no NaN gets here).  In asm: fmaxf also has to quieten
-// signalling NaNs, an instruction more for each operand of unknown origin.
+// signalling NaNs, an instruction more for each operand of unknown origin.  The
+// compiler takes the result for a vector instruction's and keeps the two wait
+// states before a lane move reads it.
 __device__ __forceinline__ float max2(float a, float b) {
     float r;
     asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
