@@ -395,6 +395,19 @@ __device__ __forceinline__ int exact_choice(const RouteArgs& a, int64_t t, float
     return id;
 }
 
+// Keys score + bias in 32 bits, kOff where the expert is off.  key: the
+// exponentials of a softmax (not read for a sigmoid).
+template <int V>
+__device__ __forceinline__ void biased_keys(const RouteArgs& a, const float (&l)[V], const float (&b)[V], float inv,
+                                            float (&key)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float x = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_of(-l[v])) : key[v] * inv;
+        const float z = x + b[v] + 0.0f;
+        key[v] = l[v] > kOff && z > kOff ? z : kOff;
+    }
+}
+
 template <int W, int V, bool BF16, bool BIAS>
 __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kernel(const RouteArgs a, int32_t* __restrict__ ids,
                                                     float* __restrict__ weights) {
@@ -426,22 +439,45 @@ __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kerne
         } else {
             float b[V];
             load_row<V, false>(a.bias, 0, sub * V, E, vec, b);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float x = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_of(-l[v])) : s[v] * inv;
-                const float z = x + b[v] + 0.0f;
-                s[v] = l[v] > kOff && z > kOff ? z : kOff;
-            }
+            biased_keys<V>(a, l, b, inv, s);
             float my_key;
             const float next = pick(s, true, my_id, my_key);
             // Twice the error of a key.  A sigmoid is off by less than 4 u of it (u = 2^-24: its exponential by (2 |l|
             // + 2) u, of which s (1 - s) counts, the sum and the reciprocal); a softmax, d below the top, by (2 d + 80)
             // u of it (the differences and products of d, a sum of at most 70 roundings), so by less than 2^-17 of
             // the top's score, which is inv; score + bias by half a step.
-            const float after_lane = __shfl(my_key, (lane & ~(W - 1)) | ((sub + 1) & (W - 1)), 64);
-            const float after = sub + 1 < k ? after_lane : next;
+            const int group = lane & ~(W - 1), beside = group | ((sub + 1) & (W - 1));
+            const float after_lane = __shfl(my_key, beside, 64), after = sub + 1 < k ? after_lane : next;
             const float tol = (a.sigmoid ? 0x1p-20f : 0x1p-16f * inv) + 0x1p-23f * (fabsf(my_key) + fabsf(after));
-            const bool close = sub < k && my_id >= 0 && after > kOff && !(my_key - after > tol);
+            // Equal logits with equal biases are the same key in 64 bits too, and in the order of their indices.
+            my_l = my_id >= 0 ? clean(logit_at<BF16>(a.logits, t * E + my_id)) : kOff;
+            const float my_b = my_id >= 0 ? a.bias[my_id] : 0.0f;
+            const float l_after = __shfl(my_l, beside, 64), b_after = __shfl(my_b, beside, 64);
+            bool close = sub < k && my_id >= 0 && after > kOff && !(my_key - after > tol);
+            const bool edge = close && sub == k - 1;   // against keys that were not chosen: all that are as near
+            close = close && !edge && !(my_l == l_after && my_b == b_after);
+            if (__ballot(edge) != 0) {
+                const int last = group + k - 1;
+                const float m = __shfl(my_key, last, 64), lm = __shfl(my_l, last, 64), bm = __shfl(my_b, last, 64),
+                            tm = __shfl(tol, last, 64);
+                const bool asked = __shfl((int)edge, last, 64) != 0;   // by every lane: an idle one would give nothing
+                bool other = false;
+                constexpr int C = V < 4 ? V : 4;
+#pragma unroll 1
+                for (int v = 0; v < V; v += C) {   // read again: the registers are the common path's
+                    const int e = sub * V + v;
+                    float x[C], key[C], bias[C];
+                    load_logits<C, BF16>(a.logits, t * E, e, E, vec, x);
+                    load_row<C, false>(a.bias, 0, e, E, vec, bias);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) key[c] = exp_of(x[c] - top);
+                    biased_keys<C>(a, x, bias, inv, key);
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        other = other || (key[c] > kOff && !(fabsf(key[c] - m) > tm) && !(x[c] == lm && bias[c] == bm));
+                }
+                close = close || (asked && other);
+            }
             constexpr unsigned long long kGroup = W == 64 ? ~0ull : (1ull << (W % 64)) - 1ull;
             unsigned long long open = __ballot(close);
             while (open != 0) {   // one token after the other, by the whole wave
@@ -450,9 +486,9 @@ __global__ __launch_bounds__(256, BIAS && W * V <= 256 ? 4 : 1) void route_kerne
                 const int id = exact_choice<(W * V + 63) / 64, BF16>(
                     a, min(t0 + base / W, a.T - 1), __int_as_float(lane_value(__float_as_int(top), base)));
                 const int mine = __shfl(id, sub, 64);
-                my_id = (lane & ~(W - 1)) == base ? mine : my_id;
+                my_id = group == base ? mine : my_id;
+                my_l = my_id >= 0 ? clean(logit_at<BF16>(a.logits, t * E + my_id)) : kOff;
             }
-            my_l = my_id >= 0 ? clean(logit_at<BF16>(a.logits, t * E + my_id)) : kOff;
         }
         float w;
         if (a.normalize) w = chosen_share<W>(my_l, a.sigmoid);

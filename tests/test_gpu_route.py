@@ -189,6 +189,22 @@ def test_choice_between_scores_that_32_bits_cannot_tell_apart():
     check_fwd(l, 3, torch.full((E,), 0.25), "softmax", True, 1.0)
 
 
+@pytest.mark.parametrize("T,E,k", [(40, 256, 8), (8192, 256, 8), (8192, 128, 4), (50, 60, 6), (20, 700, 9), (8192, 256, 1)])
+def test_ties_at_the_edge_of_the_choice(T, E, k):
+    """Keys with a bias around the last chosen one: equal logits and biases (the same key), equal keys of different
+    logits and biases, and keys that only 64 bits tell apart, among experts on both sides of the edge."""
+    g = torch.Generator().manual_seed(T + E + k)
+    l = torch.randint(-3, 4, (T, E), generator=g).float() * 0.5
+    for score in ("sigmoid", "softmax"):
+        for b in (torch.zeros(E), torch.randint(0, 3, (E,), generator=g).float() * 0.125,
+                  torch.where(torch.rand(E, generator=g) < 0.5, 0.0, 2.0 ** -24), torch.full((E,), 2.0 ** 20)):
+            check_fwd(l, k, b, score, True, 1.0)
+            check_fwd(l.to(BF), k, b, score, False, 1.0)
+    near = l + torch.randint(-1, 2, (T, E), generator=g).float() * 2.0 ** -22      # next to each other
+    check_fwd(near, k, torch.zeros(E), "sigmoid", True, 1.0)
+    check_fwd(near, k, torch.zeros(E), "softmax", True, 1.0)
+
+
 def test_gradient_of_bad_and_repeated_ids():
     """Ids outside the experts take no part; an expert named twice gets both gradients."""
     l, _ = inputs(6, 40, F32, 31)
@@ -245,6 +261,37 @@ def test_outputs_given_and_rows_left_alone():
     dl = torch.full((72, 60), -7.0, device=DEV)
     gmm.gmm_route_bwd(torch.ones(70, 6, device=DEV), l.to(DEV), a, out=dl[:70])
     assert (dl[70:] == -7).all() and not (dl[:70] == -7).any()
+
+
+@pytest.mark.parametrize("T,E,k,dt", [((1 << 22) + 5, 300, 3, BF), ((1 << 24) + 37, 8, 2, BF), ((1 << 24) + 9, 65, 5, BF)])
+def test_more_tokens_than_the_grid(T, E, k, dt):
+    """Workgroups take several tokens one after the other: the last tokens are those of a call of their own."""
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 60 GB of free device memory")
+    l = torch.randn(T, E, device=DEV, dtype=dt)
+    l[-9000:] = torch.randn(9000, E, generator=torch.Generator().manual_seed(1)).to(DEV, dt)
+    b = torch.randn(E, device=DEV) * 0.1
+    for how in (dict(normalize=False), dict(bias=b, score="sigmoid")):
+        ids, w = gmm.gmm_route(l, k, **how)
+        few = gmm.gmm_route(l[-9000:].clone(), k, **how)
+        assert torch.equal(ids[-9000:], few[0]) and torch.equal(w[-9000:], few[1])
+        how.pop("bias", None)
+        dw = torch.ones(T, k, device=DEV)
+        dw[-9000:] = torch.randn(9000, k, device=DEV)
+        g = gmm.gmm_route_bwd(dw, l, ids, **how)
+        assert torch.equal(g[-9000:], gmm.gmm_route_bwd(dw[-9000:].clone(), l[-9000:].clone(), ids[-9000:].clone(), **how))
+
+
+def test_gradient_of_no_choice_is_not_looked_at():
+    l, _ = inputs(9000, 40, F32, 71)
+    l[::3] = float("-inf")
+    for score, normalize in FORMS:
+        for T in (30, 9000):
+            ids, _ = gmm.gmm_route(l[:T].to(DEV), 4, score=score, normalize=normalize)
+            dw = torch.ones(T, 4, device=DEV)
+            dw[ids < 0] = float("nan")
+            g = gmm.gmm_route_bwd(dw, l[:T].to(DEV), ids, score=score, normalize=normalize)
+            assert torch.isfinite(g).all() and (g[::3] == 0).all()
 
 
 def test_no_tokens():

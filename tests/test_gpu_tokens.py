@@ -227,6 +227,31 @@ def test_two_streams_with_workspaces_of_their_own():
         assert all(torch.equal(a, b) for a, b in zip(o, want[n % 3]))
 
 
+@pytest.mark.parametrize("T,K", [((1 << 20) + 77, 1032), ((1 << 22) + 133, 8)])
+def test_more_tokens_than_the_grid(T, K):
+    """Workgroups take several tokens one after the other, and runs of slots grow past 1024."""
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB of free device memory")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    ids = torch.randint(-1, 5, (T, 1), generator=g, device=DEV).to(I32)
+    gs, row_of, slot_of = gmm.gmm_sort_tokens(ids, 5)
+    order = torch.argsort(torch.where(ids[:, 0] < 0, 5, ids[:, 0].long()), stable=True)
+    used = int((ids >= 0).sum())
+    assert int(gs.sum()) == used and torch.equal(slot_of[:used].long(), order[:used]) and (slot_of[used:] == -1).all()
+    assert torch.equal(row_of[order[:used], 0].long(), torch.arange(used, device=DEV)) and (row_of[ids < 0] == -1).all()
+    x = torch.randn(T, K, generator=g, device=DEV, dtype=BF)
+    rows = gmm.gmm_dispatch(x, row_of, slot_of)
+    assert torch.equal(rows[:used], x[order[:used]]) and not rows[used:].any()
+    w = torch.full((T, 1), 0.5, device=DEV)
+    back = gmm.gmm_combine(rows, row_of, weights=w)
+    assert torch.equal(back, torch.where(ids >= 0, x * 0.5, torch.zeros_like(x)))
+    dy, dw = gmm.gmm_combine_bwd(x, rows, row_of, slot_of, w)
+    assert torch.equal(dy[:used], x[order[:used]] * 0.5) and not dy[used:].any()
+    want = (x.double() ** 2).sum(1)
+    assert ((dw[:, 0].double() - torch.where(ids[:, 0] >= 0, want, 0.0)).abs() <= (K / 64 + 32) * U * want).all()
+
+
 def test_rows_past_32_bits_of_bytes_and_elements():
     """A sorted buffer of more than 2^32 elements: rows at its far end."""
     K, M = 65536, 65600
