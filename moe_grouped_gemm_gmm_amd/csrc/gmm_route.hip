@@ -16,7 +16,7 @@
 //
 // What bounds it: the forward's instructions (65536 tokens of 256 experts, k =
 // 8: 20 us for 71 MB, which a copy's 5 TB/s moves in 14; one wave a token took
-// 54), the gradient's memory (28.6 us for 138 MB, the copy 28; 44 with a wave a
+// 54), the gradient's memory (25 us for 138 MB, the copy 28; 44 with a wave a
 // token, which spent as many instructions on its lane moves).
 #include "gmm_launch.hpp"
 #include "gmm_moe.hpp"
@@ -608,11 +608,11 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(const RouteArgs a, const
             if (V >= 4 && vec) {
                 if constexpr (V >= 4) {
                     if constexpr (OUT_BF16)
-                        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(dlogits) + o + e) =
-                            make_uint2(pack_rne(d[v], d[v + 1]), pack_rne(d[v + 2], d[v + 3]));
+                        store_out(reinterpret_cast<uint16_t*>(dlogits) + o + e,
+                                  make_uint2(pack_rne(d[v], d[v + 1]), pack_rne(d[v + 2], d[v + 3])));
                     else
-                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(dlogits) + o + e) =
-                            make_float4(d[v], d[v + 1], d[v + 2], d[v + 3]);
+                        store_out(reinterpret_cast<float*>(dlogits) + o + e,
+                                  make_float4(d[v], d[v + 1], d[v + 2], d[v + 3]));
                 }
             } else {
 #pragma unroll
