@@ -1165,7 +1165,7 @@ __device__ __forceinline__ void ws_read(v8bf (&ga)[3], v8bf (&gb)[2], unsigned a
 constexpr int kWsRows = 160, kWsCols = 256, kWsStages = 3, kWsThreads = 768;
 constexpr int kWsSliceA = kWsRows * 64, kWsSliceB = kWsCols * 64, kWsStage = kWsSliceA + kWsSliceB;   // elements
 constexpr int kWsBytes = kWsStages * kWsStage * 2;
-static_assert(kWsBytes <= 163840 - 1024, "the ring fits the LDS");
+static_assert(kWsBytes <= 163840 - 2048, "the ring fits the LDS");
 
 // Stages rows of E in one stage of the ring and stores them, RB 32-row blocks
 // (of the item's five) a round, two barriers a round: VAL(i, b, q, v) gives the
@@ -1295,13 +1295,14 @@ template <int MODE, bool OUT_BF16, int SAVE>
 __device__ __forceinline__ void ws_body(const FfnArgs& a) {
     static_assert(MODE == kGated || MODE == kBwdX || MODE == kLinear, "forward and dX");
     constexpr int S = kWsStages, kSt = kWsStage;
-    constexpr bool kBTr = MODE != kBwdX;
+    constexpr bool kBTr = MODE != kBwdX, kTouch = MODE == kLinear && OUT_BF16;
     using E = typename std::conditional<OUT_BF16, uint16_t, float>::type;
     // barriers of an item's end
     constexpr int kEndBarriers = MODE == kLinear ? 2 * kLinRounds : 2 * WsRounds<E, MODE == kGated ? 128 : 256>::kRounds +
                                  (SAVE == kSaveBf16 ? 4 * WsRounds<uint16_t, 128>::kRounds : SAVE == kSaveMx8 ? 2 : 0);
     __shared__ __attribute__((aligned(1024))) uint16_t ring[S * kSt];
     __shared__ __attribute__((aligned(16))) int s_info[8][4];   // items of the last rounds: g, first row, end, column tile
+    __shared__ __attribute__((aligned(256))) int s_touch[kTouch ? 256 : 1];   // never read
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.K, NN = a.NN, N = NN / 2;
@@ -1325,6 +1326,7 @@ __device__ __forceinline__ void ws_body(const FfnArgs& a) {
         const int64_t bstep = kBTr ? 64 * (int64_t)NN : 64;
         const uint16_t *pa[5], *pb[8];
         int na = 0, round = 0, t = 0, slot = 0, left = 0;   // of the item being loaded: slices left
+        [[maybe_unused]] int lo = 0, hi = 0, col0 = 0;      // its rows and first column
         uint32_t is_item = 0, has_rows = 0;                 // of round r, at bit r % 32
         bool valid = true;
         auto next_item = [&]() {
@@ -1346,6 +1348,11 @@ __device__ __forceinline__ void ws_body(const FfnArgs& a) {
             if (left == 0) return;
             const uint16_t* wg = a.b + (int64_t)wi.g * K * NN;
             const int c0 = col * kItemCols, rows = wi.hi - wi.lo;
+            if constexpr (kTouch) {
+                lo = wi.lo;
+                hi = wi.hi;
+                col0 = c0;
+            }
             na = 0;
 #pragma unroll
             for (int i = 0; i < 5; ++i) {
@@ -1368,14 +1375,37 @@ __device__ __forceinline__ void ws_body(const FfnArgs& a) {
                 }
             }
         };
-        // fills the next slot; returns the loads issued (none for results, or past the last item)
+        // Brings the lines of a bf16 residual that the item's end reads into the
+        // XCD's cache while the last slices are multiplied, four bytes of each
+        // (256 experts, 65536 rows, K = 512, N = 2048: 296 -> 287 us; two or ten
+        // slots earlier 300 and 306, the lines are gone again; fp32, twice the
+        // lines, 374 -> 381, so not there).  Returns the loads issued.
+        auto touch_residual = [&]() {
+            int n = 0;
+            if constexpr (kTouch) {
+                if (a.residual == nullptr) return n;
+                constexpr int kRowLines = kWsCols / 64;
+#pragma unroll
+                for (int i = 0; i < (kWsRows * kRowLines + 255) / 256; ++i) {
+                    const int first = 64 * (p + 4 * i), r = (first + lane) / kRowLines;
+                    if (first >= (hi - lo) * kRowLines) break;
+                    const uint16_t* q = static_cast<const uint16_t*>(a.residual) + (int64_t)min(lo + r, hi - 1) * NN +
+                                        min(col0 + 64 * (lane % kRowLines), NN - 8);
+                    __builtin_amdgcn_global_load_lds(q, (GMM_LDS void*)(s_touch + 64 * p), 4, 0, 0);
+                    ++n;
+                }
+            }
+            return n;
+        };
+        // fills the next slot; returns the loads issued (none past the last item)
         auto advance = [&]() {
             if (!valid) return 0;
             uint16_t* sa = ring + slot * kSt + 512 * p;
             slot = slot == S - 1 ? 0 : slot + 1;
             if (left == 0) {   // the item's results go here
+                const int n = has_rows >> ((round - 1) & 31) & 1u ? touch_residual() : 0;
                 next_item();
-                return 0;
+                return n;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -1401,6 +1431,9 @@ __device__ __forceinline__ void ws_body(const FfnArgs& a) {
                 case 10: wait_vmem<10>(); break;
                 case 9: wait_vmem<9>(); break;
                 case 8: wait_vmem<8>(); break;
+                case 3: wait_vmem<3>(); break;   // of the residual
+                case 2: wait_vmem<2>(); break;
+                case 1: wait_vmem<1>(); break;
                 default: wait_vmem<0>(); break;
             }
         };
