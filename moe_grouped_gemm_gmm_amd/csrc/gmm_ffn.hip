@@ -2031,9 +2031,11 @@ FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8) {
 //   256, 2048, 512 216 / 232; not: 16384, 1, 4096, 1024 145 / 123; 12000, 60,
 //   1024, 1024 41.0 / 32.9
 //   more than two rounds where a group is two items of eight column tiles or
-//   more, with a cap of 128 rows (160): 65536, 256, 512, 2048 R 288 (280) / 320, RZ
-//   290 (313) / 318, without R 250 (243) / 237; two rounds: 8192, 32, 512, 2048 R
-//   (36.0) / 39.4, RZ (48.0) / 38.4
+//   more: 65536, 256, 512, 2048 R 284 / 320, RZ 318 / 318, without R 254 / 237;
+//   two rounds: 8192, 32, 512, 2048 R 36.0 / 39.4, RZ 48.0 / 38.4.  Such items have
+//   up to 160 rows, whatever cap made the rounds fewest (here 160 against 128): the
+//   same R 284 / 287, evenly routed 272 / 286; 40000, 256, 512, 2048 R 197 / 218;
+//   30000, 128, 2048, 1024 RZ 190 / 211; 16384, 64, 2048, 2048 R 187 / 184
 //   128 / 256 columns, K up to 256: 60000, 256, 64, 2048 80 / 82, R 156 / 199;
 //   30000, 100, 256, 512 R 25.4 / 32.4; up to 512: 16000, 64, 384, 768 R 29.1 /
 //   25.5; 8192, 32, 512, 2048 R 39.4 / 44.3; 65536, 256, 512, 2048 284 / 238
@@ -2061,7 +2063,7 @@ FfnChoice linear_fwd_choice(int M, int K, int NN, int G) {
             cost = t;
         }
     }
-    if (rounds > 2 && K < 2048) cap = 128;
+    if (rounds > 2) cap = kWsRows;
     if (cap > 0) return {kFfnLoadWaves, 12, cap, 256};
     const int64_t row_tiles = max_work_items(M, busy, 128);
     const bool wide = K > 512 || (K > 256 && (tiles < 8 || row_tiles * (NN / 128) > 8 * cus));

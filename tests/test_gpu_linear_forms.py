@@ -23,7 +23,8 @@ FORMS = {
     "load_64": (3200, 32, 768, 768, 3, 12, 64, 256),
     "load_96": (4096, 32, 1024, 1024, 3, 12, 96, 256),
     "load_160": (8192, 32, 768, 1024, 3, 12, 160, 256),
-    "load_rounds_128": (16500, 64, 512, 2048, 3, 12, 128, 256),
+    "load_128": (7400, 64, 768, 1024, 3, 12, 128, 256),
+    "load_rounds_short": (16500, 64, 512, 2048, 3, 12, 160, 256),
     "load_rounds_160": (16500, 64, 2048, 1024, 3, 12, 160, 256),
     "load_odd": (2300, 16, 832, 832, 3, 12, 64, 256),
 }

@@ -32,7 +32,7 @@ def test_the_choice_of_the_shapes_measured():
     assert c(8, 256, 512, 2048) == (1, 16, 64)
     assert c(1777, 13, 1088, 704) == (1, 32, 64)
     assert c(8192, 32, 2048, 512) == (3, 96, 256)
-    assert c(65536, 256, 512, 2048) == (3, 128, 256)
+    assert c(65536, 256, 512, 2048) == (3, 160, 256)
     assert c(65536, 256, 2048, 512) == (3, 160, 256)
     assert c(8192, 32, 512, 2048) == (2, 128, 128)
     assert c(12000, 60, 1024, 1024) == (2, 128, 256)
