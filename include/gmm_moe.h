@@ -51,7 +51,7 @@ typedef enum {
 
 typedef enum {
     GMM_ACT_NONE = 0,
-    GMM_ACT_RELU = 1,
+    GMM_ACT_RELU = 1,     /* max(z, 0); a NaN stays one, in the value and in the slope */
     GMM_ACT_SILU = 2,     /* z / (1 + exp(-z)) */
     GMM_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2 */
     GMM_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */

@@ -57,7 +57,7 @@ __device__ __forceinline__ float normal_cdf(float z, float e) {
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == kActRelu) return z > 0.0f ? z : 0.0f;
+    if constexpr (ACT == kActRelu) return z <= 0.0f ? 0.0f : z;   // a NaN stays one
     else if constexpr (ACT == kActSilu) return z * logistic(z);
     else if constexpr (ACT == kActGelu) return z * normal_cdf(z, gauss(z));
     else if constexpr (ACT == kActGeluTanh) return z * logistic(kTanhScale * (z + kTanhCubic * z * z * z));
@@ -66,7 +66,7 @@ __device__ __forceinline__ float act_value(float z) {
 
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     else if constexpr (ACT == kActSilu) {
         const float s = logistic(z);
         return s + z * s * (1.0f - s);
