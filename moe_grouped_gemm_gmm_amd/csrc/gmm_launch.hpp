@@ -164,6 +164,7 @@ int64_t ffn_dw_blocks(int64_t K, int64_t NN, int64_t G);
 // written where act is none: it is dout) and db [G,N], the column sums of dpre
 // in fp32.  dpre or db may be NULL; `part` holds linear_part_words(M, N, G) fp32.
 int64_t linear_part_words(int64_t M, int64_t N, int64_t G);
+int64_t linear_db_blocks(int64_t N, int64_t G);   // workgroups of db's second launch, whatever M
 hipError_t launch_linear_grad(const void* dout, const void* pre, int act, const int32_t* group_sizes, int M, int N, int G,
                               void* dpre, void* db, bool db_bf16, float* part, int32_t* status, hipStream_t stream);
 

@@ -127,6 +127,8 @@ int64_t grad_items(int64_t M, int64_t N, int64_t G) { return max_work_items(M, G
 
 int64_t linear_part_words(int64_t M, int64_t N, int64_t G) { return M > 0 && N > 0 && G > 0 ? grad_items(M, N, G) * N : 0; }
 
+int64_t linear_db_blocks(int64_t N, int64_t G) { return N / 64 * G; }
+
 hipError_t launch_linear_grad(const void* dout, const void* pre, int act, const int32_t* group_sizes, int M, int N, int G,
                               void* dpre, void* db, bool db_bf16, float* part, int32_t* status, hipStream_t stream) {
     if (M > 0 && ((act != kActNone && dpre != nullptr) || db != nullptr)) {

@@ -222,6 +222,7 @@ int gmm_bf16_linear_bwd(const void* dout, const void* rhs, const int32_t* group_
     GMM_TRY(check_opt_ptr(dw, "dw"));
     GMM_TRY(check_opt_ptr(db, "db"));
     GMM_TRY(check_grid(gmm::linear_part_words(M, N, G) / 64));
+    if (db != nullptr) GMM_TRY(check_grid(gmm::linear_db_blocks(N, G)));
     GMM_TRY(check_grid(gmm::ffn_dx_blocks(M, K, G)));
     GMM_TRY(check_grid(gmm::ffn_dw_blocks(K, N, G)));
     GMM_TRY(check_ws(ws, ws_bytes, gmm_workspace_bytes(GMM_OP_BF16_LINEAR_BWD, M, K, N, G)));
