@@ -74,8 +74,9 @@ __device__ __forceinline__ float act_slope(float z) {
         const float e = gauss(z);
         return normal_cdf(z, e) + z * kInvSqrt2Pi * e;
     } else if constexpr (ACT == kActGeluTanh) {
-        const float s = logistic(kTanhScale * (z + kTanhCubic * z * z * z));
-        return s + z * s * (1.0f - s) * (kTanhScale * (1.0f + 3.0f * kTanhCubic * z * z));
+        // s (1 - s) is 0 long before z^2 overflows: the bound keeps 0 times infinity out
+        const float s = logistic(kTanhScale * (z + kTanhCubic * z * z * z)), z2 = fminf(z * z, 0x1p100f);
+        return s + z * s * (1.0f - s) * (kTanhScale * (1.0f + 3.0f * kTanhCubic * z2));
     } else return 1.0f;
 }
 

@@ -83,3 +83,19 @@ def test_slope_of_nan_is_nan(act):
     nan[1, 5] = True
     assert torch.equal(db.isnan(), nan)
     assert dx[1].isnan().all() and not dx[0].isnan().any() and not dx[2].isnan().any()
+
+
+FAR = [2.0 ** 40, 1.5 * 2.0 ** 63, 2.0 ** 64, 2.0 ** 65, 1e25, 3e38]     # squares and cubes past the largest number
+
+
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "none"])
+def test_far_values(act):
+    """Far from 0 every activation is max(z, 0) and its slope the step, to the last bit."""
+    N = 64
+    z = torch.zeros((1, N), dtype=BF)
+    z[0, :2 * len(FAR)] = torch.tensor(FAR + [-v for v in FAR]).to(BF)
+    out = gmm.gmm_bf16_linear(z.to(DEV), eye(N), torch.ones(1, dtype=I32, device=DEV), activation=act, out_dtype=F32).cpu()
+    assert torch.equal(out, z.float().clamp(min=0))
+    _, db = slopes(z.to(DEV), act)
+    n = 2 * len(FAR)
+    assert torch.equal(db.cpu()[:, :n], (z > 0).float()[:, :n])
