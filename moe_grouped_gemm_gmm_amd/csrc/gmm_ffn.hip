@@ -2027,18 +2027,32 @@ FfnChoice gated_fwd_choice(int M, int K, int NN, int G, bool keep_mx8) {
 //   28.1; 6000, 20, 2048, 1280 39.4 / 48.4; 5000, 12, 2048, 1024 35.7 / 42.5;
 //   shorter: 3000, 8, 512, 2048 16.4 / 15.3
 //   more rounds where rows of x lie a multiple of 4 KB apart and a group is at
-//   most three items: 24000, 64, 2048, 1024 R 135 / 154 (Z 138 / 159); 65536,
-//   256, 2048, 512 216 / 232; not: 16384, 1, 4096, 1024 145 / 123; 12000, 60,
-//   1024, 1024 41.0 / 32.9
+//   most three items, whatever the call adds (fp32 results gain as much): 24000,
+//   64, 2048, 1024 121 / 139 (Z 126 / 140), R 128 / 156 (Z 134 / 156); 65536, 256,
+//   2048, 512 188 / 217 (Z 211 / 215); 16384, 64, 2048, 2048 R 185 / 220 (Z 210 /
+//   226); 30000, 128, 2048, 1024 166 / 188 (Z 188 / 184); not: 16384, 1, 4096, 1024
+//   145 / 123; 12000, 60, 1024, 1024 41.0 / 32.9
 //   more than two rounds where a group is two items of eight column tiles or
-//   more: 65536, 256, 512, 2048 R 284 / 320, RZ 318 / 318, without R 254 / 237;
-//   two rounds: 8192, 32, 512, 2048 R 36.0 / 39.4, RZ 48.0 / 38.4.  Such items have
-//   up to 160 rows, whatever cap made the rounds fewest (here 160 against 128): the
-//   same R 284 / 287, evenly routed 272 / 286; 40000, 256, 512, 2048 R 197 / 218;
-//   30000, 128, 2048, 1024 RZ 190 / 211; 16384, 64, 2048, 2048 R 187 / 184
+//   more: with a bf16 residual, whose lines the load waves bring near, 65536, 256,
+//   512, 2048 R 266 / 316 (Z 275 / 306); N = 2560 R 351 / 405 (Z 355 / 397); N =
+//   4096 R 512 / 614 (Z 545 / 632); K = 768 R 337 / 386 (Z 359 / 381); 40000, 256,
+//   512, 2048 R 195 / 227 (Z 200 / 220); 16500, 64, 512, 2048 R 74 / 90 (Z 80 / 92)
+//   without one about the same, a tenth less to a twentieth more, in fp32 under skew up
+//   to a fifth more (40000, 256, 512, 4096 Z 421 / 377; 10000, 64, 512, 2048 RZ 88 / 72):
+//   the first 243 / 235 (Z 244 / 232), with pre kept 282 / 275 (Z 280 / 273); N = 4096 460 /
+//   455 (Z 480 / 461); K = 768 313 / 311 (Z 324 / 310); 40000 rows 166 / 176 (Z 176 /
+//   170); 16500, 64, 512, 2048 65 / 68 (Z 69 / 71), pre 73 / 81 (Z 82 / 84); 32768,
+//   128, 512, 2048 118 / 121 (Z 120 / 124), pre 138 / 143 (Z 140 / 145); 30000, 192,
+//   768, 2048 173 / 178 (Z 176 / 176); 10000, 40, 512, 2048 40.1 / 37.7 (Z 39.6 /
+//   38.6); results and residual in fp32 358 / 361 (Z 390 / 360), 32768 rows 179 / 186
+//   (Z 199 / 184).  Seven column tiles would gain with a residual too: 65536, 256,
+//   512, 1792 R 239 / 280 (Z 237 / 266), 212 / 212 without.  Two rounds: 8192, 32,
+//   512, 2048 R 30.3 / 35.1, Z 43.1 / 36.2.  Such items have up to 160 rows,
+//   whatever cap made the rounds fewest (here 160 against 128: R 266 / 280, Z 275 /
+//   280; 40000 rows R 195 / 214, Z 200 / 206)
 //   128 / 256 columns, K up to 256: 60000, 256, 64, 2048 80 / 82, R 156 / 199;
 //   30000, 100, 256, 512 R 25.4 / 32.4; up to 512: 16000, 64, 384, 768 R 29.1 /
-//   25.5; 8192, 32, 512, 2048 R 39.4 / 44.3; 65536, 256, 512, 2048 284 / 238
+//   25.5; 8192, 32, 512, 2048 R 35.1 / 41.1; 65536, 256, 512, 2048 277 / 235
 FfnChoice linear_fwd_choice(int M, int K, int NN, int G) {
     const int busy = G < M ? G : M, rows = (M + busy - 1) / busy;
     const int64_t cus = device_cus(), tiles = (NN + 255) / 256;

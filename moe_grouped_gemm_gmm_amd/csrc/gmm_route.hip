@@ -12,7 +12,11 @@
 // last bits of 32 would change places with every change of the arithmetic.
 // Such keys are first compared in 32 bits; only where two that follow each
 // other among the k + 1 largest are closer than twice their error is the
-// wave's choice made again in 64.  The weights and their gradient are in 32 bits.
+// wave's choice made again in 64.  How many tokens that takes depends on the data
+// (65536 tokens of 256 experts, fp32, k = 8, us: normal logits of deviation 1.2 and
+// biases of 0.05 35, logits of deviation 15 with biases of 0 138, where most of the
+// softmax's scores are closer to each other than the largest one's error; with a
+// sigmoid, whose scores crowd at 1 then, 150).  The weights and their gradient are in 32 bits.
 //
 // What bounds it: the forward's instructions (65536 tokens of 256 experts, k =
 // 8: 20 us for 71 MB, which a copy's 5 TB/s moves in 14; one wave a token took

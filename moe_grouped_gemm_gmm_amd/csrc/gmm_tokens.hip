@@ -8,10 +8,12 @@
 // the last from ballots on the expert's bits, so nothing depends on the order
 // in which workgroups or atomics run (the LDS atomics only count).
 //
-// Moving rows is bound by memory: a workgroup takes one token, reads its row
-// once and touches the token's k rows, whole rows at a time, so that every
-// byte of the sorted buffer crosses the chip once and the token's row is read
-// once instead of k times.  Stores, and the loads of the sorted buffer, are
+// Moving rows is bound by memory: a workgroup takes one token and touches the
+// token's k rows, whole rows at a time, so that every byte of the sorted buffer
+// crosses the chip once.  The token's own row is read once instead of k times; the
+// gradient of combine takes the choices that have a row in pieces of 8, 4, 2 and 1
+// and reads it again, from the cache, for each (twice with 6 choices, four times
+// with 15).  Stores, and the loads of the sorted buffer, are
 // nontemporal: with 8192 tokens of 8 rows of 4 KB a buffer fills the last-level
 // cache and pushes out what the next kernel reads (there and back 155 -> 118 us,
 // its gradient 178 -> 159; dispatch and the product that reads the rows 162 -> 144
